@@ -59,6 +59,13 @@ class MbBufs(ctypes.Structure):
                 + [(n, ctypes.c_void_p) for n in _MB_FIELDS_TAIL])
 
 
+_FP8_FIELDS = ["w1q", "w1s", "w2q", "w2s", "xq", "xs", "hq", "hs", "dq", "ds", "daq", "das"]
+
+
+class Fp8Bufs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in _FP8_FIELDS]
+
+
 class PhaseTime(ctypes.Structure):
     _fields_ = [("mb", ctypes.c_int32), ("phase", ctypes.c_int32), ("stream", ctypes.c_int32),
                 ("start_ms", ctypes.c_float), ("end_ms", ctypes.c_float)]
@@ -105,6 +112,16 @@ _SIGS = {
     "moe_layer_steps_host": ([_DP, ctypes.POINTER(MbBufs), _I32, ctypes.POINTER(_VP),
                               ctypes.POINTER(_VP), ctypes.POINTER(_VP), ctypes.POINTER(_VP), _VP],
                              _I32),
+    "moe_fp8_scale_bytes": ([ctypes.c_int64, _I32], _SZ),
+    "moe_fp8_quantize_weights": ([_DP] + [_VP] * 7, _I32),
+    "moe_permute_fp8": ([_DP] + [_VP] * 5, _I32),
+    "moe_expert_ffn_fwd_fp8": ([_DP] + [_VP] * 13 + [_SZ, _VP], _I32),
+    "moe_combine_bwd_fp8": ([_DP] + [_VP] * 9, _I32),
+    "moe_expert_ffn_bwd_dgrad_fp8": ([_DP] + [_VP] * 13 + [_SZ, _VP], _I32),
+    "moe_layer_forward_fp8": ([_DP, ctypes.POINTER(MbBufs), ctypes.POINTER(Fp8Bufs), _I32, _VP],
+                              _I32),
+    "moe_layer_backward_fp8": ([_DP, ctypes.POINTER(MbBufs), ctypes.POINTER(Fp8Bufs), _I32, _VP],
+                               _I32),
     "moe_graph_capture": ([_DP, ctypes.POINTER(MbBufs), _I32, _VP, ctypes.POINTER(_VP)], _I32),
     "moe_graph_launch": ([_VP, _VP], _I32),
     "moe_graph_kernel_count": ([_VP], _I32),
@@ -320,7 +337,167 @@ def moe_layer_steps_host(desc, bufs0: "LayerBuffers", bufs1: "LayerBuffers", hos
            "moe_layer_steps_host")
 
 
+# ----------------------------------------------------------------------------- 8-bit experts
+_E4M3, _U8, _BF16, _I32T, _F32 = (torch.float8_e4m3fn, torch.uint8, torch.bfloat16, torch.int32,
+                                  torch.float32)
+
+
+def _fp8_args(what: str, *args):
+    """Checks (name, tensor, dtype, least number of elements) of a call: contiguous
+    tensors of that type on the current device, or None where the size is negative
+    (optional). Returns their addresses."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    out = []
+    for name, t, dt, n in args:
+        if t is None:
+            if n >= 0:
+                raise MoeError(MOE_ERR_INVALID_ARG, what, f"{name} is None")
+            out.append(None)
+            continue
+        if t.dtype is not dt:
+            raise MoeError(MOE_ERR_INVALID_ARG, what, f"{name} is {t.dtype}, not {dt}")
+        if not t.is_cuda or t.get_device() != dev:
+            raise MoeError(MOE_ERR_INVALID_ARG, what,
+                           f"{name} is on {t.device}, not on the current CUDA device")
+        if not t.is_contiguous():
+            raise MoeError(MOE_ERR_INVALID_ARG, what, f"{name} is not contiguous")
+        if t.numel() < abs(n):
+            raise MoeError(MOE_ERR_INVALID_ARG, what,
+                           f"{name} has {t.numel()} elements, fewer than {abs(n)}")
+        out.append(t.data_ptr())
+    return out
+
+
+def _blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+def moe_fp8_scale_bytes(rows: int, blocks: int) -> int:
+    """Bytes of the scale buffer of `rows` rows of `blocks` blocks (include/moe.h)."""
+    return int(lib().moe_fp8_scale_bytes(int(rows), int(blocks)))
+
+
+def _words(rows: int, blocks: int) -> int:
+    return -(-blocks // 4) * 4 * rows
+
+
+def moe_fp8_quantize_weights(desc, w1, w2, w1q, w1s, w2q, w2s, stream=None):
+    """Expert weights into e4m3 and one scale for each 128 x 128 block."""
+    n, nb = desc.E * desc.F * desc.H, desc.E * _blocks(desc.F) * _blocks(desc.H)
+    what = "moe_fp8_quantize_weights"
+    p = _fp8_args(what, ("w1", w1, _BF16, 2 * n), ("w2", w2, _BF16, n), ("w1q", w1q, _E4M3, 2 * n),
+                  ("w1s", w1s, _U8, 2 * nb), ("w2q", w2q, _E4M3, n), ("w2s", w2s, _U8, nb))
+    _check(lib().moe_fp8_quantize_weights(_d(desc), *p, _s(stream)), what)
+
+
+def moe_permute_fp8(desc, x, slot, xq, xs, stream=None):
+    """Permute that quantises: e4m3 rows with one scale for each 128 columns."""
+    T, H, N = desc.T, desc.H, desc.T * desc.k
+    p = _fp8_args("moe_permute_fp8", ("x", x, _BF16, T * H), ("slot", slot, _I32T, N),
+                  ("xq", xq, _E4M3, N * H), ("xs", xs, _U8, _words(N, _blocks(H))))
+    _check(lib().moe_permute_fp8(_d(desc), *p, _s(stream)), "moe_permute_fp8")
+
+
+def _fp8_weight_args(desc, w1q, w1s, w2q, w2s):
+    n, nb = desc.E * desc.F * desc.H, desc.E * _blocks(desc.F) * _blocks(desc.H)
+    return (("w1q", w1q, _E4M3, 2 * n), ("w1s", w1s, _U8, 2 * nb), ("w2q", w2q, _E4M3, n),
+            ("w2s", w2s, _U8, nb))
+
+
+def moe_expert_ffn_fwd_fp8(desc, xq, xs, off, w1q, w1s, w2q, w2s, a, h, hq, hs, o, ws,
+                           stream=None):
+    """Expert FFN forward on 8-bit operands; a and h may be None (serving)."""
+    H, F, N = desc.H, desc.F, desc.T * desc.k
+    what = "moe_expert_ffn_fwd_fp8"
+    p = _fp8_args(what, ("xq", xq, _E4M3, N * H), ("xs", xs, _U8, _words(N, _blocks(H))),
+                  ("off", off, _I32T, desc.E + 1), *_fp8_weight_args(desc, w1q, w1s, w2q, w2s),
+                  ("a", a, _BF16, -2 * N * F), ("h", h, _BF16, -N * F), ("hq", hq, _E4M3, N * F),
+                  ("hs", hs, _U8, _words(N, _blocks(F))), ("o", o, _BF16, N * H),
+                  ("ws", ws, _U8, 1))
+    _check(lib().moe_expert_ffn_fwd_fp8(_d(desc), *p, ws.numel(), _s(stream)), what)
+
+
+def moe_combine_bwd_fp8(desc, dy, o, slot, gates, d_o, dq, ds, dgates, stream=None):
+    """Combine backward into 8-bit rows; d_o (the same rows in bf16) may be None."""
+    T, H, N = desc.T, desc.H, desc.T * desc.k
+    p = _fp8_args("moe_combine_bwd_fp8", ("dy", dy, _BF16, T * H), ("o", o, _BF16, N * H),
+                  ("slot", slot, _I32T, N), ("gates", gates, _F32, N), ("d_o", d_o, _BF16, -N * H),
+                  ("dq", dq, _E4M3, N * H), ("ds", ds, _U8, _words(N, _blocks(H))),
+                  ("dgates", dgates, _F32, N))
+    _check(lib().moe_combine_bwd_fp8(_d(desc), *p, _s(stream)), "moe_combine_bwd_fp8")
+
+
+def moe_expert_ffn_bwd_dgrad_fp8(desc, dq, ds, a, off, w1q, w1s, w2q, w2s, da, daq, das, dx_perm,
+                                 ws, stream=None):
+    """Expert FFN activation gradient on 8-bit operands; da (bf16) may be None."""
+    H, F, N = desc.H, desc.F, desc.T * desc.k
+    what = "moe_expert_ffn_bwd_dgrad_fp8"
+    p = _fp8_args(what, ("dq", dq, _E4M3, N * H), ("ds", ds, _U8, _words(N, _blocks(H))),
+                  ("a", a, _BF16, 2 * N * F), ("off", off, _I32T, desc.E + 1),
+                  *_fp8_weight_args(desc, w1q, w1s, w2q, w2s), ("da", da, _BF16, -2 * N * F),
+                  ("daq", daq, _E4M3, 2 * N * F), ("das", das, _U8, _words(N, 2 * _blocks(F))),
+                  ("dx_perm", dx_perm, _BF16, N * H), ("ws", ws, _U8, 1))
+    _check(lib().moe_expert_ffn_bwd_dgrad_fp8(_d(desc), *p, ws.numel(), _s(stream)), what)
+
+
+def moe_layer_forward_fp8(desc, bufs: "LayerBuffers", fp8: "Fp8Buffers", save: bool = True,
+                          stream=None):
+    """Layer forward with 8-bit experts; save=True keeps what the backward reads."""
+    _check(lib().moe_layer_forward_fp8(_d(desc), ctypes.byref(bufs.struct()),
+                                       ctypes.byref(fp8.struct()), int(bool(save)), _s(stream)),
+           "moe_layer_forward_fp8")
+
+
+def moe_layer_backward_fp8(desc, bufs: "LayerBuffers", fp8: "Fp8Buffers", run_wgrad: bool = True,
+                           stream=None):
+    """Layer backward with 8-bit experts, after a forward that saved."""
+    _check(lib().moe_layer_backward_fp8(_d(desc), ctypes.byref(bufs.struct()),
+                                        ctypes.byref(fp8.struct()), int(bool(run_wgrad)),
+                                        _s(stream)), "moe_layer_backward_fp8")
+
+
 # ----------------------------------------------------------------------------- buffers
+class Fp8Buffers:
+    """The 8-bit buffers of one micro-batch beside its LayerBuffers. weights: another
+    Fp8Buffers whose quantised weights are shared; backward=False leaves the
+    gradient's buffers out (serving)."""
+
+    def __init__(self, desc: LayerDesc, device="cuda", weights: Optional["Fp8Buffers"] = None,
+                 backward: bool = True):
+        H, E, F, N = desc.H, desc.E, desc.F, max(desc.T * desc.k, 1)
+        nh, nf = _blocks(H), _blocks(F)
+        z = lambda *s, dt: torch.zeros(*s, dtype=torch.uint8, device=device).view(dt)  # noqa: E731
+        rows = lambda c: z(N, c, dt=_E4M3)  # noqa: E731
+        scales = lambda nb: z(-(-nb // 4), N, 4, dt=_U8)  # noqa: E731
+        self.desc = desc
+        if weights is None:
+            self.w1q, self.w2q = z(E, 2 * F, H, dt=_E4M3), z(E, H, F, dt=_E4M3)
+            self.w1s, self.w2s = z(E, 2, nf, nh, dt=_U8), z(E, nh, nf, dt=_U8)
+        else:
+            self.w1q, self.w1s, self.w2q, self.w2s = (weights.w1q, weights.w1s, weights.w2q,
+                                                      weights.w2s)
+        self.xq, self.xs, self.hq, self.hs = rows(H), scales(nh), rows(F), scales(nf)
+        self.dq = self.ds = self.daq = self.das = None
+        if backward:
+            self.dq, self.ds = rows(H), scales(nh)
+            self.daq, self.das = rows(2 * F), scales(2 * nf)
+        self._struct = None
+
+    def quantize_weights(self, w1, w2, stream=None):
+        """Fills w1q, w1s, w2q, w2s from the bf16 expert weights."""
+        moe_fp8_quantize_weights(self.desc, w1, w2, self.w1q, self.w1s, self.w2q, self.w2s,
+                                 stream)
+
+    def struct(self) -> Fp8Bufs:
+        if self._struct is None:
+            s = Fp8Bufs()
+            for n in _FP8_FIELDS:
+                t = getattr(self, n)
+                setattr(s, n, None if t is None else t.data_ptr())
+            self._struct = s
+        return self._struct
+
+
 class LayerBuffers:
     """Every device buffer of one micro-batch (torch tensors used as plain memory)."""
 

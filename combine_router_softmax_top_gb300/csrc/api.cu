@@ -4,8 +4,6 @@
 #include <stdio.h>
 #include <string.h>
 
-#include <mutex>
-
 #include "moe_internal.cuh"
 #include "moe_layer_ops.h"
 
@@ -34,24 +32,6 @@ moe_status_t check_launch(const char* what) {
   }
   return MOE_OK;
 }
-
-// Per-device helper streams and events (the host-buffer step's copy stream,
-// the backward's side stream), created on first use with that device current
-// and kept until exit.
-struct CopyLane {
-  cudaStream_t stream = nullptr;
-  cudaEvent_t start = nullptr, dy_in = nullptr, fwd_done = nullptr, y_out = nullptr;
-  cudaEvent_t dx_ready = nullptr;
-  // moe_layer_steps_host: a second copy stream (device to host) and, per
-  // input slot, the events of its pipeline
-  cudaStream_t d2h = nullptr;
-  cudaEvent_t in_ready[2] = {}, step_done[2] = {}, out_done[2] = {};
-  // moe_layer_backward's side stream: the weight gradients run on it beside
-  // the dispatch backward (they depend on the dgrad only, not on each other)
-  cudaStream_t side = nullptr;
-  cudaEvent_t fork = nullptr, join = nullptr;
-  std::mutex side_mu;  // one fork/join enqueued at a time
-};
 
 CopyLane* copy_lane() {
   constexpr int kMaxDevices = 64;

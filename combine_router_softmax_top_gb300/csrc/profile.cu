@@ -6,18 +6,20 @@
 #include <mutex>
 #include <vector>
 
-#include "moe_internal.cuh"
+#include "fp8.cuh"
 
 namespace moe {
 
 namespace {
 
-const char* const kNames[K_NUM] = {
+const char* const kNames[K_ALL] = {
     "route_logits", "route_topk", "layout_count", "layout_assign", "permute",
     "combine", "combine_bwd", "permute_bwd", "route_bwd_dx", "route_bwd_dwr", "gemm_fc1_fwd", "gemm_fc2_fwd", "gemm_fc2_dgrad",
     "gemm_fc1_dgrad", "gemm_wgrad_w1", "gemm_wgrad_w2", "dispatch_bwd", "gemm_ffn_fwd",
     "gemm_ffn_dgrad", "dispatch_fused", "gemm_wgrad_w1_accum", "gemm_wgrad_w2_accum",
-    "layout_scan", "ep_resort", "gemm_wgrad"};
+    "layout_scan", "ep_resort", "gemm_wgrad", "fp8_quantize_weights", "fp8_permute",
+    "fp8_combine_bwd", "fp8_gemm_fc1_fwd", "fp8_gemm_fc2_fwd", "fp8_gemm_fc2_dgrad",
+    "fp8_gemm_fc1_dgrad"};
 
 std::atomic<unsigned long long> g_launches{0};
 
@@ -69,7 +71,7 @@ extern "C" {
 uint64_t moe_kernel_launches(void) { return g_launches.load(); }
 
 const char* moe_kernel_name(int32_t kernel) {
-  return (kernel >= 0 && kernel < K_NUM) ? kNames[kernel] : "";
+  return (kernel >= 0 && kernel < K_ALL) ? kNames[kernel] : "";
 }
 
 moe_status_t moe_profile_start(int32_t capacity) {

@@ -51,6 +51,8 @@ extern "C" {
 #endif
 
 typedef uint16_t moe_bf16; /* bfloat16 bit pattern */
+typedef uint8_t moe_e4m3;  /* 8-bit float: 4 exponent bits, 3 mantissa bits, no infinity */
+typedef uint8_t moe_e8m0;  /* power-of-two block scale: byte b stands for 2^(b - 127), 255 for NaN */
 
 typedef enum {
   MOE_OK = 0,
@@ -416,6 +418,120 @@ moe_status_t moe_layer_steps_host(const moe_layer_desc_t* d, const moe_mb_bufs_t
                                   int32_t n, const moe_bf16* const* host_x,
                                   const moe_bf16* const* host_dy, moe_bf16* const* host_y,
                                   moe_bf16* const* host_dx, void* stream);
+
+/* ------------------------------------------------------------------ 8-bit experts */
+
+/* The experts' products on 8-bit floating-point operands, with one scale for
+ * each block of 128 values: the expert weights, the largest thing the layer
+ * reads, halve, and the rows of the send layout halve with them. The pages
+ * describe no such path; the arithmetic is stated here.
+ *
+ * A value v of a block with scale byte b is held as q = e4m3(v / 2^(b-127)),
+ * rounded to nearest even, where b is the smallest byte with
+ * max|v| <= 448 * 2^(b-127) (448 is the largest e4m3 value, so nothing is
+ * clamped). A block of zeros has b = 0. A block that holds a NaN or an infinity
+ * has b = 255 and every q NaN: it comes out of the products as NaN, in its own
+ * rows (activations) or in its expert's outputs (weights).
+ *
+ * Blocks and their layouts:
+ *   - Activation rows, C columns: 128 consecutive columns of a row, the last
+ *     block of a row may have 64. The scale bytes of an [N, C] buffer are
+ *     [ceil(nb / 4), N, 4] with nb = ceil(C / 128): block b of row s at
+ *     ((b / 4) * N + s) * 4 + b % 4 (one word holds four blocks of a row, as the
+ *     tensor cores read them). moe_fp8_scale_bytes() gives the size. The bytes
+ *     that fill up the last word are written as 0 by the permute and the combine
+ *     backward and are unspecified in hs and das.
+ *   - Rows of 2F columns (daq) are cut into blocks in their gate half and in
+ *     their up half apart: gate blocks 0..nf-1, up blocks nf..2nf-1, nf =
+ *     ceil(F / 128).
+ *   - Weights: blocks of 128 rows x 128 columns. w1 is cut in its gate rows and
+ *     its up rows apart: w1s [E, 2, nf, nh], w2s [E, nh, nf], nh = ceil(H / 128).
+ *     The same quantised weights serve the forward and the gradient.
+ * Products are accumulated in fp32; the scales are applied exactly. Buffer
+ * arguments of type moe_e4m3 and moe_e8m0 are device pointers, 16-byte aligned
+ * like every other. */
+
+/* Bytes of the scale buffer of `rows` rows of `blocks` blocks (0 if negative). */
+size_t moe_fp8_scale_bytes(int64_t rows, int32_t blocks);
+
+/* Expert weights into e4m3 and block scales, once per change of the weights:
+ * w1 [E,2F,H], w2 [E,H,F] bf16 -> w1q [E,2F,H], w1s [E,2,nf,nh], w2q [E,H,F],
+ * w2s [E,nh,nf]. */
+moe_status_t moe_fp8_quantize_weights(const moe_layer_desc_t* d, const moe_bf16* w1,
+                                      const moe_bf16* w2, moe_e4m3* w1q, moe_e8m0* w1s,
+                                      moe_e4m3* w2q, moe_e8m0* w2s, void* stream);
+
+/* Permute into the 8-bit send buffer: row slot[t,j] of (xq, xs) = quantised
+ * x[t,:], for every j. Slots outside 0..N-1 are skipped, rows that no slot names
+ * are left as they were. x [T,H] bf16, slot [T,k] int32 (of the dispatch
+ * layout) -> xq [N,H], xs. */
+moe_status_t moe_permute_fp8(const moe_layer_desc_t* d, const moe_bf16* x, const int32_t* slot,
+                             moe_e4m3* xq, moe_e8m0* xs, void* stream);
+
+/* Expert FFN forward on 8-bit operands, per expert e on its rows:
+ *   a  = bf16(xq_e @ w1q[e]^T with scales)             [rows, 2F]
+ *   h  = bf16(silu(a[:, :F]) * a[:, F:])               [rows, F] (from the bf16 a)
+ *   hq, hs = quantised h
+ *   o  = bf16(hq_e @ w2q[e]^T with scales)             [rows, H]
+ * a and h may be NULL (serving): they are then not written, the results are the
+ * same. With a backward to follow, a is needed by moe_expert_ffn_bwd_dgrad_fp8
+ * and h by moe_expert_ffn_bwd_wgrad. off [E+1] int32 on the device; values
+ * outside 0..N are taken as the nearest bound; rows at or past off[E] are left
+ * as they were. hq [N,F] and hs are scratch that holds quantised h afterwards. */
+moe_status_t moe_expert_ffn_fwd_fp8(const moe_layer_desc_t* d, const moe_e4m3* xq,
+                                    const moe_e8m0* xs, const int32_t* off, const moe_e4m3* w1q,
+                                    const moe_e8m0* w1s, const moe_e4m3* w2q, const moe_e8m0* w2s,
+                                    moe_bf16* a, moe_bf16* h, moe_e4m3* hq, moe_e8m0* hs,
+                                    moe_bf16* o, void* ws, size_t ws_bytes, void* stream);
+
+/* Combine backward into 8-bit rows: row slot[t,j] of (dq, ds) = quantised
+ * bf16(gates[t,j] * dy[t,:]), also stored as bf16 in d_o unless d_o is NULL (the
+ * weight gradients need it), and dgates[t,j] = sum_h dy[t,h] * o[slot[t,j],h] in
+ * fp32. Slots outside 0..N-1 are skipped (their dgates are 0). */
+moe_status_t moe_combine_bwd_fp8(const moe_layer_desc_t* d, const moe_bf16* dy, const moe_bf16* o,
+                                 const int32_t* slot, const float* gates, moe_bf16* d_o,
+                                 moe_e4m3* dq, moe_e8m0* ds, float* dgates, void* stream);
+
+/* Expert FFN activation gradient on 8-bit operands, per expert e on its rows:
+ *   dh      = dq_e @ w2q[e] with scales              (fp32, not stored)
+ *   da_up   = bf16(dh * silu(a_g))
+ *   da_gate = bf16(dh * a_u * s(a_g) * (1 + a_g * (1 - s(a_g))))   s = sigmoid
+ *   daq, das = quantised da
+ *   dx_perm = bf16(daq_e @ w1q[e] with scales)
+ * da [N,2F] may be NULL when no weight gradient follows. daq [N,2F] and das are
+ * scratch. Offsets and rows past off[E] as in moe_expert_ffn_fwd_fp8. The
+ * weight gradients themselves are moe_expert_ffn_bwd_wgrad on the bf16 x_perm,
+ * h, d_o and da: they are bound by writing dW, which no operand type shrinks. */
+moe_status_t moe_expert_ffn_bwd_dgrad_fp8(const moe_layer_desc_t* d, const moe_e4m3* dq,
+                                          const moe_e8m0* ds, const moe_bf16* a,
+                                          const int32_t* off, const moe_e4m3* w1q,
+                                          const moe_e8m0* w1s, const moe_e4m3* w2q,
+                                          const moe_e8m0* w2s, moe_bf16* da, moe_e4m3* daq,
+                                          moe_e8m0* das, moe_bf16* dx_perm, void* ws,
+                                          size_t ws_bytes, void* stream);
+
+/* The 8-bit buffers of one micro-batch beside its moe_mb_bufs_t (device
+ * pointers, caller-owned; the weights may be shared). */
+typedef struct moe_fp8_bufs {
+  const moe_e4m3* w1q; const moe_e8m0* w1s; const moe_e4m3* w2q; const moe_e8m0* w2s;
+  moe_e4m3* xq; moe_e8m0* xs; moe_e4m3* hq; moe_e8m0* hs;     /* forward  */
+  moe_e4m3* dq; moe_e8m0* ds; moe_e4m3* daq; moe_e8m0* das;   /* backward */
+} moe_fp8_bufs_t;
+
+/* Layer forward with 8-bit experts: route, dispatch layout, 8-bit permute,
+ * expert FFN, combine. save != 0 also stores what the backward reads (b->x_perm,
+ * b->a, b->h); with save = 0 (serving) those three may be NULL. b->w1, b->w2 and
+ * the gradient buffers are not used. */
+moe_status_t moe_layer_forward_fp8(const moe_layer_desc_t* d, const moe_mb_bufs_t* b,
+                                   const moe_fp8_bufs_t* q, int32_t save, void* stream);
+
+/* Layer backward with 8-bit experts, after a forward with save != 0: combine
+ * backward, activation gradient, dispatch and router backward, and, when
+ * run_wgrad != 0, the bf16 weight gradients on the side stream as in
+ * moe_layer_backward (flags apply as there). With run_wgrad = 0 b->d_o and b->da
+ * may be NULL. Gradients pass through the roundings to 8 bits unchanged. */
+moe_status_t moe_layer_backward_fp8(const moe_layer_desc_t* d, const moe_mb_bufs_t* b,
+                                    const moe_fp8_bufs_t* q, int32_t run_wgrad, void* stream);
 
 /* ------------------------------------------------------------------ CUDA graphs */
 
