@@ -21,8 +21,8 @@ namespace moe {
 constexpr int kFp8Block = 128;  // values (or rows and columns) that share a scale
 
 enum Fp8KernelId {  // kernel ids past those of the bf16 layer
-  K_FP8_QUANT_W = K_NUM, K_FP8_PERMUTE, K_FP8_COMBINE_BWD, K_FP8_FC1_FWD, K_FP8_FC2_FWD,
-  K_FP8_FC2_DGRAD, K_FP8_FC1_DGRAD, K_ALL
+  K_FP8_QUANT_W = K_NUM, K_FP8_PERMUTE, K_FP8_COMBINE_BWD, K_FP8_FFN_FWD, K_FP8_FFN_DGRAD,
+  K_ALL
 };
 
 // ---------------------------------------------------------------- block scales

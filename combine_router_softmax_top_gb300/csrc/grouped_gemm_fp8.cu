@@ -9,15 +9,28 @@
 // one scale per 32 K values: the four K = 32 steps of a block use the same
 // bytes), so the fp32 accumulator needs no pass over it between blocks.
 //
-// One persistent kernel per GEMM, one CTA per SM, warp-specialised:
-//   warp 0      TMA producer of the operand ring (A 128 x 128 B | B 256 x 128 B a stage)
-//   warp 1      TMEM allocator + single-thread MMA issuer
-//   warp 2      scales: packs the scale bytes of four K blocks (the four bytes
-//               of a TMEM cell) into shared memory, ahead of the MMA issuer,
-//               which copies them into TMEM (tcgen05.cp)
+// One persistent launch per chain, a CTA pair (tcgen05 cta_group::2, M = 256,
+// N = 256) per two SMs, warp-specialised:
+//   warp 0      TMA producer of the operand ring: this CTA's 128 rows of A and its
+//               half of B, 128 bytes of K, 32 KB a stage, 6 stages
+//   warp 1      TMEM allocator + (even CTA) single-thread MMA issuer for the pair
+//   warps 12..15 scales: each writes the scale bytes of four K blocks (the four
+//               bytes of a TMEM cell) into its 32 TMEM lanes (tcgen05.st), ahead of
+//               the MMA issuer. Copying them from shared memory (tcgen05.cp) in the
+//               MMA issuer's order instead drains the tensor pipe: 647 clocks a
+//               stage of four MMAs against 512 without.
 //   warps 4..11 epilogue: TMEM -> registers -> SwiGLU (or its gradient),
 //               rounding, block maxima, e4m3 -> global; two warps per TMEM lane
 //               quarter, each owning 64 of every 128 columns
+// The first GEMM's tiles come first; a tile of the second starts once every
+// tile of its expert in the first has been stored (per-expert counters). All
+// CTAs are resident and meet their first tiles before any second, so the waits
+// end.
+//
+// TMEM: two 256-column accumulators and two buffers of 12 scale columns do not
+// fit 512 columns, so the accumulators share 32: columns 0..255 and 224..479.
+// The epilogue reads the shared columns first and releases them (ovl), so the
+// next tile's MMAs start while it works on the rest.
 //
 // Ragged groups as in the bf16 GEMMs: expert e owns rows off[e]..off[e+1]-1; a
 // tile's rows past the expert's end are computed on whatever TMA loaded and
@@ -42,20 +55,23 @@ enum Fp8Mode {
   FC1_DGRAD = 3  // dx_perm = daq @ W1q
 };
 
-constexpr int BM = 128, BN = 256, BK = 128;
-constexpr int kABytes = BM * BK, kBBytes = BN * BK;
+constexpr int BM = 128, BN = 256, BK = 128;   // BM: rows of one CTA of the pair
+constexpr int kABytes = BM * BK, kBBytes = BN / 2 * BK;
 constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kStages = 4;
-constexpr int kScaleSlots = 4;                // four-K-block groups of scales in flight
-constexpr int kScaleBytes = 512 + 2 * 512;    // A rows, then both 128-column halves of B
+constexpr int kStages = 6;
+constexpr int kABoxRows = 16;                 // tiles of 64 rows or fewer load boxes of 16
 constexpr size_t kEpiStageBytes = 8 * 2048;
 constexpr int kTmemCols = 512;
-constexpr int kTmemScales = 480;              // two buffers of 12 columns
-constexpr int kThreads = 384;
+constexpr int kAccStep = 224;                 // second accumulator's first column
+constexpr int kTmemScales = 480;              // two buffers: 4 columns for A, 8 for B
+constexpr int kThreads = 512;
+// registers a thread: 128 at launch; the epilogue's two warpgroups take what the
+// control and scale warpgroups give up (2 * 56 + 2 * 192 <= 4 * 128)
+constexpr int kRegsControl = 56, kRegsEpilogue = 192;
 constexpr int kMaxE = 256;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr size_t kDynSmem =
-    (size_t)kStages * kStageBytes + kScaleSlots * kScaleBytes + kEpiStageBytes + 1024;
+    (size_t)kStages * kStageBytes + kEpiStageBytes + 1024;
 
 struct KParams {
   int E, H, F;
@@ -69,11 +85,13 @@ struct KParams {
   uint8_t* s;         // hs | das
   const bf16* aux;    // FC2 dgrad: the saved pre-activation
   int* status;
+  int* dep;           // per-expert count of first-GEMM epilogue warps done
 };
 
 template <int MODE>
 struct Mode {
   static constexpr bool kBMn = MODE == FC2_DGRAD || MODE == FC1_DGRAD;  // N contiguous in B
+  static constexpr bool kFirst = MODE == FC1_FWD || MODE == FC2_DGRAD;
   __device__ static int kblocks(const KParams& p) {
     const int nh = (p.H + 127) / 128, nf = (p.F + 127) / 128;
     return MODE == FC1_FWD || MODE == FC2_DGRAD ? nh : MODE == FC2_FWD ? nf : 2 * nf;
@@ -85,33 +103,36 @@ struct Mode {
 };
 
 struct Tile {
-  int e, m0, n0, rows, row0;
+  int e, m0, n0, rows, row0;  // m0: first row of this CTA's 128 in the expert; rows <= 0: none
+  int rows_odd;               // even CTA: rows left for the odd one
 };
 
 struct SmemCtl {
   uint64_t full[kStages], empty[kStages];
-  uint64_t sf_full[kScaleSlots], sf_empty[kScaleSlots];
-  uint64_t tmem_full, tmem_empty, drain;
+  uint64_t sf_full[2], sf_empty[2];
+  uint64_t tmem_full[2], tmem_empty[2], ovl, drain;
   uint32_t tmem_base;
   int abort;
-  int tstart[kMaxE + 1];
+  int tstart[2][kMaxE + 1];  // tile prefixes of the two GEMMs
   int off[kMaxE + 1];
-  uint32_t amax[2][8][32];  // block maxima handed between the two warps of a quarter
+  uint32_t amax[2][8][32];   // block maxima handed between the two warps of a quarter
 };
 
 template <int MODE>
-__device__ __forceinline__ Tile tile_at(const KParams& p, const SmemCtl& c, int tile,
-                                        int& cursor) {
-  while (c.tstart[cursor + 1] <= tile) ++cursor;
+__device__ __forceinline__ Tile tile_at(const KParams& p, const SmemCtl& c, int tile, int& cursor,
+                                        uint32_t rank) {
+  const int* tstart = c.tstart[Mode<MODE>::kFirst ? 0 : 1];
+  while (tstart[cursor + 1] <= tile) ++cursor;
   Tile t;
   t.e = cursor;
   t.row0 = c.off[cursor];
   const int cnt = c.off[cursor + 1] - t.row0;
-  const int local = tile - c.tstart[cursor];
-  const int mt = (cnt + BM - 1) / BM;
-  t.m0 = (local % mt) * BM;
+  const int local = tile - tstart[cursor];
+  const int mt = (cnt + 2 * BM - 1) / (2 * BM);
+  t.m0 = (local % mt) * 2 * BM + (int)rank * BM;
   t.n0 = (local / mt) * (MODE == FC1_FWD ? 128 : BN);
   t.rows = min(BM, cnt - t.m0);
+  t.rows_odd = rank == 0 ? cnt - t.m0 - BM : 0;
   return t;
 }
 
@@ -137,43 +158,55 @@ __host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N, int b_mn) {
   return ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
          ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void umma_mxf8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+// The pair's MMA: A rows, the scales of A and D are each CTA's own, B's N rows
+// are half in each CTA, B's scales whole in both.
+__device__ __forceinline__ void umma_mxf8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                               uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X "
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X "
       "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
-// 32 rows of 16 bytes from shared memory into four TMEM columns, repeated in
-// each warp's 32 lanes
-__device__ __forceinline__ void tmem_cp_scales(uint32_t dst, uint32_t saddr) {
-  // no swizzle: 8-row groups 128 bytes apart
-  const uint64_t desc = (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 16) |
-                        ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(dst), "l"(desc)
+// This warp's 32 lanes x 4 and x 8 TMEM columns
+__device__ __forceinline__ void tmem_st_x4(uint32_t taddr, const uint32_t (&w)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+               "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                : "memory");
 }
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
-                                            int32_t c0, int32_t c1, int32_t c2) {
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+template <int REGS>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map,
+                                                 uint32_t bar_cluster, int32_t c0, int32_t c1,
+                                                 int32_t c2) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(ptx::smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      ".cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(ptx::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
 
 // ---------------------------------------------------------------- stores
 // A warp's 32 rows x 64 bytes (thread i holds row i as four 16-byte chunks)
 // through its 2 KB buffer, so that each store covers 8 rows x 64 contiguous
-// bytes. Chunk c of row r sits at c ^ ((r >> 1) & 3): no bank conflicts.
+// bytes. Chunk c of row r sits at c ^ ((r >> 1) & 3): no bank conflicts. v[q] is
+// chunk q ^ flip.
 __device__ __forceinline__ void warp_store64(uint4* stage, const uint4 (&v)[4], uint8_t* base,
                                              size_t pitch, int lane, int valid_rows,
-                                             bool cols_ok) {
+                                             bool cols_ok, int flip = 0) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) stage[lane * 4 + (q ^ ((lane >> 1) & 3))] = v[q];
+  for (int q = 0; q < 4; ++q) stage[lane * 4 + (q ^ flip ^ ((lane >> 1) & 3))] = v[q];
   __syncwarp();
   if (cols_ok) {
 #pragma unroll
@@ -195,10 +228,11 @@ __device__ __forceinline__ void warp_store_words(uint4* stage, const uint32_t* w
   for (int q = 0; q < 4; ++q) v[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
   warp_store64(stage, v, reinterpret_cast<uint8_t*>(base), ld * 2, lane, valid_rows, cols_ok);
 }
-// 64 bf16 columns (32 packed words) rounded to e4m3
+// 64 bf16 columns (32 packed words) rounded to e4m3; the words of the 32 higher
+// columns come first when rev is set
 __device__ __forceinline__ void warp_store_fp8(uint4* stage, const uint32_t* w, float inv,
                                                uint8_t* base, size_t ld, int lane, int valid_rows,
-                                               bool cols_ok) {
+                                               bool cols_ok, int rev) {
   uint4 v[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q)
@@ -206,15 +240,68 @@ __device__ __forceinline__ void warp_store_fp8(uint4* stage, const uint32_t* w, 
                       fp8x4_of_bf16(w[8 * q + 2], w[8 * q + 3], inv),
                       fp8x4_of_bf16(w[8 * q + 4], w[8 * q + 5], inv),
                       fp8x4_of_bf16(w[8 * q + 6], w[8 * q + 7], inv));
-  warp_store64(stage, v, base, ld, lane, valid_rows, cols_ok);
+  warp_store64(stage, v, base, ld, lane, valid_rows, cols_ok, 2 * rev);
+}
+
+// ================================================================ dependences
+__device__ __forceinline__ int ld_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+// A second-GEMM tile of expert e: wait (bounded) until the expert's first-GEMM
+// tiles have all stored their output.
+__device__ __forceinline__ bool wait_expert(SmemCtl& c, const KParams& p, int e) {
+  const int target = 16 * (c.tstart[0][e + 1] - c.tstart[0][e]);  // 8 warps in each CTA
+  if (ld_acquire(p.dep + e) < target) {
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (ld_acquire(p.dep + e) < target) {
+      __nanosleep(64);
+      if (*(volatile int*)&c.abort || ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+        flag_timeout(c, p.status, 10);
+        return false;
+      }
+    }
+  }
+  return true;
 }
 
 // ================================================================ producer
+// Bytes of A loaded for a CTA's `rows` valid rows: rows that no expert has are not
+// fetched (what the buffer held stays in the unused rows of the product).
+__device__ __forceinline__ int a_bytes(int rows) {
+  return rows <= 0 ? 0 : rows > 64 ? kABytes : (rows + kABoxRows - 1) / kABoxRows * kABoxRows * BK;
+}
+template <int MODE>
+__device__ __forceinline__ void load_a(uint8_t* dst, const CUtensorMap* big,
+                                       const CUtensorMap* small, uint32_t bar, int x, int half,
+                                       int row, int rows) {
+  if (rows <= 0) return;
+  if (rows > 64) {
+    if (MODE == FC1_DGRAD) tma_load_3d_pair(dst, big, bar, x, half, row);
+    else ptx::tma_load_2d_pair(dst, big, bar, x, row);
+    return;
+  }
+  for (int r = 0; r < rows; r += kABoxRows) {
+    if (MODE == FC1_DGRAD) tma_load_3d_pair(dst + r * BK, small, bar, x, half, row + r);
+    else ptx::tma_load_2d_pair(dst + r * BK, small, bar, x, row + r);
+  }
+}
+
 template <int MODE>
 __device__ __forceinline__ bool producer_tile(SmemCtl& c, uint8_t* smem, const KParams& p,
-                                              const CUtensorMap* tmA, const CUtensorMap* tmB,
-                                              const Tile& t, int& stage, uint32_t& phase) {
+                                              const CUtensorMap* tmA, const CUtensorMap* tmS,
+                                              const CUtensorMap* tmB, const Tile& t, uint32_t rank,
+                                              int& stage, uint32_t& phase) {
+  // (the even CTA announces both CTAs' bytes)
+  const uint32_t bytes = 2 * kBBytes + a_bytes(t.rows) + a_bytes(min(BM, t.rows_odd));
+  const int row = t.row0 + t.m0;
   const int nk = Mode<MODE>::kblocks(p), nf = (p.F + 127) / 128;
+  if (!Mode<MODE>::kFirst) {
+    if (!wait_expert(c, p, t.e)) return false;
+    // the generic writes it waited for, before the TMA (async-proxy) reads
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+  }
   for (int kt = 0; kt < nk; ++kt) {
     if (!ptx::mbar_wait(&c.empty[stage], phase ^ 1, &c.abort, kWaitLimitNs)) {
       flag_timeout(c, p.status, 1);
@@ -222,26 +309,23 @@ __device__ __forceinline__ bool producer_tile(SmemCtl& c, uint8_t* smem, const K
     }
     uint8_t* sA = smem + stage * kStageBytes;
     uint8_t* sB = sA + kABytes;
-    uint64_t* bar = &c.full[stage];
     const int k0 = kt * BK;
-    ptx::mbar_arrive_expect_tx(bar, kStageBytes);
-    if (MODE == FC1_FWD) {
-      ptx::tma_load_2d(sA, tmA, bar, k0, t.row0 + t.m0);
-      ptx::tma_load_2d(sB, tmB, bar, k0, t.e * 2 * p.F + t.n0);                // 128 gate rows
-      ptx::tma_load_2d(sB + 16384, tmB, bar, k0, t.e * 2 * p.F + p.F + t.n0);  // 128 up rows
+    // both CTAs' loads complete on the even CTA's full[stage]
+    const uint32_t fb = ptx::mapa_shared(&c.full[stage], 0);
+    if (rank == 0) ptx::mbar_arrive_expect_tx(&c.full[stage], bytes);
+    if (MODE == FC1_FWD) {  // even CTA: 128 gate rows of W1, odd CTA: 128 up rows
+      load_a<MODE>(sA, tmA, tmS, fb, k0, 0, row, t.rows);
+      ptx::tma_load_2d_pair(sB, tmB, fb, k0, (2 * t.e + rank) * p.F + t.n0);
     } else if (MODE == FC2_FWD) {
-      ptx::tma_load_2d(sA, tmA, bar, k0, t.row0 + t.m0);
-      ptx::tma_load_2d(sB, tmB, bar, k0, t.e * p.H + t.n0);
-      ptx::tma_load_2d(sB + 16384, tmB, bar, k0, t.e * p.H + t.n0 + 128);
+      load_a<MODE>(sA, tmA, tmS, fb, k0, 0, row, t.rows);
+      ptx::tma_load_2d_pair(sB, tmB, fb, k0, t.e * p.H + t.n0 + 128 * rank);
     } else if (MODE == FC2_DGRAD) {
-      ptx::tma_load_2d(sA, tmA, bar, k0, t.row0 + t.m0);
-      tma_load_3d(sB, tmB, bar, t.n0, k0, t.e);
-      tma_load_3d(sB + 16384, tmB, bar, t.n0 + 128, k0, t.e);
+      load_a<MODE>(sA, tmA, tmS, fb, k0, 0, row, t.rows);
+      tma_load_3d_pair(sB, tmB, fb, t.n0 + 128 * rank, k0, t.e);
     } else {
       const int half = kt >= nf, kb = (kt - half * nf) * BK;
-      tma_load_3d(sA, tmA, bar, kb, half, t.row0 + t.m0);
-      tma_load_3d(sB, tmB, bar, t.n0, kb, 2 * t.e + half);
-      tma_load_3d(sB + 16384, tmB, bar, t.n0 + 128, kb, 2 * t.e + half);
+      load_a<MODE>(sA, tmA, tmS, fb, kb, half, row, t.rows);
+      tma_load_3d_pair(sB, tmB, fb, t.n0 + 128 * rank, kb, 2 * t.e + half);
     }
     if (++stage == kStages) {
       stage = 0;
@@ -252,6 +336,16 @@ __device__ __forceinline__ bool producer_tile(SmemCtl& c, uint8_t* smem, const K
 }
 
 // ================================================================ scales
+// One arrival on the even CTA's barrier, after this warp's TMEM accesses.
+__device__ __forceinline__ void release(uint64_t* bar, uint32_t rank, int lane) {
+  ptx::tc_fence_before();
+  __syncwarp();
+  if (lane == 0) {
+    if (rank == 0) ptx::mbar_arrive(bar);
+    else ptx::mbar_arrive_cluster(ptx::mapa_shared(bar, 0));
+  }
+}
+
 // Scale byte of weight block (K block kb, 128-column half i of the tile).
 template <int MODE>
 __device__ __forceinline__ uint32_t weight_scale(const KParams& p, const Tile& t, int kb, int i) {
@@ -272,12 +366,19 @@ __device__ __forceinline__ uint32_t weight_scale(const KParams& p, const Tile& t
 }
 
 template <int MODE>
-__device__ __forceinline__ bool scales_tile(SmemCtl& c, uint8_t* sf, const KParams& p,
-                                            const Tile& t, uint32_t& group, int lane) {
+__device__ __forceinline__ bool scales_tile(SmemCtl& c, const KParams& p, const Tile& t,
+                                            uint32_t tmem, uint32_t rank, uint32_t& group, int quarter,
+                                            int lane) {
   const int nk = Mode<MODE>::kblocks(p);
   const uint32_t* words = reinterpret_cast<const uint32_t*>(p.sa);
   const long long r0 = (long long)t.row0 + t.m0;
+  if (!Mode<MODE>::kFirst) {
+    bool ok = true;
+    if (lane == 0) ok = wait_expert(c, p, t.e);
+    if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+  }
   for (int g = 0; g * 4 < nk; ++g, ++group) {
+    // row r of the tile: lane r % 32, column r / 32
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -289,84 +390,92 @@ __device__ __forceinline__ bool scales_tile(SmemCtl& c, uint8_t* sf, const KPara
     uint32_t wb[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i) wb[i >> 2] |= __shfl_sync(0xffffffffu, b, i) << (8 * (i & 3));
-    const int slot = group % kScaleSlots;
-    if (!ptx::mbar_wait(&c.sf_empty[slot], ((group / kScaleSlots) & 1) ^ 1, &c.abort,
-                        kWaitLimitNs)) {
+    const int buf = group & 1;
+    if (!ptx::mbar_wait(&c.sf_empty[buf], ((group >> 1) & 1) ^ 1, &c.abort, kWaitLimitNs)) {
       if (lane == 0) flag_timeout(c, p.status, 2);
       return false;
     }
-    uint4* dst = reinterpret_cast<uint4*>(sf + slot * kScaleBytes);
-    dst[lane] = make_uint4(w[0], w[1], w[2], w[3]);
-    dst[32 + lane] = make_uint4(wb[0], wb[0], wb[0], wb[0]);
-    dst[64 + lane] = make_uint4(wb[1], wb[1], wb[1], wb[1]);
-    ptx::fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&c.sf_full[slot]);
+    ptx::tc_fence_after();  // the MMAs that read this buffer are done
+    const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + kTmemScales + buf * 12;
+    const uint32_t w0[4] = {wb[0], wb[0], wb[0], wb[0]}, w1[4] = {wb[1], wb[1], wb[1], wb[1]};
+    tmem_st_x4(at, w);
+    tmem_st_x4(at + 4, w0);
+    tmem_st_x4(at + 8, w1);
+    tmem_st_wait();
+    release(&c.sf_full[buf], rank, lane);
   }
   return true;
 }
 
 // ================================================================ MMA issuer
+// The whole warp runs this, so that addresses and descriptors stay in uniform
+// registers; one elected lane issues.
+struct MmaState {
+  int stage = 0;
+  uint32_t phase = 0, group = 0, tiles = 0;
+};
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 template <int MODE>
-__device__ __forceinline__ bool mma_tile(SmemCtl& c, uint8_t* smem, uint8_t* sf, const KParams& p,
-                                         uint32_t tmem, int& stage, uint32_t& phase,
-                                         uint32_t& group, uint32_t& acc_phase) {
-  constexpr uint32_t idesc = idesc_mxf8(BM, BN, Mode<MODE>::kBMn);
-  constexpr uint32_t b_lbo = Mode<MODE>::kBMn ? 16384 : 16;
+__device__ __forceinline__ bool mma_tile(SmemCtl& c, uint32_t smem, const KParams& p,
+                                         uint32_t tmem, MmaState& m) {
+  constexpr uint32_t idesc = idesc_mxf8(2 * BM, BN, Mode<MODE>::kBMn);
+  // one 128-byte atom wide in N (no second atom: LBO unused), or K-major
+  const uint64_t desc0 = ptx::sdesc_sw128(0, 16, 1024);
   constexpr uint32_t b_adv = Mode<MODE>::kBMn ? (4096 >> 4) : (32 >> 4);
   const int nk = Mode<MODE>::kblocks(p);
-  if (!ptx::mbar_wait(&c.tmem_empty, acc_phase ^ 1, &c.abort, kWaitLimitNs)) {
-    flag_timeout(c, p.status, 3);
+  const int acc = m.tiles & 1;
+  auto wait = [&](uint64_t* bar, uint32_t parity, int where) {
+    const bool got = ptx::mbar_wait(bar, parity, &c.abort, kWaitLimitNs);
+    if (__all_sync(0xffffffffu, got)) return true;
+    flag_timeout(c, p.status, where);
     return false;
-  }
+  };
+  // this accumulator free (two tiles ago), and the columns it shares with the
+  // other one read by the previous tile's epilogue
+  if (!wait(&c.tmem_empty[acc], ((m.tiles >> 1) & 1) ^ 1, 3)) return false;
+  if (m.tiles > 0 && !wait(&c.ovl, (m.tiles - 1) & 1, 3)) return false;
   ptx::tc_fence_after();
-  uint32_t sfa = 0, sfb = 0;
-  for (int kt = 0; kt < nk; ++kt) {
-    if ((kt & 3) == 0) {
-      // the next four K blocks' scales into the other TMEM buffer, once the
-      // MMAs that read it two groups ago are done
-      const int slot = group % kScaleSlots;
-      bool ok = ptx::mbar_wait(&c.sf_full[slot], (group / kScaleSlots) & 1, &c.abort, kWaitLimitNs);
-      if (ok && group >= 2)
-        ok = ptx::mbar_wait(&c.sf_empty[(group - 2) % kScaleSlots],
-                            ((group - 2) / kScaleSlots) & 1, &c.abort, kWaitLimitNs);
-      if (!ok) {
-        flag_timeout(c, p.status, 4);
-        return false;
-      }
-      ptx::tc_fence_after();
-      sfa = tmem + kTmemScales + (group & 1) * 12;
-      sfb = sfa + 4;
-      const uint32_t s = ptx::smem_u32(sf + slot * kScaleBytes);
-      tmem_cp_scales(sfa, s);
-      tmem_cp_scales(sfb, s + 512);
-      tmem_cp_scales(sfb + 4, s + 1024);
-    }
-    if (!ptx::mbar_wait(&c.full[stage], phase, &c.abort, kWaitLimitNs)) {
-      flag_timeout(c, p.status, 5);
-      return false;
-    }
-    ptx::tc_fence_after();
-    const uint32_t a_addr = ptx::smem_u32(smem + stage * kStageBytes);
-    const uint64_t adesc = ptx::sdesc_sw128(a_addr, 16, 1024);
-    const uint64_t bdesc = ptx::sdesc_sw128(a_addr + kABytes, b_lbo, 1024);
-    const uint32_t id = idesc | ((uint32_t)(kt & 3) << 4) | ((uint32_t)(kt & 3) << 29);
+  const uint32_t d = tmem + acc * kAccStep;
+  for (int k0 = 0; k0 < nk; k0 += 4) {  // four K blocks: one buffer of scales
+    const int buf = m.group & 1;
+    if (!wait(&c.sf_full[buf], (m.group >> 1) & 1, 4)) return false;
+    const uint32_t sfa = tmem + kTmemScales + buf * 12;
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-      umma_mxf8(tmem, adesc + (uint64_t)(kk * 2), bdesc + (uint64_t)(kk * b_adv), id, sfa, sfb,
-                (kt | kk) != 0);
-    ptx::umma_commit(&c.empty[stage]);
-    if ((kt & 3) == 3 || kt == nk - 1) {
-      ptx::umma_commit(&c.sf_empty[group % kScaleSlots]);
-      ++group;
+    for (int kb = 0; kb < 4; ++kb) {
+      if (k0 + kb >= nk) break;
+      if (!wait(&c.full[m.stage], m.phase, 5)) return false;
+      ptx::tc_fence_after();
+      const uint64_t adesc = desc0 | ((smem + m.stage * kStageBytes) >> 4);
+      const uint64_t bdesc = adesc + (kABytes >> 4);
+      constexpr uint32_t kSel = (1u << 4) | (1u << 29);  // scale byte kb of both operands
+      const uint32_t acc_on = (k0 + kb) != 0;
+      if (elect_one()) {
+        umma_mxf8_pair(d, adesc, bdesc, idesc | kb * kSel, sfa, sfa + 4, acc_on);
+#pragma unroll
+        for (int kk = 1; kk < 4; ++kk)
+          umma_mxf8_pair(d, adesc + kk * 2, bdesc + kk * b_adv, idesc | kb * kSel, sfa, sfa + 4, 1);
+        ptx::umma_commit_pair(&c.empty[m.stage], 3);
+        if (kb == 3 || k0 + kb == nk - 1) ptx::umma_commit_pair(&c.sf_empty[buf], 3);
+        if (k0 + kb == nk - 1) ptx::umma_commit_pair(&c.tmem_full[acc], 3);
+      }
+      __syncwarp();
+      if (++m.stage == kStages) {
+        m.stage = 0;
+        m.phase ^= 1;
+      }
     }
-    if (++stage == kStages) {
-      stage = 0;
-      phase ^= 1;
-    }
+    ++m.group;
   }
-  ptx::umma_commit(&c.tmem_full);
-  acc_phase ^= 1;
+  ++m.tiles;
   return true;
 }
 
@@ -381,49 +490,43 @@ __device__ __forceinline__ uint32_t pair_max(SmemCtl& c, uint32_t m, int ew, int
   return max(m, c.amax[buf][ew ^ 4][lane]);
 }
 
-// Plain fp32 tile -> bf16: this warp's 32 rows x 64 columns of each 128.
-__device__ __forceinline__ void store_plain(uint4* stage, uint32_t tbase, int hf, bf16* slab,
-                                            int ld, int n0, int lane, int slab_rows) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int cc = (i >> 1) * 4 + 2 * hf + (i & 1);
-    uint32_t v[32];
-    ptx::tmem_ld_32x32b_x32(tbase + 32 * cc, v);
-    ptx::tmem_ld_wait(v);
-    uint32_t w[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      w[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-    warp_store_words(stage, w, slab + 32 * cc, ld, lane, slab_rows, n0 + 32 * cc < ld);
-  }
-}
-
+// The columns that the two accumulators share are the first one's last 32 and
+// the second one's first 32. An epilogue therefore takes its 32-column chunks
+// in falling order on the first accumulator (rev = 1) and in rising order on the
+// second; the warps that hold the shared chunk (hf == rev) release it as soon as
+// it is in registers.
 template <int MODE>
 __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, uint8_t* stage_base, const KParams& p,
-                                              const Tile& t, uint32_t tmem, uint32_t& acc_phase,
-                                              int ew, int lane) {
+                                              const Tile& t, uint32_t tmem, uint32_t rank,
+                                              uint32_t& tiles, int ew, int lane) {
   const int q = ew & 3, hf = ew >> 2;
+  const int acc = tiles & 1, rev = acc ^ 1;
   uint4* stage = reinterpret_cast<uint4*>(stage_base) + ew * 128;
-  if (!ptx::mbar_wait(&c.tmem_full, acc_phase, &c.abort, kWaitLimitNs)) {
+  if (!ptx::mbar_wait(&c.tmem_full[acc], (tiles >> 1) & 1, &c.abort, kWaitLimitNs)) {
     if (lane == 0) flag_timeout(c, p.status, 6);
     return false;
   }
   ptx::tc_fence_after();
-  const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
+  const uint32_t tbase = tmem + acc * kAccStep + ((uint32_t)(q * 32) << 16);
   const size_t row0 = (size_t)t.row0 + t.m0 + q * 32;  // this warp's 32 rows
   const int slab_rows = min(32, t.rows - q * 32);
-  if (MODE == FC1_FWD) {
+  if (slab_rows <= 0) {  // (both warps of the quarter)
+    if (hf == rev) release(&c.ovl, rank, lane);
+    release(&c.tmem_empty[acc], rank, lane);
+  } else if (MODE == FC1_FWD) {
     // columns 0..127 gate, 128..255 up of one 128-wide block of h
     uint32_t hw[32];
     uint32_t mx = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int cc = 2 * hf + i, f = t.n0 + 32 * cc;
+      const int cc = 2 * hf + (i ^ rev), f = t.n0 + 32 * cc;
       const bool ok = f < p.F;
       uint32_t g[32], u[32];
       ptx::tmem_ld_32x32b_x32(tbase + 32 * cc, g);
       ptx::tmem_ld_32x32b_x32(tbase + 128 + 32 * cc, u);
       ptx::tmem_ld_wait(g, u);
+      if (i == 0 && hf == rev) release(&c.ovl, rank, lane);
+      if (i == 1) release(&c.tmem_empty[acc], rank, lane);
       uint32_t gw[16], uw[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
@@ -444,22 +547,22 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, uint8_t* stage_base, c
         warp_store_words(stage, hw + 16 * i, p.out1 + row0 * (size_t)p.F + f, p.F, lane, slab_rows,
                          ok);
     }
-    const uint32_t b = fp8_scale_byte(pair_max(c, absmax_bits(mx), ew, lane, acc_phase));
+    const uint32_t b = fp8_scale_byte(pair_max(c, absmax_bits(mx), ew, lane, acc));
     const int f = t.n0 + 64 * hf, fb = t.n0 / 128;
     warp_store_fp8(stage, hw, fp8_inv_scale(b), p.q + row0 * (size_t)p.F + f, p.F, lane, slab_rows,
-                   f < p.F);
+                   f < p.F, rev);
     if (hf == 0 && lane < slab_rows)
       p.s[((size_t)(fb >> 2) * p.N + row0 + lane) * 4 + (fb & 3)] = (uint8_t)b;
   } else if (MODE == FC2_DGRAD) {
     const int nf = (p.F + 127) / 128;
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half) {  // 128 columns: one block of da_gate, one of da_up
-      if (t.n0 + 128 * half >= p.F) break;
+    for (int hi = 0; hi < 2; ++hi) {  // 128 columns: one block of da_gate, one of da_up
+      const int half = hi ^ rev;
       uint32_t gw[32], uw[32];
       uint32_t mg = 0, mu = 0;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int cc = 4 * half + 2 * hf + i, f = t.n0 + 32 * cc;
+        const int cc = 4 * half + 2 * hf + (i ^ rev), f = t.n0 + 32 * cc;
         const bool ok = f < p.F;
         uint32_t v[32];
         ptx::tmem_ld_32x32b_x32(tbase + 32 * cc, v);
@@ -473,6 +576,8 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, uint8_t* stage_base, c
           uc[j] = rok ? __ldg(src + p.F / 8 + j) : make_uint4(0, 0, 0, 0);
         }
         ptx::tmem_ld_wait(v);
+        if (hi == 0 && i == 0 && hf == rev) release(&c.ovl, rank, lane);
+        if (hi == 1 && i == 1) release(&c.tmem_empty[acc], rank, lane);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const uint32_t* gp = reinterpret_cast<const uint32_t*>(gc);
@@ -498,71 +603,104 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, uint8_t* stage_base, c
       const uint32_t bu = fp8_scale_byte(pair_max(c, absmax_bits(mu), ew, lane, 1));
       const int f = t.n0 + 128 * half + 64 * hf;
       uint8_t* qbase = p.q + row0 * (size_t)(2 * p.F);
-      warp_store_fp8(stage, gw, fp8_inv_scale(bg), qbase + f, 2 * p.F, lane, slab_rows, f < p.F);
+      warp_store_fp8(stage, gw, fp8_inv_scale(bg), qbase + f, 2 * p.F, lane, slab_rows, f < p.F,
+                     rev);
       warp_store_fp8(stage, uw, fp8_inv_scale(bu), qbase + p.F + f, 2 * p.F, lane, slab_rows,
-                     f < p.F);
-      if (lane < slab_rows) {
+                     f < p.F, rev);
+      if (lane < slab_rows && t.n0 + 128 * half < p.F) {
         const int kb = hf * nf + t.n0 / 128 + half;  // the gate's byte or the up half's
         p.s[((size_t)(kb >> 2) * p.N + row0 + lane) * 4 + (kb & 3)] = (uint8_t)(hf ? bu : bg);
       }
     }
   } else {
-    store_plain(stage, tbase, hf, p.out0 + row0 * (size_t)p.H + t.n0, p.H, t.n0, lane, slab_rows);
+    // plain fp32 tile -> bf16
+    bf16* slab = p.out0 + row0 * (size_t)p.H + t.n0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int ci = i ^ (3 * rev);
+      const int cc = (ci >> 1) * 4 + 2 * hf + (ci & 1);
+      uint32_t v[32];
+      ptx::tmem_ld_32x32b_x32(tbase + 32 * cc, v);
+      ptx::tmem_ld_wait(v);
+      if (i == 0 && hf == rev) release(&c.ovl, rank, lane);
+      if (i == 3) release(&c.tmem_empty[acc], rank, lane);
+      uint32_t w[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        w[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+      warp_store_words(stage, w, slab + 32 * cc, p.H, lane, slab_rows, t.n0 + 32 * cc < p.H);
+    }
   }
-  ptx::tc_fence_before();
-  __syncwarp();
-  if (lane == 0) ptx::mbar_arrive(&c.tmem_empty);
-  acc_phase ^= 1;
+  if (Mode<MODE>::kFirst) {
+    // this warp's part of the tile is stored: visible before the counter moves
+    __threadfence();
+    __syncwarp();
+    if (lane == 0) atomicAdd(p.dep + t.e, 1);
+  }
+  ++tiles;
   return true;
 }
 
-template <int MODE>
+template <int M1, int M2>
 __global__ void __launch_bounds__(kThreads, 1)
-    grouped_gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmA,
-                            const __grid_constant__ CUtensorMap tmB, const KParams p) {
+    grouped_gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmA1,
+                            const __grid_constant__ CUtensorMap tmS1,
+                            const __grid_constant__ CUtensorMap tmB1,
+                            const __grid_constant__ CUtensorMap tmA2,
+                            const __grid_constant__ CUtensorMap tmS2,
+                            const __grid_constant__ CUtensorMap tmB2, const KParams p1,
+                            const KParams p2) {
   extern __shared__ uint8_t dyn_smem[];
   __shared__ SmemCtl ctl;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) &
                                              ~uintptr_t(1023));
-  uint8_t* sf = smem + kStages * kStageBytes;
-  uint8_t* stage_base = sf + kScaleSlots * kScaleBytes;
+  uint8_t* stage_base = smem + kStages * kStageBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = p1.E;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(&ctl.full[s], 1);
       ptx::mbar_init(&ctl.empty[s], 1);
     }
-    for (int s = 0; s < kScaleSlots; ++s) {
-      ptx::mbar_init(&ctl.sf_full[s], 1);
-      ptx::mbar_init(&ctl.sf_empty[s], 1);
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(&ctl.sf_full[a], 8);  // both CTAs' scale warps
+      ptx::mbar_init(&ctl.sf_empty[a], 1);
+      ptx::mbar_init(&ctl.tmem_full[a], 1);
+      ptx::mbar_init(&ctl.tmem_empty[a], 16);  // both CTAs' epilogue warps
     }
-    ptx::mbar_init(&ctl.tmem_full, 1);
-    ptx::mbar_init(&ctl.tmem_empty, 8);
+    ptx::mbar_init(&ctl.ovl, 8);  // the four warps of each CTA that hold the shared columns
     ptx::mbar_init(&ctl.drain, 1);
     ctl.abort = 0;
     ptx::fence_mbar_init();
   }
+  __syncthreads();
+  ptx::cluster_sync();  // barriers are live in both CTAs before TMEM is allocated for the pair
   if (warp == 1) {
-    ptx::tmem_alloc(&ctl.tmem_base, kTmemCols);
-    ptx::tmem_relinquish();
+    ptx::tmem_alloc_pair(&ctl.tmem_base, kTmemCols);
+    ptx::tmem_relinquish_pair();
   }
   if (threadIdx.x == 0) {
-    ptx::tma_prefetch_desc(&tmA);
-    ptx::tma_prefetch_desc(&tmB);
+    ptx::tma_prefetch_desc(&tmA1);
+    ptx::tma_prefetch_desc(&tmS1);
+    ptx::tma_prefetch_desc(&tmS2);
+    ptx::tma_prefetch_desc(&tmB1);
+    ptx::tma_prefetch_desc(&tmA2);
+    ptx::tma_prefetch_desc(&tmB2);
   }
   pdl_wait();
   // offsets outside 0..N would send stores out of the buffers
-  for (int e = threadIdx.x; e <= p.E; e += blockDim.x)
-    ctl.off[e] = (int)min(max((long long)p.off[e], 0ll), p.N);
+  for (int e = threadIdx.x; e <= E; e += blockDim.x)
+    ctl.off[e] = (int)min(max((long long)p1.off[e], 0ll), p1.N);
   __syncthreads();
-  if (warp == 0) {  // tiles per expert -> exclusive prefix
+  if (warp < 2) {  // pair tiles per expert -> exclusive prefix, one warp for each GEMM
+    const int nt = warp == 0 ? Mode<M1>::ntiles(p1) : Mode<M2>::ntiles(p2);
     int carry = 0;
-    for (int base = 0; base < p.E; base += 32) {
+    for (int base = 0; base < E; base += 32) {
       const int e = base + lane;
       int n = 0;
-      if (e < p.E) {
+      if (e < E) {
         const int cnt = ctl.off[e + 1] - ctl.off[e];
-        n = cnt > 0 ? (cnt + BM - 1) / BM * Mode<MODE>::ntiles(p) : 0;
+        n = cnt > 0 ? (cnt + 2 * BM - 1) / (2 * BM) * nt : 0;
       }
       int incl = n;
 #pragma unroll
@@ -570,56 +708,68 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
       }
-      if (e < p.E) ctl.tstart[e] = carry + incl - n;
+      if (e < E) ctl.tstart[warp][e] = carry + incl - n;
       carry += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) ctl.tstart[p.E] = carry;
+    if (lane == 0) ctl.tstart[warp][E] = carry;
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
-  const int total = ctl.tstart[p.E];
-  int cursor = 0;
-  if (warp == 0) {
-    if (lane == 0) {
+  const uint32_t rank = ptx::cluster_ctarank();
+  const int total1 = ctl.tstart[0][E], total = total1 + ctl.tstart[1][E];
+  const int first = (int)ptx::cluster_id_x(), stride = (int)ptx::cluster_count_x();
+  int cur1 = 0, cur2 = 0;
+  auto tile1 = [&](int i) { return tile_at<M1>(p1, ctl, i, cur1, rank); };
+  auto tile2 = [&](int i) { return tile_at<M2>(p2, ctl, i - total1, cur2, rank); };
+  if (warp < 4) {
+    regs_dec<kRegsControl>();
+    if (warp == 0 && lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
-      for (int tile = blockIdx.x; tile < total; tile += gridDim.x)
-        if (!producer_tile<MODE>(ctl, smem, p, &tmA, &tmB, tile_at<MODE>(p, ctl, tile, cursor),
-                                 stage, phase))
-          break;
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, group = 0, acc_phase = 0;
-      for (int tile = blockIdx.x; tile < total; tile += gridDim.x)
-        if (!mma_tile<MODE>(ctl, smem, sf, p, tmem, stage, phase, group, acc_phase)) break;
-      // no MMA may still run when TMEM is released
-      ptx::umma_commit(&ctl.drain);
+      bool ok = true;
+      for (int i = first; ok && i < total; i += stride)
+        ok = i < total1 ? producer_tile<M1>(ctl, smem, p1, &tmA1, &tmS1, &tmB1, tile1(i), rank,
+                                            stage, phase)
+                        : producer_tile<M2>(ctl, smem, p2, &tmA2, &tmS2, &tmB2, tile2(i), rank,
+                                            stage, phase);
+    } else if (warp == 1 && rank == 0) {
+      MmaState m;
+      bool ok = true;
+      for (int i = first; ok && i < total; i += stride)
+        ok = i < total1 ? mma_tile<M1>(ctl, ptx::smem_u32(smem), p1, tmem, m)
+                        : mma_tile<M2>(ctl, ptx::smem_u32(smem), p2, tmem, m);
+      // no MMA may still run when TMEM is released (the same lane is elected as above)
+      __syncwarp();
+      if (elect_one()) ptx::umma_commit_pair(&ctl.drain, 1);
       if (!ptx::mbar_wait(&ctl.drain, 0, &ctl.abort, kWaitLimitNs)) {
         int dummy = 0;
         ptx::mbar_wait(&ctl.drain, 0, &dummy, kWaitLimitNs);
       }
     }
     __syncwarp();
-  } else if (warp == 2) {
+  } else if (warp < 12) {
+    regs_inc<kRegsEpilogue>();
+    uint32_t tiles = 0;
+    bool ok = true;
+    for (int i = first; ok && i < total; i += stride)
+      ok = i < total1
+               ? epilogue_tile<M1>(ctl, stage_base, p1, tile1(i), tmem, rank, tiles, warp - 4, lane)
+               : epilogue_tile<M2>(ctl, stage_base, p2, tile2(i), tmem, rank, tiles, warp - 4, lane);
+  } else {
+    regs_dec<kRegsControl>();
     uint32_t group = 0;
-    for (int tile = blockIdx.x; tile < total; tile += gridDim.x)
-      if (!scales_tile<MODE>(ctl, sf, p, tile_at<MODE>(p, ctl, tile, cursor), group, lane)) break;
-  } else if (warp >= 4) {
-    uint32_t acc_phase = 0;
-    for (int tile = blockIdx.x; tile < total; tile += gridDim.x)
-      if (!epilogue_tile<MODE>(ctl, stage_base, p, tile_at<MODE>(p, ctl, tile, cursor), tmem,
-                               acc_phase, warp - 4, lane))
-        break;
+    bool ok = true;
+    for (int i = first; ok && i < total; i += stride)
+      ok = i < total1 ? scales_tile<M1>(ctl, p1, tile1(i), tmem, rank, group, warp - 12, lane)
+                      : scales_tile<M2>(ctl, p2, tile2(i), tmem, rank, group, warp - 12, lane);
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == 1) ptx::tmem_dealloc(tmem, kTmemCols);
+  ptx::cluster_sync();  // the peer may still arrive on this CTA's barriers
+  if (warp == 1) ptx::tmem_dealloc_pair(tmem, kTmemCols);
 }
 
 // ------------------------------------------------------------------ host side
@@ -666,31 +816,66 @@ bool make_map(CUtensorMap* m, const void* base, int dims, long long d0, long lon
   return true;
 }
 
-template <int MODE>
-moe_status_t launch_mode(const moe_layer_desc_t& d, const CUtensorMap& a, const CUtensorMap& b,
-                         const KParams& p, cudaStream_t st) {
-  // once for each device (the attribute belongs to the device's copy of the kernel)
-  static std::atomic<uint64_t> ready{0};
+// How many pairs can be resident at once on the current device, after setting
+// the kernel's shared memory up there (once for each device).
+template <int M1, int M2>
+cudaError_t resident_pairs(int* pairs) {
+  static std::atomic<int> known[64];
   int dev = 0;
-  cudaError_t attr = cudaGetDevice(&dev);
-  const uint64_t bit = 1ull << (dev & 63);
-  if (attr == cudaSuccess && !(ready.load() & bit)) {
-    attr = cudaFuncSetAttribute(grouped_gemm_fp8_kernel<MODE>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDynSmem);
-    if (attr == cudaSuccess) ready.fetch_or(bit);
-  }
-  if (attr != cudaSuccess) {
-    set_error("kernel attribute setup failed: %s", cudaGetErrorString(attr));
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (*pairs = known[dev].load()) > 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(grouped_gemm_fp8_kernel<M1, M2>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDynSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(device_sm_count() / 2 * 2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kDynSmem;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaOccupancyMaxActiveClusters(pairs, grouped_gemm_fp8_kernel<M1, M2>, &cfg);
+  if (e == cudaSuccess && *pairs < 1) e = cudaErrorLaunchOutOfResources;
+  if (e == cudaSuccess && dev < 64) known[dev].store(*pairs);
+  return e;
+}
+
+template <int M1, int M2>
+moe_status_t launch_chain(const moe_layer_desc_t& d, const CUtensorMap (&m)[6], const KParams& p1,
+                          const KParams& p2, int kernel_id, bool counters_zeroed, cudaStream_t st) {
+  int pairs = 0;
+  cudaError_t e = resident_pairs<M1, M2>(&pairs);
+  if (e == cudaSuccess && !counters_zeroed)
+    e = cudaMemsetAsync(p1.dep, 0, (size_t)d.E * sizeof(int), st);
+  if (e != cudaSuccess) {
+    set_error("grouped_gemm_fp8_kernel set-up: %s", cudaGetErrorString(e));
     return MOE_ERR_CUDA;
   }
-  const int nt = MODE == FC1_FWD ? ceil_div(d.F, 128)
-                                 : ceil_div(MODE == FC2_DGRAD ? d.F : d.H, BN);
-  const long long tiles = (p.N / BM + (p.N < d.E ? p.N : d.E)) * nt;  // at most
-  const int grid = (int)std::min<long long>(device_sm_count(), tiles);
-  cudaError_t e;
+  // at most as many pairs as can be resident (second-GEMM tiles wait for
+  // first-GEMM tiles of other pairs), and no more than there can be tiles
+  const long long n1 = M1 == FC1_FWD ? ceil_div(d.F, 128) : ceil_div(d.F, BN);
+  const long long rows = p1.N / (2 * BM) + std::min<long long>(p1.N, d.E);
+  pairs = (int)std::min<long long>(pairs, rows * (n1 + ceil_div(d.H, BN)));
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = MOE_PDL;
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kDynSmem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
   {
-    LaunchScope _ls(K_FP8_FC1_FWD + MODE, st);
-    e = launch_k(grouped_gemm_fp8_kernel<MODE>, grid, kThreads, kDynSmem, st, a, b, p);
+    LaunchScope _ls(kernel_id, st);
+    e = cudaLaunchKernelEx(&cfg, grouped_gemm_fp8_kernel<M1, M2>, m[0], m[1], m[2], m[3], m[4], m[5], p1, p2);
   }
   if (e != cudaSuccess) {
     set_error("grouped_gemm_fp8_kernel launch: %s", cudaGetErrorString(e));
@@ -699,7 +884,7 @@ moe_status_t launch_mode(const moe_layer_desc_t& d, const CUtensorMap& a, const 
   return check_launch("grouped_gemm_fp8_kernel");
 }
 
-KParams params(const moe_layer_desc_t& d, const int32_t* off, int* status) {
+KParams params(const moe_layer_desc_t& d, const int32_t* off, int* status, int* dep) {
   KParams p = {};
   p.E = d.E;
   p.H = d.H;
@@ -707,6 +892,7 @@ KParams params(const moe_layer_desc_t& d, const int32_t* off, int* status) {
   p.N = (long long)d.T * d.k;
   p.off = off;
   p.status = status;
+  p.dep = dep;
   return p;
 }
 
@@ -718,13 +904,13 @@ moe_status_t launch_ffn_fwd_fp8(const moe_layer_desc_t& d, const uint8_t* xq, co
                                 cudaStream_t st, bool counters_zeroed) {
   const long long N = (long long)d.T * d.k;
   if (N == 0) return MOE_OK;
-  CUtensorMap a1, b1, a2, b2;
-  if (!make_map(&a1, xq, 2, d.H, N, 1, BM, 1) ||
-      !make_map(&b1, w.w1q, 2, d.H, 2ll * d.E * d.F, 1, 128, 1) ||
-      !make_map(&a2, hq, 2, d.F, N, 1, BM, 1) ||
-      !make_map(&b2, w.w2q, 2, d.F, (long long)d.E * d.H, 1, 128, 1))
+  CUtensorMap m[6];
+  if (!make_map(&m[0], xq, 2, d.H, N, 1, BM, 1) || !make_map(&m[1], xq, 2, d.H, N, 1, kABoxRows, 1) ||
+      !make_map(&m[2], w.w1q, 2, d.H, 2ll * d.E * d.F, 1, 128, 1) ||
+      !make_map(&m[3], hq, 2, d.F, N, 1, BM, 1) || !make_map(&m[4], hq, 2, d.F, N, 1, kABoxRows, 1) ||
+      !make_map(&m[5], w.w2q, 2, d.F, (long long)d.E * d.H, 1, 128, 1))
     return MOE_ERR_CUDA;
-  KParams p1 = params(d, off, status), p2 = p1;
+  KParams p1 = params(d, off, status, dep), p2 = p1;
   p1.sa = xs;
   p1.sb = w.w1s;
   p1.out0 = a;
@@ -734,8 +920,7 @@ moe_status_t launch_ffn_fwd_fp8(const moe_layer_desc_t& d, const uint8_t* xq, co
   p2.sa = hs;
   p2.sb = w.w2s;
   p2.out0 = o;
-  const moe_status_t s = launch_mode<FC1_FWD>(d, a1, b1, p1, st);
-  return s != MOE_OK ? s : launch_mode<FC2_FWD>(d, a2, b2, p2, st);
+  return launch_chain<FC1_FWD, FC2_FWD>(d, m, p1, p2, K_FP8_FFN_FWD, counters_zeroed, st);
 }
 
 moe_status_t launch_ffn_dgrad_fp8(const moe_layer_desc_t& d, const uint8_t* dq, const uint8_t* ds,
@@ -744,13 +929,13 @@ moe_status_t launch_ffn_dgrad_fp8(const moe_layer_desc_t& d, const uint8_t* dq, 
                                   cudaStream_t st, bool counters_zeroed) {
   const long long N = (long long)d.T * d.k;
   if (N == 0) return MOE_OK;
-  CUtensorMap a1, b1, a2, b2;
-  if (!make_map(&a1, dq, 2, d.H, N, 1, BM, 1) ||
-      !make_map(&b1, w.w2q, 3, d.F, d.H, d.E, 128, 1) ||
-      !make_map(&a2, daq, 3, d.F, 2, N, 1, BM) ||
-      !make_map(&b2, w.w1q, 3, d.H, d.F, 2ll * d.E, 128, 1))
+  CUtensorMap m[6];
+  if (!make_map(&m[0], dq, 2, d.H, N, 1, BM, 1) || !make_map(&m[1], dq, 2, d.H, N, 1, kABoxRows, 1) ||
+      !make_map(&m[2], w.w2q, 3, d.F, d.H, d.E, 128, 1) ||
+      !make_map(&m[3], daq, 3, d.F, 2, N, 1, BM) || !make_map(&m[4], daq, 3, d.F, 2, N, 1, kABoxRows) ||
+      !make_map(&m[5], w.w1q, 3, d.H, d.F, 2ll * d.E, 128, 1))
     return MOE_ERR_CUDA;
-  KParams p1 = params(d, off, status), p2 = p1;
+  KParams p1 = params(d, off, status, dep), p2 = p1;
   p1.sa = ds;
   p1.sb = w.w2s;
   p1.out0 = da;
@@ -760,8 +945,7 @@ moe_status_t launch_ffn_dgrad_fp8(const moe_layer_desc_t& d, const uint8_t* dq, 
   p2.sa = das;
   p2.sb = w.w1s;
   p2.out0 = dx_perm;
-  const moe_status_t s = launch_mode<FC2_DGRAD>(d, a1, b1, p1, st);
-  return s != MOE_OK ? s : launch_mode<FC1_DGRAD>(d, a2, b2, p2, st);
+  return launch_chain<FC2_DGRAD, FC1_DGRAD>(d, m, p1, p2, K_FP8_FFN_DGRAD, counters_zeroed, st);
 }
 
 }  // namespace moe
