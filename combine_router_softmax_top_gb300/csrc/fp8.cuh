@@ -22,7 +22,7 @@ constexpr int kFp8Block = 128;  // values (or rows and columns) that share a sca
 
 enum Fp8KernelId {  // kernel ids past those of the bf16 layer
   K_FP8_QUANT_W = K_NUM, K_FP8_PERMUTE, K_FP8_COMBINE_BWD, K_FP8_FFN_FWD, K_FP8_FFN_DGRAD,
-  K_ALL
+  K_FP8_ZERO, K_FP8_ROWS_FFN, K_ALL
 };
 
 // ---------------------------------------------------------------- block scales
@@ -85,6 +85,13 @@ moe_status_t launch_ffn_fwd_fp8(const moe_layer_desc_t& d, const uint8_t* xq, co
                                 const int32_t* off, const Fp8Weights& w, bf16* a, bf16* h,
                                 uint8_t* hq, uint8_t* hs, bf16* o, int* status, int* dep,
                                 cudaStream_t st, bool counters_zeroed = false);
+// The forward for few rows an expert (rows_fp8.cu), which launch_ffn_fwd_fp8 takes
+// up to kFp8FewRows rows an expert on average.
+constexpr long long kFp8FewRows = 16;
+moe_status_t launch_ffn_rows_fp8(const moe_layer_desc_t& d, const uint8_t* xq, const uint8_t* xs,
+                                 const int32_t* off, const Fp8Weights& w, bf16* a, bf16* h,
+                                 uint8_t* hq, uint8_t* hs, bf16* o, int* status, int* dep,
+                                 cudaStream_t st, bool counters_zeroed);
 // Expert FFN activation gradient: da (bf16) is written when given.
 moe_status_t launch_ffn_dgrad_fp8(const moe_layer_desc_t& d, const uint8_t* dq, const uint8_t* ds,
                                   const bf16* a, const int32_t* off, const Fp8Weights& w, bf16* da,

@@ -21,6 +21,13 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
     if (!aligned16(p)) { set_error("%s is not 16-byte aligned", #p); return MOE_ERR_INVALID_ARG; } \
   } while (0)
 
+// rows that the expert products move in whole 32-byte sectors
+#define MOE_PTR32(p)                                                                           \
+  do {                                                                                         \
+    MOE_PTR(p);                                                                                \
+    if (reinterpret_cast<uintptr_t>(p) & 31u) { set_error("%s is not 32-byte aligned", #p); return MOE_ERR_INVALID_ARG; } \
+  } while (0)
+
 #define MOE_PTR_OPT(p)                                                                         \
   do {                                                                                         \
     if ((p) && !aligned16(p)) { set_error("%s is not 16-byte aligned", #p); return MOE_ERR_INVALID_ARG; } \
@@ -82,7 +89,9 @@ moe_status_t moe_expert_ffn_fwd_fp8(const moe_layer_desc_t* d, const moe_e4m3* x
                                     moe_bf16* o, void* ws, size_t ws_bytes, void* stream) {
   MOE_CHECK(validate(d));
   MOE_PTR(xq); MOE_PTR(xs); MOE_PTR(off); MOE_PTR(w1q); MOE_PTR(w1s); MOE_PTR(w2q); MOE_PTR(w2s);
-  MOE_PTR_OPT(a); MOE_PTR_OPT(h); MOE_PTR(hq); MOE_PTR(hs); MOE_PTR(o);
+  if (a) MOE_PTR32(a);
+  if (h) MOE_PTR32(h);
+  MOE_PTR32(hq); MOE_PTR(hs); MOE_PTR32(o);
   MOE_CHECK(check_ws(*d, ws, ws_bytes));
   return launch_ffn_fwd_fp8(*d, xq, xs, off, Fp8Weights{w1q, w1s, w2q, w2s}, BFW(a), BFW(h), hq,
                             hs, BFW(o), status_of(ws), dep_of(*d, ws), S(stream));
@@ -106,8 +115,9 @@ moe_status_t moe_expert_ffn_bwd_dgrad_fp8(const moe_layer_desc_t* d, const moe_e
                                           moe_e8m0* das, moe_bf16* dx_perm, void* ws,
                                           size_t ws_bytes, void* stream) {
   MOE_CHECK(validate(d));
-  MOE_PTR(dq); MOE_PTR(ds); MOE_PTR(a); MOE_PTR(off); MOE_PTR(w1q); MOE_PTR(w1s); MOE_PTR(w2q);
-  MOE_PTR(w2s); MOE_PTR_OPT(da); MOE_PTR(daq); MOE_PTR(das); MOE_PTR(dx_perm);
+  MOE_PTR(dq); MOE_PTR(ds); MOE_PTR32(a); MOE_PTR(off); MOE_PTR(w1q); MOE_PTR(w1s); MOE_PTR(w2q);
+  MOE_PTR(w2s); MOE_PTR32(daq); MOE_PTR(das); MOE_PTR32(dx_perm);
+  if (da) MOE_PTR32(da);
   MOE_CHECK(check_ws(*d, ws, ws_bytes));
   return launch_ffn_dgrad_fp8(*d, dq, ds, BF(a), off, Fp8Weights{w1q, w1s, w2q, w2s}, BFW(da), daq,
                               das, BFW(dx_perm), status_of(ws), dep_of(*d, ws), S(stream));
@@ -133,12 +143,12 @@ moe_status_t moe_layer_forward_fp8(const moe_layer_desc_t* d, const moe_mb_bufs_
                                    const moe_fp8_bufs_t* q, int32_t save, void* stream) {
   MOE_CHECK(validate(d));
   MOE_CHECK(check_weights(q));
-  MOE_PTR(q->xq); MOE_PTR(q->xs); MOE_PTR(q->hq); MOE_PTR(q->hs);
+  MOE_PTR(q->xq); MOE_PTR(q->xs); MOE_PTR32(q->hq); MOE_PTR(q->hs);
   if (!b) { set_error("buffer struct is NULL"); return MOE_ERR_INVALID_ARG; }
   MOE_PTR(b->x); MOE_PTR(b->w_r); MOE_PTR_OPT(b->bias); MOE_PTR_OPT(b->logits); MOE_PTR(b->idx);
   MOE_PTR(b->gates); MOE_PTR(b->cnt); MOE_PTR(b->off); MOE_PTR(b->slot); MOE_PTR(b->row_src);
-  MOE_PTR(b->cnt_re); MOE_PTR(b->rank_off); MOE_PTR(b->o); MOE_PTR(b->y);
-  if (save) { MOE_PTR(b->x_perm); MOE_PTR(b->a); MOE_PTR(b->h); }
+  MOE_PTR(b->cnt_re); MOE_PTR(b->rank_off); MOE_PTR32(b->o); MOE_PTR(b->y);
+  if (save) { MOE_PTR(b->x_perm); MOE_PTR32(b->a); MOE_PTR32(b->h); }
   MOE_CHECK(check_ws(*d, b->ws, b->ws_bytes));
   const WsLayout w = ws_layout(*d);
   char* ws = static_cast<char*>(b->ws);
@@ -166,17 +176,18 @@ moe_status_t moe_layer_backward_fp8(const moe_layer_desc_t* d, const moe_mb_bufs
                                     const moe_fp8_bufs_t* q, int32_t run_wgrad, void* stream) {
   MOE_CHECK(validate(d));
   MOE_CHECK(check_weights(q));
-  MOE_PTR(q->dq); MOE_PTR(q->ds); MOE_PTR(q->daq); MOE_PTR(q->das);
+  MOE_PTR(q->dq); MOE_PTR(q->ds); MOE_PTR32(q->daq); MOE_PTR(q->das);
   if (!b) { set_error("buffer struct is NULL"); return MOE_ERR_INVALID_ARG; }
   MOE_PTR(b->x); MOE_PTR(b->dy); MOE_PTR(b->w_r); MOE_PTR(b->idx); MOE_PTR(b->gates);
-  MOE_PTR(b->off); MOE_PTR(b->slot); MOE_PTR(b->row_src); MOE_PTR(b->a); MOE_PTR(b->o);
-  MOE_PTR(b->dgates); MOE_PTR(b->dx_perm); MOE_PTR(b->dx); MOE_PTR(b->dw_r);
+  MOE_PTR(b->off); MOE_PTR(b->slot); MOE_PTR(b->row_src); MOE_PTR32(b->a); MOE_PTR(b->o);
+  MOE_PTR(b->dgates); MOE_PTR32(b->dx_perm); MOE_PTR(b->dx); MOE_PTR(b->dw_r);
   if (run_wgrad) {  // the weight gradients are products of the bf16 rows
-    MOE_PTR(b->x_perm); MOE_PTR(b->h); MOE_PTR(b->d_o); MOE_PTR(b->da);
+    MOE_PTR(b->x_perm); MOE_PTR(b->h); MOE_PTR(b->d_o); MOE_PTR32(b->da);
     if (d->flags & MOE_FLAG_WGRAD_ACCUM_FP32) { MOE_PTR(b->main_dw1); MOE_PTR(b->main_dw2); }
     else { MOE_PTR(b->dw1); MOE_PTR(b->dw2); }
   } else {
-    MOE_PTR_OPT(b->d_o); MOE_PTR_OPT(b->da);
+    MOE_PTR_OPT(b->d_o);
+    if (b->da) MOE_PTR32(b->da);
   }
   MOE_CHECK(check_ws(*d, b->ws, b->ws_bytes));
   cudaStream_t st = S(stream);

@@ -4,7 +4,7 @@
 // scale for each 128 columns. All three are bound by HBM.
 #include <algorithm>
 
-#include "fp8.cuh"
+#include "fp8_mma.cuh"
 
 namespace moe {
 
@@ -339,4 +339,23 @@ moe_status_t launch_combine_bwd_fp8(const moe_layer_desc_t& d, const bf16* dy, c
   return launched(e, "combine_bwd_fp8_kernel");
 }
 
+namespace fp8 {
+
+namespace {
+
+// Clears the counters. A kernel rather than a memset, so that the chain's set-up
+// overlaps it (programmatic dependent launch).
+__global__ void __launch_bounds__(256) zero_counters_kernel(int* dep, int n) {
+  pdl_wait();
+  if ((int)threadIdx.x < n) dep[threadIdx.x] = 0;
+}
+
+}  // namespace
+
+cudaError_t launch_zero_counters(int* dep, int n, cudaStream_t st) {
+  LaunchScope _ls(K_FP8_ZERO, st);
+  return launch_k(zero_counters_kernel, 1, 256, 0, st, dep, n);
+}
+
+}  // namespace fp8
 }  // namespace moe

@@ -14,6 +14,7 @@
 //   warp 0      TMA producer of the operand ring: this CTA's 128 rows of A and its
 //               half of B, 128 bytes of K, 32 KB a stage, 6 stages
 //   warp 1      TMEM allocator + (even CTA) single-thread MMA issuer for the pair
+//   warp 2      counts first-GEMM tiles for their experts (below)
 //   warps 12..15 scales: each writes the scale bytes of four K blocks (the four
 //               bytes of a TMEM cell) into its 32 TMEM lanes (tcgen05.st), ahead of
 //               the MMA issuer. Copying them from shared memory (tcgen05.cp) in the
@@ -39,12 +40,12 @@
 // gate or up half) zero-fill it.
 #include <algorithm>
 #include <atomic>
-#include <mutex>
 
-#include "fp8.cuh"
-#include "sm100_ptx.cuh"
+#include "fp8_mma.cuh"
 
 namespace moe {
+
+using namespace fp8;
 
 namespace {
 
@@ -60,18 +61,15 @@ constexpr int kABytes = BM * BK, kBBytes = BN / 2 * BK;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kStages = 6;
 constexpr int kABoxRows = 16;                 // tiles of 64 rows or fewer load boxes of 16
-constexpr size_t kEpiStageBytes = 8 * 2048;
 constexpr int kTmemCols = 512;
 constexpr int kAccStep = 224;                 // second accumulator's first column
 constexpr int kTmemScales = 480;              // two buffers: 4 columns for A, 8 for B
 constexpr int kThreads = 512;
 // registers a thread: 128 at launch; the epilogue's two warpgroups take what the
-// control and scale warpgroups give up (2 * 56 + 2 * 192 <= 4 * 128)
-constexpr int kRegsControl = 56, kRegsEpilogue = 192;
+// control and scale warpgroups give up (2 * 72 + 2 * 184 = 4 * 128)
+constexpr int kRegsControl = 72, kRegsEpilogue = 184;
 constexpr int kMaxE = 256;
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
-constexpr size_t kDynSmem =
-    (size_t)kStages * kStageBytes + kEpiStageBytes + 1024;
+constexpr size_t kDynSmem = (size_t)kStages * kStageBytes + 1024;
 
 struct KParams {
   int E, H, F;
@@ -85,7 +83,7 @@ struct KParams {
   uint8_t* s;         // hs | das
   const bf16* aux;    // FC2 dgrad: the saved pre-activation
   int* status;
-  int* dep;           // per-expert count of first-GEMM epilogue warps done
+  int* dep;           // per-expert count of first-GEMM tiles stored, by CTA
 };
 
 template <int MODE>
@@ -111,6 +109,7 @@ struct SmemCtl {
   uint64_t full[kStages], empty[kStages];
   uint64_t sf_full[2], sf_empty[2];
   uint64_t tmem_full[2], tmem_empty[2], ovl, drain;
+  uint64_t stored[2], counted[2];  // a first-GEMM tile's stores issued; counted for its expert
   uint32_t tmem_base;
   int abort;
   int tstart[2][kMaxE + 1];  // tile prefixes of the two GEMMs
@@ -141,23 +140,7 @@ __device__ __forceinline__ void flag_timeout(SmemCtl& c, int* status, int where)
   atomicExch(status + ST_TIMEOUT, where);
 }
 
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&b);
-}
-
-// s(x) = 1 / (1 + e^-x): relative error near 1e-6 over the whole range
-__device__ __forceinline__ float sigmoid_f(float x) {
-  return __fdividef(1.f, 1.f + __expf(-x));
-}
-
 // ---------------------------------------------------------------- tcgen05, block-scaled
-// kind::mxf8f6f4 instruction descriptor: e4m3 operands (format 0), UE8M0 scales
-// (bit 23), fp32 D; bits 4-5 and 29-30 select the byte of the scale cells.
-__host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N, int b_mn) {
-  return ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
-         ((uint32_t)(M >> 4) << 24);
-}
 // The pair's MMA: A rows, the scales of A and D are each CTA's own, B's N rows
 // are half in each CTA, B's scales whole in both.
 __device__ __forceinline__ void umma_mxf8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -169,15 +152,6 @@ __device__ __forceinline__ void umma_mxf8_pair(uint32_t d, uint64_t a, uint64_t 
       "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
-}
-// This warp's 32 lanes x 4 and x 8 TMEM columns
-__device__ __forceinline__ void tmem_st_x4(uint32_t taddr, const uint32_t (&w)[4]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
-               "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-               : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 template <int REGS>
 __device__ __forceinline__ void regs_inc() {
@@ -197,62 +171,40 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
-// ---------------------------------------------------------------- stores
-// A warp's 32 rows x 64 bytes (thread i holds row i as four 16-byte chunks)
-// through its 2 KB buffer, so that each store covers 8 rows x 64 contiguous
-// bytes. Chunk c of row r sits at c ^ ((r >> 1) & 3): no bank conflicts. v[q] is
-// chunk q ^ flip.
-__device__ __forceinline__ void warp_store64(uint4* stage, const uint4 (&v)[4], uint8_t* base,
-                                             size_t pitch, int lane, int valid_rows,
-                                             bool cols_ok, int flip = 0) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) stage[lane * 4 + (q ^ flip ^ ((lane >> 1) & 3))] = v[q];
-  __syncwarp();
-  if (cols_ok) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = i * 8 + (lane >> 2), c = lane & 3;
-      if (row < valid_rows)
-        *reinterpret_cast<uint4*>(base + (size_t)row * pitch + c * 16) =
-            stage[row * 4 + (c ^ ((row >> 1) & 3))];
-    }
-  }
-  __syncwarp();
+// ---------------------------------------------------------------- loads and stores
+// A thread holds 32 consecutive columns of one row, so it moves whole 32-byte
+// sectors itself (256-bit accesses). A transposing pass through shared memory
+// would take bandwidth there from the operands: at the full MMA rate the tensor
+// core's reads (32 KB a stage) and TMA's writes (32 KB) already fill it.
+__device__ __forceinline__ void st_sector(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void ld_sector(const void* p, uint32_t* w) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                 "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
 }
 // 32 bf16 columns held as 16 packed words
-__device__ __forceinline__ void warp_store_words(uint4* stage, const uint32_t* w, bf16* base,
-                                                 size_t ld, int lane, int valid_rows,
-                                                 bool cols_ok) {
-  uint4 v[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) v[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-  warp_store64(stage, v, reinterpret_cast<uint8_t*>(base), ld * 2, lane, valid_rows, cols_ok);
+__device__ __forceinline__ void store_words(bf16* p, const uint32_t* w) {
+  st_sector(p, w);
+  st_sector(p + 16, w + 8);
 }
-// 64 bf16 columns (32 packed words) rounded to e4m3; the words of the 32 higher
-// columns come first when rev is set
-__device__ __forceinline__ void warp_store_fp8(uint4* stage, const uint32_t* w, float inv,
-                                               uint8_t* base, size_t ld, int lane, int valid_rows,
-                                               bool cols_ok, int rev) {
-  uint4 v[4];
+// 32 bf16 columns (16 packed words) rounded to e4m3
+__device__ __forceinline__ void store_fp8(uint8_t* p, const uint32_t* w, float inv) {
+  uint32_t v[8];
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
-    v[q] = make_uint4(fp8x4_of_bf16(w[8 * q], w[8 * q + 1], inv),
-                      fp8x4_of_bf16(w[8 * q + 2], w[8 * q + 3], inv),
-                      fp8x4_of_bf16(w[8 * q + 4], w[8 * q + 5], inv),
-                      fp8x4_of_bf16(w[8 * q + 6], w[8 * q + 7], inv));
-  warp_store64(stage, v, base, ld, lane, valid_rows, cols_ok, 2 * rev);
+  for (int q = 0; q < 8; ++q) v[q] = fp8x4_of_bf16(w[2 * q], w[2 * q + 1], inv);
+  st_sector(p, v);
 }
 
 // ================================================================ dependences
-__device__ __forceinline__ int ld_acquire(const int* p) {
-  int v;
-  asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
 // A second-GEMM tile of expert e: wait (bounded) until the expert's first-GEMM
 // tiles have all stored their output.
 __device__ __forceinline__ bool wait_expert(SmemCtl& c, const KParams& p, int e) {
-  const int target = 16 * (c.tstart[0][e + 1] - c.tstart[0][e]);  // 8 warps in each CTA
+  const int target = 2 * (c.tstart[0][e + 1] - c.tstart[0][e]);  // both CTAs of the pair
   if (ld_acquire(p.dep + e) < target) {
     const uint64_t t0 = ptx::globaltimer_ns();
     while (ld_acquire(p.dep + e) < target) {
@@ -415,15 +367,6 @@ struct MmaState {
   int stage = 0;
   uint32_t phase = 0, group = 0, tiles = 0;
 };
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
 template <int MODE>
 __device__ __forceinline__ bool mma_tile(SmemCtl& c, uint32_t smem, const KParams& p,
                                          uint32_t tmem, MmaState& m) {
@@ -495,22 +438,54 @@ __device__ __forceinline__ uint32_t pair_max(SmemCtl& c, uint32_t m, int ew, int
 // in falling order on the first accumulator (rev = 1) and in rising order on the
 // second; the warps that hold the shared chunk (hf == rev) release it as soon as
 // it is in registers.
+// Asks L2 for the pre-activations that this thread will read in tile t: their
+// HBM latency is the longest part of a chunk's work otherwise.
+__device__ __forceinline__ void prefetch_a(const KParams& p, const Tile& t, int ew, int lane) {
+  const int r = (ew & 3) * 32 + lane;
+  if (r >= t.rows) return;
+  const bf16* src = p.aux + ((size_t)t.row0 + t.m0 + r) * (2 * p.F);
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int f = t.n0 + 128 * half + 64 * (ew >> 2);  // 64 columns: one 128-byte line
+    if (f < p.F) {
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(src + f));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(src + p.F + f));
+    }
+  }
+}
+
 template <int MODE>
-__device__ __forceinline__ bool epilogue_tile(SmemCtl& c, uint8_t* stage_base, const KParams& p,
-                                              const Tile& t, uint32_t tmem, uint32_t rank,
-                                              uint32_t& tiles, int ew, int lane) {
+__device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const KParams& p, const Tile& t,
+                                              uint32_t tmem, uint32_t rank, uint32_t& tiles,
+                                              int ew, int lane) {
   const int q = ew & 3, hf = ew >> 2;
   const int acc = tiles & 1, rev = acc ^ 1;
-  uint4* stage = reinterpret_cast<uint4*>(stage_base) + ew * 128;
+  const size_t row = (size_t)t.row0 + t.m0 + q * 32 + lane;  // this thread's row
+  const bool rok = q * 32 + lane < t.rows;
+  // FC2 dgrad: 32 columns of the saved gate and up pre-activations
+  uint32_t ag[16], au[16];
+  auto load_a = [&](int cc) {
+    const int f = t.n0 + 32 * cc;
+    if (rok && f < p.F) {
+      const bf16* src = p.aux + row * (size_t)(2 * p.F) + f;
+      ld_sector(src, ag);
+      ld_sector(src + 16, ag + 8);
+      ld_sector(src + p.F, au);
+      ld_sector(src + p.F + 16, au + 8);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) ag[j] = au[j] = 0;
+    }
+  };
+  if (MODE == FC2_DGRAD) load_a(4 * rev + 2 * hf + rev);  // while the MMAs run
   if (!ptx::mbar_wait(&c.tmem_full[acc], (tiles >> 1) & 1, &c.abort, kWaitLimitNs)) {
     if (lane == 0) flag_timeout(c, p.status, 6);
     return false;
   }
+  __syncwarp();
   ptx::tc_fence_after();
   const uint32_t tbase = tmem + acc * kAccStep + ((uint32_t)(q * 32) << 16);
-  const size_t row0 = (size_t)t.row0 + t.m0 + q * 32;  // this warp's 32 rows
-  const int slab_rows = min(32, t.rows - q * 32);
-  if (slab_rows <= 0) {  // (both warps of the quarter)
+  if (q * 32 >= t.rows) {  // nothing to store (both warps of the quarter)
     if (hf == rev) release(&c.ovl, rank, lane);
     release(&c.tmem_empty[acc], rank, lane);
   } else if (MODE == FC1_FWD) {
@@ -538,21 +513,24 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, uint8_t* stage_base, c
         hw[16 * i + j] = h2;
         if (ok) mx = absmax_bf16x2(mx, h2);  // columns past F are not part of the block
       }
-      if (p.out0) {
-        bf16* abase = p.out0 + row0 * (size_t)(2 * p.F);
-        warp_store_words(stage, gw, abase + f, 2 * p.F, lane, slab_rows, ok);
-        warp_store_words(stage, uw, abase + p.F + f, 2 * p.F, lane, slab_rows, ok);
+      if (rok && ok) {
+        if (p.out0) {
+          bf16* a = p.out0 + row * (size_t)(2 * p.F) + f;
+          store_words(a, gw);
+          store_words(a + p.F, uw);
+        }
+        if (p.out1) store_words(p.out1 + row * (size_t)p.F + f, hw + 16 * i);
       }
-      if (p.out1)
-        warp_store_words(stage, hw + 16 * i, p.out1 + row0 * (size_t)p.F + f, p.F, lane, slab_rows,
-                         ok);
     }
     const uint32_t b = fp8_scale_byte(pair_max(c, absmax_bits(mx), ew, lane, acc));
+    const float inv = fp8_inv_scale(b);
     const int f = t.n0 + 64 * hf, fb = t.n0 / 128;
-    warp_store_fp8(stage, hw, fp8_inv_scale(b), p.q + row0 * (size_t)p.F + f, p.F, lane, slab_rows,
-                   f < p.F, rev);
-    if (hf == 0 && lane < slab_rows)
-      p.s[((size_t)(fb >> 2) * p.N + row0 + lane) * 4 + (fb & 3)] = (uint8_t)b;
+    if (rok && f < p.F) {
+      uint8_t* qp = p.q + row * (size_t)p.F + f;
+      store_fp8(qp + 32 * rev, hw, inv);
+      store_fp8(qp + 32 * (rev ^ 1), hw + 16, inv);
+    }
+    if (hf == 0 && rok) p.s[((size_t)(fb >> 2) * p.N + row) * 4 + (fb & 3)] = (uint8_t)b;
   } else if (MODE == FC2_DGRAD) {
     const int nf = (p.F + 127) / 128;
 #pragma unroll 1
@@ -566,77 +544,99 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, uint8_t* stage_base, c
         const bool ok = f < p.F;
         uint32_t v[32];
         ptx::tmem_ld_32x32b_x32(tbase + 32 * cc, v);
-        uint4 gc[4], uc[4];
-        const bool rok = ok && lane < slab_rows;
-        const uint4* src =
-            reinterpret_cast<const uint4*>(p.aux + (row0 + lane) * (size_t)(2 * p.F) + f);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          gc[j] = rok ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
-          uc[j] = rok ? __ldg(src + p.F / 8 + j) : make_uint4(0, 0, 0, 0);
-        }
         ptx::tmem_ld_wait(v);
         if (hi == 0 && i == 0 && hf == rev) release(&c.ovl, rank, lane);
         if (hi == 1 && i == 1) release(&c.tmem_empty[acc], rank, lane);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const uint32_t* gp = reinterpret_cast<const uint32_t*>(gc);
-          const uint32_t* up = reinterpret_cast<const uint32_t*>(uc);
           const float d0 = __uint_as_float(v[2 * j]), d1 = __uint_as_float(v[2 * j + 1]);
-          const float a0 = bf16_lo(gp[j]), a1 = bf16_hi(gp[j]);
+          const float a0 = bf16_lo(ag[j]), a1 = bf16_hi(ag[j]);
           const float s0 = sigmoid_f(a0), s1 = sigmoid_f(a1);
-          uw[16 * i + j] = pack_bf16x2(d0 * a0 * s0, d1 * a1 * s1);
-          gw[16 * i + j] = pack_bf16x2(d0 * bf16_lo(up[j]) * s0 * (1.f + a0 * (1.f - s0)),
-                                       d1 * bf16_hi(up[j]) * s1 * (1.f + a1 * (1.f - s1)));
+          const float e0 = d0 * s0, e1 = d1 * s1;
+          uw[16 * i + j] = pack_bf16x2(e0 * a0, e1 * a1);
+          gw[16 * i + j] = pack_bf16x2(e0 * bf16_lo(au[j]) * fmaf(a0, 1.f - s0, 1.f),
+                                       e1 * bf16_hi(au[j]) * fmaf(a1, 1.f - s1, 1.f));
           if (ok) {
             mu = absmax_bf16x2(mu, uw[16 * i + j]);
             mg = absmax_bf16x2(mg, gw[16 * i + j]);
           }
         }
-        if (p.out0) {
-          bf16* dbase = p.out0 + row0 * (size_t)(2 * p.F);
-          warp_store_words(stage, gw + 16 * i, dbase + f, 2 * p.F, lane, slab_rows, ok);
-          warp_store_words(stage, uw + 16 * i, dbase + p.F + f, 2 * p.F, lane, slab_rows, ok);
+        // the next chunk's, beside this one's stores
+        if (i == 0) load_a(4 * half + 2 * hf + (rev ^ 1));
+        else if (hi == 0) load_a(4 * (half ^ 1) + 2 * hf + rev);
+        if (p.out0 && rok && ok) {
+          bf16* da = p.out0 + row * (size_t)(2 * p.F) + f;
+          store_words(da, gw + 16 * i);
+          store_words(da + p.F, uw + 16 * i);
         }
       }
       const uint32_t bg = fp8_scale_byte(pair_max(c, absmax_bits(mg), ew, lane, 0));
       const uint32_t bu = fp8_scale_byte(pair_max(c, absmax_bits(mu), ew, lane, 1));
+      const float ig = fp8_inv_scale(bg), iu = fp8_inv_scale(bu);
       const int f = t.n0 + 128 * half + 64 * hf;
-      uint8_t* qbase = p.q + row0 * (size_t)(2 * p.F);
-      warp_store_fp8(stage, gw, fp8_inv_scale(bg), qbase + f, 2 * p.F, lane, slab_rows, f < p.F,
-                     rev);
-      warp_store_fp8(stage, uw, fp8_inv_scale(bu), qbase + p.F + f, 2 * p.F, lane, slab_rows,
-                     f < p.F, rev);
-      if (lane < slab_rows && t.n0 + 128 * half < p.F) {
+      if (rok && f < p.F) {
+        uint8_t* qp = p.q + row * (size_t)(2 * p.F) + f;
+        store_fp8(qp + 32 * rev, gw, ig);
+        store_fp8(qp + 32 * (rev ^ 1), gw + 16, ig);
+        store_fp8(qp + p.F + 32 * rev, uw, iu);
+        store_fp8(qp + p.F + 32 * (rev ^ 1), uw + 16, iu);
+      }
+      if (rok && t.n0 + 128 * half < p.F) {
         const int kb = hf * nf + t.n0 / 128 + half;  // the gate's byte or the up half's
-        p.s[((size_t)(kb >> 2) * p.N + row0 + lane) * 4 + (kb & 3)] = (uint8_t)(hf ? bu : bg);
+        p.s[((size_t)(kb >> 2) * p.N + row) * 4 + (kb & 3)] = (uint8_t)(hf ? bu : bg);
       }
     }
   } else {
-    // plain fp32 tile -> bf16
-    bf16* slab = p.out0 + row0 * (size_t)p.H + t.n0;
+    // plain fp32 tile -> bf16; the next chunk's TMEM load runs beside the stores
+    bf16* out = p.out0 + row * (size_t)p.H + t.n0;
+    auto chunk = [&](int i) {
+      const int ci = i ^ (3 * rev);
+      return (ci >> 1) * 4 + 2 * hf + (ci & 1);
+    };
+    uint32_t v[2][32];
+    ptx::tmem_ld_32x32b_x32(tbase + 32 * chunk(0), v[0]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int ci = i ^ (3 * rev);
-      const int cc = (ci >> 1) * 4 + 2 * hf + (ci & 1);
-      uint32_t v[32];
-      ptx::tmem_ld_32x32b_x32(tbase + 32 * cc, v);
-      ptx::tmem_ld_wait(v);
+      ptx::tmem_ld_wait(v[i & 1]);
       if (i == 0 && hf == rev) release(&c.ovl, rank, lane);
       if (i == 3) release(&c.tmem_empty[acc], rank, lane);
+      if (i < 3) ptx::tmem_ld_32x32b_x32(tbase + 32 * chunk(i + 1), v[(i + 1) & 1]);
+      const int cc = chunk(i);
       uint32_t w[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j)
-        w[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-      warp_store_words(stage, w, slab + 32 * cc, p.H, lane, slab_rows, t.n0 + 32 * cc < p.H);
+        w[j] = pack_bf16x2(__uint_as_float(v[i & 1][2 * j]), __uint_as_float(v[i & 1][2 * j + 1]));
+      if (rok && t.n0 + 32 * cc < p.H) store_words(out + 32 * cc, w);
     }
   }
   if (Mode<MODE>::kFirst) {
-    // this warp's part of the tile is stored: visible before the counter moves
-    __threadfence();
+    // hand the tile to the counting warp, which has counted the one before last
     __syncwarp();
-    if (lane == 0) atomicAdd(p.dep + t.e, 1);
+    if (lane == 0) {
+      if (!ptx::mbar_wait(&c.counted[acc], ((tiles >> 1) & 1) ^ 1, &c.abort, kWaitLimitNs))
+        flag_timeout(c, p.status, 7);
+      ptx::mbar_arrive(&c.stored[acc]);
+    }
+    __syncwarp();
   }
+  ++tiles;
+  return true;
+}
+
+// ================================================================ counting
+// Counts a first-GEMM tile for its expert once the epilogue's stores are visible
+// device-wide: the fence takes 3000 to 4000 clocks with stores in flight, which
+// the epilogue warps spend on the next tile. (Their stores are ordered before
+// their arrivals, the arrivals before this fence, the fence before the count.)
+__device__ __forceinline__ bool count_tile(SmemCtl& c, const KParams& p, int e, uint32_t& tiles) {
+  const int acc = tiles & 1;
+  if (!ptx::mbar_wait(&c.stored[acc], (tiles >> 1) & 1, &c.abort, kWaitLimitNs)) {
+    flag_timeout(c, p.status, 8);
+    return false;
+  }
+  __threadfence();
+  atomicAdd(p.dep + e, 1);
+  ptx::mbar_arrive(&c.counted[acc]);
   ++tiles;
   return true;
 }
@@ -654,7 +654,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ SmemCtl ctl;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) &
                                              ~uintptr_t(1023));
-  uint8_t* stage_base = smem + kStages * kStageBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = p1.E;
   if (threadIdx.x == 0) {
@@ -665,6 +664,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(&ctl.sf_full[a], 8);  // both CTAs' scale warps
       ptx::mbar_init(&ctl.sf_empty[a], 1);
+      ptx::mbar_init(&ctl.stored[a], 8);  // this CTA's epilogue warps
+      ptx::mbar_init(&ctl.counted[a], 1);
       ptx::mbar_init(&ctl.tmem_full[a], 1);
       ptx::mbar_init(&ctl.tmem_empty[a], 16);  // both CTAs' epilogue warps
     }
@@ -734,6 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             stage, phase)
                         : producer_tile<M2>(ctl, smem, p2, &tmA2, &tmS2, &tmB2, tile2(i), rank,
                                             stage, phase);
+      if (!ok && rank == 0) drain_loads<kStages>(ctl.full, stage, phase);  // both CTAs' loads
     } else if (warp == 1 && rank == 0) {
       MmaState m;
       bool ok = true;
@@ -748,15 +750,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_wait(&ctl.drain, 0, &dummy, kWaitLimitNs);
       }
     }
+    else if (warp == 2 && lane == 0) {
+      uint32_t tiles = 0;
+      bool ok = true;
+      for (int i = first; ok && i < total1; i += stride) ok = count_tile(ctl, p1, tile1(i).e, tiles);
+    }
     __syncwarp();
   } else if (warp < 12) {
     regs_inc<kRegsEpilogue>();
     uint32_t tiles = 0;
     bool ok = true;
-    for (int i = first; ok && i < total; i += stride)
-      ok = i < total1
-               ? epilogue_tile<M1>(ctl, stage_base, p1, tile1(i), tmem, rank, tiles, warp - 4, lane)
-               : epilogue_tile<M2>(ctl, stage_base, p2, tile2(i), tmem, rank, tiles, warp - 4, lane);
+    for (int i = first; ok && i < total; i += stride) {
+      if (i < total1) {
+        const Tile t = tile1(i);
+        if (M1 == FC2_DGRAD && i + stride < total1)
+          prefetch_a(p1, tile1(i + stride), warp - 4, lane);
+        ok = epilogue_tile<M1>(ctl, p1, t, tmem, rank, tiles, warp - 4, lane);
+      } else {
+        ok = epilogue_tile<M2>(ctl, p2, tile2(i), tmem, rank, tiles, warp - 4, lane);
+      }
+    }
   } else {
     regs_dec<kRegsControl>();
     uint32_t group = 0;
@@ -773,49 +786,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ host side
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  });
-  return fn;
-}
-
-// Load map of e4m3 bytes, up to three dimensions (innermost first), boxes of
-// 128 bytes x box1 x box2, 128-byte swizzle; what lies outside reads as zero.
-bool make_map(CUtensorMap* m, const void* base, int dims, long long d0, long long d1, long long d2,
-              int box1, int box2) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) {
-    set_error("cuTensorMapEncodeTiled is not available from the driver");
-    return false;
-  }
-  cuuint64_t dim[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
-  cuuint64_t strides[2] = {(cuuint64_t)d0, (cuuint64_t)(d0 * d1)};
-  cuuint32_t box[3] = {128, (cuuint32_t)box1, (cuuint32_t)box2};
-  cuuint32_t es[3] = {1, 1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, dims, const_cast<void*>(base), dim, strides,
-                   box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) {
-    set_error("cuTensorMapEncodeTiled failed (%d) for a %lld x %lld x %lld map", (int)r, d2, d1,
-              d0);
-    return false;
-  }
-  return true;
-}
-
 // How many pairs can be resident at once on the current device, after setting
 // the kernel's shared memory up there (once for each device).
 template <int M1, int M2>
@@ -849,8 +819,7 @@ moe_status_t launch_chain(const moe_layer_desc_t& d, const CUtensorMap (&m)[6], 
                           const KParams& p2, int kernel_id, bool counters_zeroed, cudaStream_t st) {
   int pairs = 0;
   cudaError_t e = resident_pairs<M1, M2>(&pairs);
-  if (e == cudaSuccess && !counters_zeroed)
-    e = cudaMemsetAsync(p1.dep, 0, (size_t)d.E * sizeof(int), st);
+  if (e == cudaSuccess && !counters_zeroed) e = launch_zero_counters(p1.dep, d.E, st);
   if (e != cudaSuccess) {
     set_error("grouped_gemm_fp8_kernel set-up: %s", cudaGetErrorString(e));
     return MOE_ERR_CUDA;
@@ -904,6 +873,9 @@ moe_status_t launch_ffn_fwd_fp8(const moe_layer_desc_t& d, const uint8_t* xq, co
                                 cudaStream_t st, bool counters_zeroed) {
   const long long N = (long long)d.T * d.k;
   if (N == 0) return MOE_OK;
+  if (N <= kFp8FewRows * d.E)
+    return launch_ffn_rows_fp8(d, xq, xs, off, w, a, h, hq, hs, o, status, dep, st,
+                               counters_zeroed);
   CUtensorMap m[6];
   if (!make_map(&m[0], xq, 2, d.H, N, 1, BM, 1) || !make_map(&m[1], xq, 2, d.H, N, 1, kABoxRows, 1) ||
       !make_map(&m[2], w.w1q, 2, d.H, 2ll * d.E * d.F, 1, 128, 1) ||

@@ -18,7 +18,7 @@ const char* const kNames[K_ALL] = {
     "gemm_fc1_dgrad", "gemm_wgrad_w1", "gemm_wgrad_w2", "dispatch_bwd", "gemm_ffn_fwd",
     "gemm_ffn_dgrad", "dispatch_fused", "gemm_wgrad_w1_accum", "gemm_wgrad_w2_accum",
     "layout_scan", "ep_resort", "gemm_wgrad", "fp8_quantize_weights", "fp8_permute",
-    "fp8_combine_bwd", "fp8_gemm_ffn_fwd", "fp8_gemm_ffn_dgrad"};
+    "fp8_combine_bwd", "fp8_gemm_ffn_fwd", "fp8_gemm_ffn_dgrad", "fp8_zero_counters", "fp8_rows_ffn"};
 
 std::atomic<unsigned long long> g_launches{0};
 
