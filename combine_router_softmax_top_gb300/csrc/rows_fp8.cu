@@ -40,7 +40,7 @@ constexpr int kAccCols = 2 * NT;              // TMEM columns of one accumulator
 constexpr int kTmemScales = 2 * kAccCols;     // two buffers of 12: two M tiles, the rows
 constexpr int kTmemCols = 256;
 constexpr int kSmallBox = 8;                  // rows of the small TMA box
-static_assert(16 * kMaxE < 65536 && (16 * kMaxE / NT + kMaxE) * 128 < 65536, "16-bit tables");
+static_assert(kFp8FewRows * kMaxE < 65536, "16-bit tables");
 constexpr size_t kDynSmem = (size_t)kStages * kStageBytes + 1024;
 
 struct RowsParams {
@@ -66,7 +66,7 @@ struct SmemCtl {
   uint64_t sf_full[2], sf_empty[2], tmem_full[2], tmem_empty[2], drain;
   uint32_t tmem_base;
   int abort;
-  uint16_t tstart[2][kMaxE + 1];  // at most (N / 32 + E) * 128 tiles, N <= 16 E, E <= 256
+  uint16_t rtile[kMaxE + 1];      // first row tile of each expert
   uint16_t off[kMaxE + 1];
   uint16_t amax[4][NT];           // block maxima of each warp's columns, as bf16 bits
   uint4 h[NT][16];    // the tile's h, bf16 [row][128]
@@ -83,11 +83,12 @@ __device__ __forceinline__ int ncols(const RowsParams& p) {  // column blocks of
 
 template <int G>
 __device__ __forceinline__ Tile tile_at(const RowsParams& p, const SmemCtl& c, int i, int& cursor) {
-  while (c.tstart[G][cursor + 1] <= i) ++cursor;
+  const int nc = ncols<G>(p);
+  while (c.rtile[cursor + 1] * nc <= i) ++cursor;
   Tile t;
   t.e = cursor;
   const int cnt = c.off[cursor + 1] - c.off[cursor];
-  const int local = i - c.tstart[G][cursor], nt = (cnt + NT - 1) / NT;
+  const int local = i - c.rtile[cursor] * nc, nt = (cnt + NT - 1) / NT;
   const int r = (local % nt) * NT;  // row tiles fastest: they share the weights
   t.n0 = (local / nt) * (G == kFc1 ? 128 : 256);
   t.row = (long long)c.off[cursor] + r;
@@ -101,7 +102,7 @@ __device__ __forceinline__ void flag_timeout(SmemCtl& c, int* status, int where)
 }
 
 __device__ __forceinline__ bool wait_expert(SmemCtl& c, const RowsParams& p, int e) {
-  const int target = c.tstart[0][e + 1] - c.tstart[0][e];
+  const int target = (c.rtile[e + 1] - c.rtile[e]) * ncols<kFc1>(p);
   if (ld_acquire(p.dep + e) < target) {
     const uint64_t t0 = ptx::globaltimer_ns();
     while (ld_acquire(p.dep + e) < target) {
@@ -396,32 +397,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int e = threadIdx.x; e <= p.E; e += blockDim.x)
     ctl.off[e] = (uint16_t)min(max((long long)p.off[e], 0ll), p.N);
   __syncthreads();
-  if (warp < 2) {  // tiles per expert -> exclusive prefix, one warp for each product
-    const int nc = warp == 0 ? ncols<kFc1>(p) : ncols<kFc2>(p);
+  if (warp == 0) {  // row tiles of the experts -> exclusive prefix
     int carry = 0;
     for (int base = 0; base < p.E; base += 32) {
       const int e = base + lane;
-      int n = 0;
-      if (e < p.E) {
-        const int cnt = ctl.off[e + 1] - ctl.off[e];
-        n = cnt > 0 ? (cnt + NT - 1) / NT * nc : 0;
-      }
+      const int n = e < p.E ? max(0, (ctl.off[e + 1] - ctl.off[e] + NT - 1) / NT) : 0;
       int incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
       }
-      if (e < p.E) ctl.tstart[warp][e] = (uint16_t)(carry + incl - n);
+      if (e < p.E) ctl.rtile[e] = (uint16_t)(carry + incl - n);
       carry += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) ctl.tstart[warp][p.E] = (uint16_t)carry;
+    if (lane == 0) ctl.rtile[p.E] = (uint16_t)carry;
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
-  const int total1 = ctl.tstart[0][p.E], total = total1 + ctl.tstart[1][p.E];
+  const int total1 = ctl.rtile[p.E] * ncols<kFc1>(p);
+  const int total = total1 + ctl.rtile[p.E] * ncols<kFc2>(p);
   int cur1 = 0, cur2 = 0;
   auto tile1 = [&](int i) { return tile_at<kFc1>(p, ctl, i, cur1); };
   auto tile2 = [&](int i) { return tile_at<kFc2>(p, ctl, i - total1, cur2); };
