@@ -28,10 +28,14 @@
 // CTAs are resident and meet their first tiles before any second, so the waits
 // end.
 //
-// TMEM: two 256-column accumulators and two buffers of 12 scale columns do not
-// fit 512 columns, so the accumulators share 32: columns 0..255 and 224..479.
+// TMEM: two 256-column accumulators and four buffers of 12 scale columns do not
+// fit 512 columns, so the accumulators share 64: columns 0..255 and 192..447.
 // The epilogue reads the shared columns first and releases them (ovl), so the
-// next tile's MMAs start while it works on the rest.
+// next tile's MMAs start while it works on the rest. (Two scale buffers would
+// need only 32 shared columns, but a buffer's turn-around through both CTAs -
+// MMAs done, scale warps, MMA issuer - takes 2000 clocks and more, as long as
+// the four K blocks of the other buffer: the K loop ran at 595 clocks a block
+// instead of 512.)
 //
 // Ragged groups as in the bf16 GEMMs: expert e owns rows off[e]..off[e+1]-1; a
 // tile's rows past the expert's end are computed on whatever TMA loaded and
@@ -62,8 +66,9 @@ constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kStages = 6;
 constexpr int kABoxRows = 16;                 // tiles of 64 rows or fewer load boxes of 16
 constexpr int kTmemCols = 512;
-constexpr int kAccStep = 224;                 // second accumulator's first column
-constexpr int kTmemScales = 480;              // two buffers: 4 columns for A, 8 for B
+constexpr int kAccStep = 192;                 // second accumulator's first column
+constexpr int kTmemScales = 448;              // buffers of 4 columns for A, 8 for B
+constexpr int kSf = 4;                        // scale buffers
 constexpr int kThreads = 512;
 // registers a thread: 128 at launch; the epilogue's two warpgroups take what the
 // control and scale warpgroups give up (2 * 72 + 2 * 184 = 4 * 128)
@@ -107,7 +112,7 @@ struct Tile {
 
 struct SmemCtl {
   uint64_t full[kStages], empty[kStages];
-  uint64_t sf_full[2], sf_empty[2];
+  uint64_t sf_full[kSf], sf_empty[kSf];
   uint64_t tmem_full[2], tmem_empty[2], ovl, drain;
   uint64_t stored[2], counted[2];  // a first-GEMM tile's stores issued; counted for its expert
   uint32_t tmem_base;
@@ -288,13 +293,19 @@ __device__ __forceinline__ bool producer_tile(SmemCtl& c, uint8_t* smem, const K
 }
 
 // ================================================================ scales
+// What these arrivals order are TMEM accesses, complete when their waits return:
+// no earlier memory operation needs to be released to the other CTA.
+__device__ __forceinline__ void arrive_remote(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
+               : "memory");
+}
 // One arrival on the even CTA's barrier, after this warp's TMEM accesses.
 __device__ __forceinline__ void release(uint64_t* bar, uint32_t rank, int lane) {
   ptx::tc_fence_before();
   __syncwarp();
   if (lane == 0) {
     if (rank == 0) ptx::mbar_arrive(bar);
-    else ptx::mbar_arrive_cluster(ptx::mapa_shared(bar, 0));
+    else arrive_remote(ptx::mapa_shared(bar, 0));
   }
 }
 
@@ -342,8 +353,8 @@ __device__ __forceinline__ bool scales_tile(SmemCtl& c, const KParams& p, const 
     uint32_t wb[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i) wb[i >> 2] |= __shfl_sync(0xffffffffu, b, i) << (8 * (i & 3));
-    const int buf = group & 1;
-    if (!ptx::mbar_wait(&c.sf_empty[buf], ((group >> 1) & 1) ^ 1, &c.abort, kWaitLimitNs)) {
+    const int buf = group % kSf;
+    if (!ptx::mbar_wait(&c.sf_empty[buf], ((group / kSf) & 1) ^ 1, &c.abort, kWaitLimitNs)) {
       if (lane == 0) flag_timeout(c, p.status, 2);
       return false;
     }
@@ -382,21 +393,26 @@ __device__ __forceinline__ bool mma_tile(SmemCtl& c, uint32_t smem, const KParam
     flag_timeout(c, p.status, where);
     return false;
   };
-  // this accumulator free (two tiles ago), and the columns it shares with the
-  // other one read by the previous tile's epilogue
+  // the first stage and scales, then this accumulator (free since the tile before
+  // the last), and last the columns it shares with the previous tile's, which come
+  // free last: only they delay the first MMA
+  if (!wait(&c.sf_full[m.group % kSf], (m.group / kSf) & 1, 4)) return false;
+  if (!wait(&c.full[m.stage], m.phase, 5)) return false;
   if (!wait(&c.tmem_empty[acc], ((m.tiles >> 1) & 1) ^ 1, 3)) return false;
   if (m.tiles > 0 && !wait(&c.ovl, (m.tiles - 1) & 1, 3)) return false;
   ptx::tc_fence_after();
   const uint32_t d = tmem + acc * kAccStep;
   for (int k0 = 0; k0 < nk; k0 += 4) {  // four K blocks: one buffer of scales
-    const int buf = m.group & 1;
-    if (!wait(&c.sf_full[buf], (m.group >> 1) & 1, 4)) return false;
+    const int buf = m.group % kSf;
+    if (k0 && !wait(&c.sf_full[buf], (m.group / kSf) & 1, 4)) return false;
     const uint32_t sfa = tmem + kTmemScales + buf * 12;
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
       if (k0 + kb >= nk) break;
-      if (!wait(&c.full[m.stage], m.phase, 5)) return false;
-      ptx::tc_fence_after();
+      if (k0 + kb) {
+        if (!wait(&c.full[m.stage], m.phase, 5)) return false;
+        ptx::tc_fence_after();
+      }
       const uint64_t adesc = desc0 | ((smem + m.stage * kStageBytes) >> 4);
       const uint64_t bdesc = adesc + (kABytes >> 4);
       constexpr uint32_t kSel = (1u << 4) | (1u << 29);  // scale byte kb of both operands
@@ -433,11 +449,11 @@ __device__ __forceinline__ uint32_t pair_max(SmemCtl& c, uint32_t m, int ew, int
   return max(m, c.amax[buf][ew ^ 4][lane]);
 }
 
-// The columns that the two accumulators share are the first one's last 32 and
-// the second one's first 32. An epilogue therefore takes its 32-column chunks
+// The columns that the two accumulators share are the first one's last 64 and
+// the second one's first 64. An epilogue therefore takes its 32-column chunks
 // in falling order on the first accumulator (rev = 1) and in rising order on the
-// second; the warps that hold the shared chunk (hf == rev) release it as soon as
-// it is in registers.
+// second; the warps that hold the shared chunks (hf == rev) release them as soon
+// as both are in registers.
 // Asks L2 for the pre-activations that this thread will read in tile t: their
 // HBM latency is the longest part of a chunk's work otherwise.
 __device__ __forceinline__ void prefetch_a(const KParams& p, const Tile& t, int ew, int lane) {
@@ -490,23 +506,30 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const KParams& p, cons
     release(&c.tmem_empty[acc], rank, lane);
   } else if (MODE == FC1_FWD) {
     // columns 0..127 gate, 128..255 up of one 128-wide block of h
+    // (the shared columns: up 64..127 of the first accumulator, gate 0..63 of the second)
     uint32_t hw[32];
     uint32_t mx = 0;
+    uint32_t s0[32], s1[32], g[32];
+    const uint32_t sbase = tbase + 128 * rev + 64 * hf, obase = tbase + 128 * (rev ^ 1) + 64 * hf;
+    ptx::tmem_ld_32x32b_x32(sbase + 32 * rev, s0);
+    ptx::tmem_ld_32x32b_x32(sbase + 32 * (rev ^ 1), s1);
+    ptx::tmem_ld_wait(s0, s1);
+    if (hf == rev) release(&c.ovl, rank, lane);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int cc = 2 * hf + (i ^ rev), f = t.n0 + 32 * cc;
       const bool ok = f < p.F;
-      uint32_t g[32], u[32];
-      ptx::tmem_ld_32x32b_x32(tbase + 32 * cc, g);
-      ptx::tmem_ld_32x32b_x32(tbase + 128 + 32 * cc, u);
-      ptx::tmem_ld_wait(g, u);
-      if (i == 0 && hf == rev) release(&c.ovl, rank, lane);
+      uint32_t(&sh)[32] = i ? s1 : s0;
+      ptx::tmem_ld_32x32b_x32(obase + 32 * (i ^ rev), g);
+      ptx::tmem_ld_wait(g);
       if (i == 1) release(&c.tmem_empty[acc], rank, lane);
       uint32_t gw[16], uw[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        gw[j] = pack_bf16x2(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1]));
-        uw[j] = pack_bf16x2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+        const uint32_t ws = pack_bf16x2(__uint_as_float(sh[2 * j]), __uint_as_float(sh[2 * j + 1]));
+        const uint32_t wo = pack_bf16x2(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1]));
+        gw[j] = rev ? wo : ws;
+        uw[j] = rev ? ws : wo;
         const float g0 = bf16_lo(gw[j]), g1 = bf16_hi(gw[j]);
         const uint32_t h2 = pack_bf16x2(g0 * sigmoid_f(g0) * bf16_lo(uw[j]),
                                         g1 * sigmoid_f(g1) * bf16_hi(uw[j]));
@@ -533,23 +556,25 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const KParams& p, cons
     if (hf == 0 && rok) p.s[((size_t)(fb >> 2) * p.N + row) * 4 + (fb & 3)] = (uint8_t)b;
   } else if (MODE == FC2_DGRAD) {
     const int nf = (p.F + 127) / 128;
+    uint32_t v[2][32];  // both chunks of the half: the first half's may be the shared columns
 #pragma unroll 1
     for (int hi = 0; hi < 2; ++hi) {  // 128 columns: one block of da_gate, one of da_up
       const int half = hi ^ rev;
       uint32_t gw[32], uw[32];
       uint32_t mg = 0, mu = 0;
+      const uint32_t vbase = tbase + 128 * half + 64 * hf;
+      ptx::tmem_ld_32x32b_x32(vbase + 32 * rev, v[0]);
+      ptx::tmem_ld_32x32b_x32(vbase + 32 * (rev ^ 1), v[1]);
+      ptx::tmem_ld_wait(v[0], v[1]);
+      if (hi == 0 && hf == rev) release(&c.ovl, rank, lane);
+      if (hi == 1) release(&c.tmem_empty[acc], rank, lane);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int cc = 4 * half + 2 * hf + (i ^ rev), f = t.n0 + 32 * cc;
         const bool ok = f < p.F;
-        uint32_t v[32];
-        ptx::tmem_ld_32x32b_x32(tbase + 32 * cc, v);
-        ptx::tmem_ld_wait(v);
-        if (hi == 0 && i == 0 && hf == rev) release(&c.ovl, rank, lane);
-        if (hi == 1 && i == 1) release(&c.tmem_empty[acc], rank, lane);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const float d0 = __uint_as_float(v[2 * j]), d1 = __uint_as_float(v[2 * j + 1]);
+          const float d0 = __uint_as_float(v[i][2 * j]), d1 = __uint_as_float(v[i][2 * j + 1]);
           const float a0 = bf16_lo(ag[j]), a1 = bf16_hi(ag[j]);
           const float s0 = sigmoid_f(a0), s1 = sigmoid_f(a1);
           const float e0 = d0 * s0, e1 = d1 * s1;
@@ -595,17 +620,21 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const KParams& p, cons
     };
     uint32_t v[2][32];
     ptx::tmem_ld_32x32b_x32(tbase + 32 * chunk(0), v[0]);
+    ptx::tmem_ld_32x32b_x32(tbase + 32 * chunk(1), v[1]);
+    ptx::tmem_ld_wait(v[0], v[1]);
+    if (hf == rev) release(&c.ovl, rank, lane);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      ptx::tmem_ld_wait(v[i & 1]);
-      if (i == 0 && hf == rev) release(&c.ovl, rank, lane);
-      if (i == 3) release(&c.tmem_empty[acc], rank, lane);
-      if (i < 3) ptx::tmem_ld_32x32b_x32(tbase + 32 * chunk(i + 1), v[(i + 1) & 1]);
+      if (i == 2) {
+        ptx::tmem_ld_wait(v[0], v[1]);
+        release(&c.tmem_empty[acc], rank, lane);
+      }
       const int cc = chunk(i);
       uint32_t w[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j)
         w[j] = pack_bf16x2(__uint_as_float(v[i & 1][2 * j]), __uint_as_float(v[i & 1][2 * j + 1]));
+      if (i < 2) ptx::tmem_ld_32x32b_x32(tbase + 32 * chunk(i + 2), v[i]);
       if (rok && t.n0 + 32 * cc < p.H) store_words(out + 32 * cc, w);
     }
   }
@@ -661,9 +690,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&ctl.full[s], 1);
       ptx::mbar_init(&ctl.empty[s], 1);
     }
+    for (int b = 0; b < kSf; ++b) {
+      ptx::mbar_init(&ctl.sf_full[b], 8);  // both CTAs' scale warps
+      ptx::mbar_init(&ctl.sf_empty[b], 1);
+    }
     for (int a = 0; a < 2; ++a) {
-      ptx::mbar_init(&ctl.sf_full[a], 8);  // both CTAs' scale warps
-      ptx::mbar_init(&ctl.sf_empty[a], 1);
       ptx::mbar_init(&ctl.stored[a], 8);  // this CTA's epilogue warps
       ptx::mbar_init(&ctl.counted[a], 1);
       ptx::mbar_init(&ctl.tmem_full[a], 1);
