@@ -88,7 +88,7 @@ __device__ __forceinline__ int ld_acquire(const int* p) {
 // landed, so that none writes into shared memory that is no longer this
 // kernel's. stage, phase: the producer's place in the ring.
 template <int STAGES>
-__device__ __forceinline__ void drain_loads(uint64_t (&full)[STAGES], int stage, uint32_t phase) {
+__device__ __forceinline__ void drain_loads(uint64_t* full, int stage, uint32_t phase) {
   int none = 0;
   for (int s = 0; s < STAGES; ++s)
     ptx::mbar_wait(&full[s], s < stage ? phase : phase ^ 1, &none, kWaitLimitNs / STAGES);
@@ -133,6 +133,28 @@ inline bool make_map(CUtensorMap* m, const void* base, int dims, long long d0, l
   if (r != CUDA_SUCCESS) {
     set_error("cuTensorMapEncodeTiled failed (%d) for a %lld x %lld x %lld map", (int)r, d2, d1,
               d0);
+    return false;
+  }
+  return true;
+}
+
+// Map of bf16 rows [rows, cols] in boxes of 32 columns x box_rows, 64-byte swizzle.
+inline bool make_rows_map(CUtensorMap* m, const void* base, long long rows, long long cols,
+                          int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) {
+    set_error("cuTensorMapEncodeTiled is not available from the driver");
+    return false;
+  }
+  cuuint64_t dim[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+  cuuint32_t box[2] = {32, (cuuint32_t)box_rows};
+  cuuint32_t es[2] = {1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dim, strides,
+                   box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    set_error("cuTensorMapEncodeTiled failed (%d) for a %lld x %lld map", (int)r, rows, cols);
     return false;
   }
   return true;

@@ -15,6 +15,7 @@
 //               half of B, 128 bytes of K, 32 KB a stage, 6 stages
 //   warp 1      TMEM allocator + (even CTA) single-thread MMA issuer for the pair
 //   warp 2      counts first-GEMM tiles for their experts (below)
+//   warp 3      gradient: loads the saved pre-activations for the epilogue
 //   warps 12..15 scales: each writes the scale bytes of four K blocks (the four
 //               bytes of a TMEM cell) into its 32 TMEM lanes (tcgen05.st), ahead of
 //               the MMA issuer. Copying them from shared memory (tcgen05.cp) in the
@@ -63,7 +64,9 @@ enum Fp8Mode {
 constexpr int BM = 128, BN = 256, BK = 128;   // BM: rows of one CTA of the pair
 constexpr int kABytes = BM * BK, kBBytes = BN / 2 * BK;
 constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kStages = 6;
+constexpr int kStagesMax = 6;
+constexpr int kAuxBytes = 4 * 8192;           // gate and up of both 32-column steps, 128 rows
+constexpr int kEpiBytes = 8 * 2048;           // a 32 x 32 bf16 box for each epilogue warp
 constexpr int kABoxRows = 16;                 // tiles of 64 rows or fewer load boxes of 16
 constexpr int kTmemCols = 512;
 constexpr int kAccStep = 192;                 // second accumulator's first column
@@ -74,7 +77,23 @@ constexpr int kThreads = 512;
 // control and scale warpgroups give up (2 * 72 + 2 * 184 = 4 * 128)
 constexpr int kRegsControl = 72, kRegsEpilogue = 184;
 constexpr int kMaxE = 256;
-constexpr size_t kDynSmem = (size_t)kStages * kStageBytes + 1024;
+
+// Launch-wide constants: the gradient chain gives one operand stage up for the
+// saved pre-activations of its first GEMM.
+template <int M1>
+struct Chain {
+  static constexpr bool kAux = M1 == 2;
+  static constexpr int kStages = kAux ? 5 : 6;
+  static constexpr int kAuxAt = kStages * kStageBytes;
+  static constexpr int kEpiAt = kAuxAt + (kAux ? kAuxBytes : 0);
+  static constexpr size_t kDynSmem = kEpiAt + kEpiBytes + 1024;
+};
+
+struct Maps {
+  CUtensorMap a1, s1, b1, a2, s2, b2;  // operands: A, A in small boxes, B of both GEMMs
+  CUtensorMap o1, o2, o3;              // a | da, h, o | dx_perm
+  CUtensorMap aux;                     // the saved pre-activation
+};
 
 struct KParams {
   int E, H, F;
@@ -86,7 +105,6 @@ struct KParams {
   bf16* out1;         // h (may be NULL)
   uint8_t* q;         // hq | daq
   uint8_t* s;         // hs | das
-  const bf16* aux;    // FC2 dgrad: the saved pre-activation
   int* status;
   int* dep;           // per-expert count of first-GEMM tiles stored, by CTA
 };
@@ -111,7 +129,8 @@ struct Tile {
 };
 
 struct SmemCtl {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[kStagesMax], empty[kStagesMax];
+  uint64_t aux_full, aux_empty;
   uint64_t sf_full[kSf], sf_empty[kSf];
   uint64_t tmem_full[2], tmem_empty[2], ovl, drain;
   uint64_t stored[2], counted[2];  // a first-GEMM tile's stores issued; counted for its expert
@@ -176,26 +195,41 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
-// ---------------------------------------------------------------- loads and stores
-// A thread holds 32 consecutive columns of one row, so it moves whole 32-byte
-// sectors itself (256-bit accesses). A transposing pass through shared memory
-// would take bandwidth there from the operands: at the full MMA rate the tensor
-// core's reads (32 KB a stage) and TMA's writes (32 KB) already fill it.
+// ---------------------------------------------------------------- stores
+// 32 rows (thread i holds row i) x 32 bf16 columns (16 packed words). Whole boxes
+// leave through this warp's 2 KB buffer as one TMA store, in whole lines; a box
+// that ends with the expert's rows is written by its threads, a 32-byte sector at
+// a time (256-bit stores): slower, as every sector is a request of its own (the
+// gradient's epilogue takes 31000 clocks a tile that way, 18000 without stores).
 __device__ __forceinline__ void st_sector(void* p, const uint32_t* w) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
                "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
-__device__ __forceinline__ void ld_sector(const void* p, uint32_t* w) {
-  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
-                 "=r"(w[6]), "=r"(w[7])
-               : "l"(p));
-}
-// 32 bf16 columns held as 16 packed words
-__device__ __forceinline__ void store_words(bf16* p, const uint32_t* w) {
-  st_sector(p, w);
-  st_sector(p + 16, w + 8);
+struct Out {       // one warp's slab of an output
+  uint4* buf;      // its shared buffer
+  int lane, rows;  // valid rows of the slab
+};
+__device__ __forceinline__ void store_box(const Out& o, const CUtensorMap* map, const uint32_t* w,
+                                          bf16* base, size_t row, int ld, int x) {
+  if (o.rows >= 32) {
+    if (o.lane == 0) ptx::bulk_wait_group_read0();  // the last box has left the buffer
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 4; ++q)  // 64-byte swizzle
+      o.buf[o.lane * 4 + (q ^ ((o.lane >> 1) & 3))] =
+          make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (o.lane == 0) {
+      ptx::tma_store_2d(map, o.buf, x, (int)row);
+      ptx::bulk_commit_group();
+    }
+  } else if (o.lane < o.rows) {
+    bf16* p = base + (row + o.lane) * (size_t)ld + x;
+    st_sector(p, w);
+    st_sector(p + 16, w + 8);
+  }
 }
 // 32 bf16 columns (16 packed words) rounded to e4m3
 __device__ __forceinline__ void store_fp8(uint8_t* p, const uint32_t* w, float inv) {
@@ -245,7 +279,7 @@ __device__ __forceinline__ void load_a(uint8_t* dst, const CUtensorMap* big,
   }
 }
 
-template <int MODE>
+template <int MODE, int KS>
 __device__ __forceinline__ bool producer_tile(SmemCtl& c, uint8_t* smem, const KParams& p,
                                               const CUtensorMap* tmA, const CUtensorMap* tmS,
                                               const CUtensorMap* tmB, const Tile& t, uint32_t rank,
@@ -284,7 +318,7 @@ __device__ __forceinline__ bool producer_tile(SmemCtl& c, uint8_t* smem, const K
       load_a<MODE>(sA, tmA, tmS, fb, kb, half, row, t.rows);
       tma_load_3d_pair(sB, tmB, fb, t.n0 + 128 * rank, kb, 2 * t.e + half);
     }
-    if (++stage == kStages) {
+    if (++stage == KS) {
       stage = 0;
       phase ^= 1;
     }
@@ -378,7 +412,7 @@ struct MmaState {
   int stage = 0;
   uint32_t phase = 0, group = 0, tiles = 0;
 };
-template <int MODE>
+template <int MODE, int KS>
 __device__ __forceinline__ bool mma_tile(SmemCtl& c, uint32_t smem, const KParams& p,
                                          uint32_t tmem, MmaState& m) {
   constexpr uint32_t idesc = idesc_mxf8(2 * BM, BN, Mode<MODE>::kBMn);
@@ -427,7 +461,7 @@ __device__ __forceinline__ bool mma_tile(SmemCtl& c, uint32_t smem, const KParam
         if (k0 + kb == nk - 1) ptx::umma_commit_pair(&c.tmem_full[acc], 3);
       }
       __syncwarp();
-      if (++m.stage == kStages) {
+      if (++m.stage == KS) {
         m.stage = 0;
         m.phase ^= 1;
       }
@@ -449,51 +483,47 @@ __device__ __forceinline__ uint32_t pair_max(SmemCtl& c, uint32_t m, int ew, int
   return max(m, c.amax[buf][ew ^ 4][lane]);
 }
 
-// The columns that the two accumulators share are the first one's last 64 and
-// the second one's first 64. An epilogue therefore takes its 32-column chunks
-// in falling order on the first accumulator (rev = 1) and in rising order on the
-// second; the warps that hold the shared chunks (hf == rev) release them as soon
-// as both are in registers.
-// Asks L2 for the pre-activations that this thread will read in tile t: their
-// HBM latency is the longest part of a chunk's work otherwise.
-__device__ __forceinline__ void prefetch_a(const KParams& p, const Tile& t, int ew, int lane) {
-  const int r = (ew & 3) * 32 + lane;
-  if (r >= t.rows) return;
-  const bf16* src = p.aux + ((size_t)t.row0 + t.m0 + r) * (2 * p.F);
+// ================================================================ aux loader
+// FC2 dgrad: the saved pre-activations of a tile, in the epilogue's four steps:
+// for each 128 columns (half) and each 32 of a warp's 64 columns (i), the gate and
+// up boxes of both warps of a quarter.
+__device__ __forceinline__ bool aux_tile(SmemCtl& c, uint8_t* aux, const KParams& p,
+                                         const CUtensorMap* map, const Tile& t, uint32_t& tiles,
+                                         uint32_t& ph) {
+  const int rev = (tiles & 1) ^ 1;
+  ++tiles;
+  if (t.rows <= 0) return true;
+  for (int n = 0; n < 4; ++n, ph ^= 1) {
+    if (!ptx::mbar_wait(&c.aux_empty, ph ^ 1, &c.abort, kWaitLimitNs)) {
+      flag_timeout(c, p.status, 9);
+      return false;
+    }
+    ptx::mbar_arrive_expect_tx(&c.aux_full, kAuxBytes);
+    const int x = t.n0 + 128 * ((n >> 1) ^ rev) + 32 * (n & 1);
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int f = t.n0 + 128 * half + 64 * (ew >> 2);  // 64 columns: one 128-byte line
-    if (f < p.F) {
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(src + f));
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(src + p.F + f));
+    for (int h = 0; h < 2; ++h) {
+      ptx::tma_load_2d(aux + 16384 * h, map, &c.aux_full, x + 64 * h, t.row0 + t.m0);
+      ptx::tma_load_2d(aux + 16384 * h + 8192, map, &c.aux_full, p.F + x + 64 * h, t.row0 + t.m0);
     }
   }
+  return true;
 }
 
+// The columns that the two accumulators share are the first one's last 64 and
+// the second one's first 64. An epilogue therefore starts with the higher half of
+// its columns on the first accumulator (rev = 1) and with the lower half on the
+// second; the warps that hold the shared columns (hf == rev) release them as soon
+// as they are in registers.
 template <int MODE>
-__device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const KParams& p, const Tile& t,
+__device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const uint8_t* aux, uint4* buf,
+                                              const KParams& p, const Maps& m, const Tile& t,
                                               uint32_t tmem, uint32_t rank, uint32_t& tiles,
-                                              int ew, int lane) {
+                                              uint32_t& aux_ph, int ew, int lane) {
   const int q = ew & 3, hf = ew >> 2;
   const int acc = tiles & 1, rev = acc ^ 1;
-  const size_t row = (size_t)t.row0 + t.m0 + q * 32 + lane;  // this thread's row
+  const size_t row0 = (size_t)t.row0 + t.m0 + q * 32, row = row0 + lane;  // this warp's, thread's
   const bool rok = q * 32 + lane < t.rows;
-  // FC2 dgrad: 32 columns of the saved gate and up pre-activations
-  uint32_t ag[16], au[16];
-  auto load_a = [&](int cc) {
-    const int f = t.n0 + 32 * cc;
-    if (rok && f < p.F) {
-      const bf16* src = p.aux + row * (size_t)(2 * p.F) + f;
-      ld_sector(src, ag);
-      ld_sector(src + 16, ag + 8);
-      ld_sector(src + p.F, au);
-      ld_sector(src + p.F + 16, au + 8);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) ag[j] = au[j] = 0;
-    }
-  };
-  if (MODE == FC2_DGRAD) load_a(4 * rev + 2 * hf + rev);  // while the MMAs run
+  const Out out = {buf, lane, t.rows - q * 32};
   if (!ptx::mbar_wait(&c.tmem_full[acc], (tiles >> 1) & 1, &c.abort, kWaitLimitNs)) {
     if (lane == 0) flag_timeout(c, p.status, 6);
     return false;
@@ -504,30 +534,40 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const KParams& p, cons
   if (q * 32 >= t.rows) {  // nothing to store (both warps of the quarter)
     if (hf == rev) release(&c.ovl, rank, lane);
     release(&c.tmem_empty[acc], rank, lane);
+    if (MODE == FC2_DGRAD && t.rows > 0) {  // the other quarters' pre-activations pass by
+      for (int n = 0; n < 4; ++n, aux_ph ^= 1) {
+        if (!ptx::mbar_wait(&c.aux_full, aux_ph, &c.abort, kWaitLimitNs)) {
+          if (lane == 0) flag_timeout(c, p.status, 11);
+          return false;
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&c.aux_empty);
+      }
+    }
   } else if (MODE == FC1_FWD) {
-    // columns 0..127 gate, 128..255 up of one 128-wide block of h
-    // (the shared columns: up 64..127 of the first accumulator, gate 0..63 of the second)
-    uint32_t hw[32];
+    // columns 0..127 gate, 128..255 up of one 128-wide block of h; this warp's 64
+    // of each, the shared ones (up 64..127 of the first accumulator, gate 0..63 of
+    // the second) first
+    uint32_t hw[32], s0[32], s1[32], o[32];
     uint32_t mx = 0;
-    uint32_t s0[32], s1[32], g[32];
     const uint32_t sbase = tbase + 128 * rev + 64 * hf, obase = tbase + 128 * (rev ^ 1) + 64 * hf;
-    ptx::tmem_ld_32x32b_x32(sbase + 32 * rev, s0);
-    ptx::tmem_ld_32x32b_x32(sbase + 32 * (rev ^ 1), s1);
+    ptx::tmem_ld_32x32b_x32(sbase, s0);
+    ptx::tmem_ld_32x32b_x32(sbase + 32, s1);
     ptx::tmem_ld_wait(s0, s1);
     if (hf == rev) release(&c.ovl, rank, lane);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int cc = 2 * hf + (i ^ rev), f = t.n0 + 32 * cc;
+      const int f = t.n0 + 64 * hf + 32 * i;
       const bool ok = f < p.F;
       uint32_t(&sh)[32] = i ? s1 : s0;
-      ptx::tmem_ld_32x32b_x32(obase + 32 * (i ^ rev), g);
-      ptx::tmem_ld_wait(g);
+      ptx::tmem_ld_32x32b_x32(obase + 32 * i, o);
+      ptx::tmem_ld_wait(o);
       if (i == 1) release(&c.tmem_empty[acc], rank, lane);
       uint32_t gw[16], uw[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const uint32_t ws = pack_bf16x2(__uint_as_float(sh[2 * j]), __uint_as_float(sh[2 * j + 1]));
-        const uint32_t wo = pack_bf16x2(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1]));
+        const uint32_t wo = pack_bf16x2(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
         gw[j] = rev ? wo : ws;
         uw[j] = rev ? ws : wo;
         const float g0 = bf16_lo(gw[j]), g1 = bf16_hi(gw[j]);
@@ -536,13 +576,12 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const KParams& p, cons
         hw[16 * i + j] = h2;
         if (ok) mx = absmax_bf16x2(mx, h2);  // columns past F are not part of the block
       }
-      if (rok && ok) {
+      if (ok) {
         if (p.out0) {
-          bf16* a = p.out0 + row * (size_t)(2 * p.F) + f;
-          store_words(a, gw);
-          store_words(a + p.F, uw);
+          store_box(out, &m.o1, gw, p.out0, row0, 2 * p.F, f);
+          store_box(out, &m.o1, uw, p.out0, row0, 2 * p.F, p.F + f);
         }
-        if (p.out1) store_words(p.out1 + row * (size_t)p.F + f, hw + 16 * i);
+        if (p.out1) store_box(out, &m.o2, hw + 16 * i, p.out1, row0, p.F, f);
       }
     }
     const uint32_t b = fp8_scale_byte(pair_max(c, absmax_bits(mx), ew, lane, acc));
@@ -550,49 +589,64 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const KParams& p, cons
     const int f = t.n0 + 64 * hf, fb = t.n0 / 128;
     if (rok && f < p.F) {
       uint8_t* qp = p.q + row * (size_t)p.F + f;
-      store_fp8(qp + 32 * rev, hw, inv);
-      store_fp8(qp + 32 * (rev ^ 1), hw + 16, inv);
+      store_fp8(qp, hw, inv);
+      store_fp8(qp + 32, hw + 16, inv);
     }
     if (hf == 0 && rok) p.s[((size_t)(fb >> 2) * p.N + row) * 4 + (fb & 3)] = (uint8_t)b;
   } else if (MODE == FC2_DGRAD) {
     const int nf = (p.F + 127) / 128;
-    uint32_t v[2][32];  // both chunks of the half: the first half's may be the shared columns
+    uint32_t v[2][32];
 #pragma unroll 1
     for (int hi = 0; hi < 2; ++hi) {  // 128 columns: one block of da_gate, one of da_up
       const int half = hi ^ rev;
       uint32_t gw[32], uw[32];
       uint32_t mg = 0, mu = 0;
       const uint32_t vbase = tbase + 128 * half + 64 * hf;
-      ptx::tmem_ld_32x32b_x32(vbase + 32 * rev, v[0]);
-      ptx::tmem_ld_32x32b_x32(vbase + 32 * (rev ^ 1), v[1]);
+      ptx::tmem_ld_32x32b_x32(vbase, v[0]);
+      ptx::tmem_ld_32x32b_x32(vbase + 32, v[1]);
       ptx::tmem_ld_wait(v[0], v[1]);
       if (hi == 0 && hf == rev) release(&c.ovl, rank, lane);
       if (hi == 1) release(&c.tmem_empty[acc], rank, lane);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int cc = 4 * half + 2 * hf + (i ^ rev), f = t.n0 + 32 * cc;
+      for (int i = 0; i < 2; ++i, aux_ph ^= 1) {
+        const int f = t.n0 + 128 * half + 64 * hf + 32 * i;
         const bool ok = f < p.F;
+        // the step's gate and up boxes: 64-byte rows, 16-byte chunk j of row r at j ^ ((r >> 1) & 3)
+        if (!ptx::mbar_wait(&c.aux_full, aux_ph, &c.abort, kWaitLimitNs)) {
+          if (lane == 0) flag_timeout(c, p.status, 12);
+          return false;
+        }
+        uint4 gc[4], uc[4];
+        const int r = q * 32 + lane;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int at = 16384 * hf + r * 64 + ((j ^ ((r >> 1) & 3)) * 16);
+          gc[j] = *reinterpret_cast<const uint4*>(aux + at);
+          uc[j] = *reinterpret_cast<const uint4*>(aux + 8192 + at);
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&c.aux_empty);
+        const uint32_t* ag = reinterpret_cast<const uint32_t*>(gc);
+        const uint32_t* au = reinterpret_cast<const uint32_t*>(uc);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const float d0 = __uint_as_float(v[i][2 * j]), d1 = __uint_as_float(v[i][2 * j + 1]);
           const float a0 = bf16_lo(ag[j]), a1 = bf16_hi(ag[j]);
           const float s0 = sigmoid_f(a0), s1 = sigmoid_f(a1);
           const float e0 = d0 * s0, e1 = d1 * s1;
-          uw[16 * i + j] = pack_bf16x2(e0 * a0, e1 * a1);
-          gw[16 * i + j] = pack_bf16x2(e0 * bf16_lo(au[j]) * fmaf(a0, 1.f - s0, 1.f),
-                                       e1 * bf16_hi(au[j]) * fmaf(a1, 1.f - s1, 1.f));
+          const uint32_t u2 = pack_bf16x2(e0 * a0, e1 * a1);
+          const uint32_t g2 = pack_bf16x2(e0 * bf16_lo(au[j]) * fmaf(a0, 1.f - s0, 1.f),
+                                          e1 * bf16_hi(au[j]) * fmaf(a1, 1.f - s1, 1.f));
+          uw[16 * i + j] = u2;
+          gw[16 * i + j] = g2;
           if (ok) {
-            mu = absmax_bf16x2(mu, uw[16 * i + j]);
-            mg = absmax_bf16x2(mg, gw[16 * i + j]);
+            mu = absmax_bf16x2(mu, u2);
+            mg = absmax_bf16x2(mg, g2);
           }
         }
-        // the next chunk's, beside this one's stores
-        if (i == 0) load_a(4 * half + 2 * hf + (rev ^ 1));
-        else if (hi == 0) load_a(4 * (half ^ 1) + 2 * hf + rev);
-        if (p.out0 && rok && ok) {
-          bf16* da = p.out0 + row * (size_t)(2 * p.F) + f;
-          store_words(da, gw + 16 * i);
-          store_words(da + p.F, uw + 16 * i);
+        if (p.out0 && ok) {
+          store_box(out, &m.o1, gw + 16 * i, p.out0, row0, 2 * p.F, f);
+          store_box(out, &m.o1, uw + 16 * i, p.out0, row0, 2 * p.F, p.F + f);
         }
       }
       const uint32_t bg = fp8_scale_byte(pair_max(c, absmax_bits(mg), ew, lane, 0));
@@ -601,10 +655,10 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const KParams& p, cons
       const int f = t.n0 + 128 * half + 64 * hf;
       if (rok && f < p.F) {
         uint8_t* qp = p.q + row * (size_t)(2 * p.F) + f;
-        store_fp8(qp + 32 * rev, gw, ig);
-        store_fp8(qp + 32 * (rev ^ 1), gw + 16, ig);
-        store_fp8(qp + p.F + 32 * rev, uw, iu);
-        store_fp8(qp + p.F + 32 * (rev ^ 1), uw + 16, iu);
+        store_fp8(qp, gw, ig);
+        store_fp8(qp + 32, gw + 16, ig);
+        store_fp8(qp + p.F, uw, iu);
+        store_fp8(qp + p.F + 32, uw + 16, iu);
       }
       if (rok && t.n0 + 128 * half < p.F) {
         const int kb = hf * nf + t.n0 / 128 + half;  // the gate's byte or the up half's
@@ -612,30 +666,27 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const KParams& p, cons
       }
     }
   } else {
-    // plain fp32 tile -> bf16; the next chunk's TMEM load runs beside the stores
-    bf16* out = p.out0 + row * (size_t)p.H + t.n0;
-    auto chunk = [&](int i) {
-      const int ci = i ^ (3 * rev);
-      return (ci >> 1) * 4 + 2 * hf + (ci & 1);
-    };
+    // plain fp32 tile -> bf16; the other half's TMEM loads run beside the stores
     uint32_t v[2][32];
-    ptx::tmem_ld_32x32b_x32(tbase + 32 * chunk(0), v[0]);
-    ptx::tmem_ld_32x32b_x32(tbase + 32 * chunk(1), v[1]);
+    const uint32_t vbase = tbase + 64 * hf;
+    ptx::tmem_ld_32x32b_x32(vbase + 128 * rev, v[0]);
+    ptx::tmem_ld_32x32b_x32(vbase + 128 * rev + 32, v[1]);
     ptx::tmem_ld_wait(v[0], v[1]);
     if (hf == rev) release(&c.ovl, rank, lane);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      const int half = (i >> 1) ^ rev;
       if (i == 2) {
         ptx::tmem_ld_wait(v[0], v[1]);
         release(&c.tmem_empty[acc], rank, lane);
       }
-      const int cc = chunk(i);
+      const int col = 128 * half + 64 * hf + 32 * (i & 1);
       uint32_t w[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j)
         w[j] = pack_bf16x2(__uint_as_float(v[i & 1][2 * j]), __uint_as_float(v[i & 1][2 * j + 1]));
-      if (i < 2) ptx::tmem_ld_32x32b_x32(tbase + 32 * chunk(i + 2), v[i]);
-      if (rok && t.n0 + 32 * cc < p.H) store_words(out + 32 * cc, w);
+      if (i < 2) ptx::tmem_ld_32x32b_x32(vbase + 128 * (rev ^ 1) + 32 * i, v[i]);
+      if (t.n0 + col < p.H) store_box(out, &m.o3, w, p.out0, row0, p.H, t.n0 + col);
     }
   }
   if (Mode<MODE>::kFirst) {
@@ -672,13 +723,9 @@ __device__ __forceinline__ bool count_tile(SmemCtl& c, const KParams& p, int e, 
 
 template <int M1, int M2>
 __global__ void __launch_bounds__(kThreads, 1)
-    grouped_gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmA1,
-                            const __grid_constant__ CUtensorMap tmS1,
-                            const __grid_constant__ CUtensorMap tmB1,
-                            const __grid_constant__ CUtensorMap tmA2,
-                            const __grid_constant__ CUtensorMap tmS2,
-                            const __grid_constant__ CUtensorMap tmB2, const KParams p1,
-                            const KParams p2) {
+    grouped_gemm_fp8_kernel(const __grid_constant__ Maps m, const KParams p1, const KParams p2) {
+  using C = Chain<M1>;
+  constexpr int KS = C::kStages;
   extern __shared__ uint8_t dyn_smem[];
   __shared__ SmemCtl ctl;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) &
@@ -686,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = p1.E;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < KS; ++s) {
       ptx::mbar_init(&ctl.full[s], 1);
       ptx::mbar_init(&ctl.empty[s], 1);
     }
@@ -701,6 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&ctl.tmem_empty[a], 16);  // both CTAs' epilogue warps
     }
     ptx::mbar_init(&ctl.ovl, 8);  // the four warps of each CTA that hold the shared columns
+    ptx::mbar_init(&ctl.aux_full, 1);
+    ptx::mbar_init(&ctl.aux_empty, 8);
     ptx::mbar_init(&ctl.drain, 1);
     ctl.abort = 0;
     ptx::fence_mbar_init();
@@ -712,12 +761,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tmem_relinquish_pair();
   }
   if (threadIdx.x == 0) {
-    ptx::tma_prefetch_desc(&tmA1);
-    ptx::tma_prefetch_desc(&tmS1);
-    ptx::tma_prefetch_desc(&tmS2);
-    ptx::tma_prefetch_desc(&tmB1);
-    ptx::tma_prefetch_desc(&tmA2);
-    ptx::tma_prefetch_desc(&tmB2);
+    for (const CUtensorMap* t : {&m.a1, &m.s1, &m.b1, &m.a2, &m.s2, &m.b2})
+      ptx::tma_prefetch_desc(t);
   }
   pdl_wait();
   // offsets outside 0..N would send stores out of the buffers
@@ -762,17 +807,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int i = first; ok && i < total; i += stride)
-        ok = i < total1 ? producer_tile<M1>(ctl, smem, p1, &tmA1, &tmS1, &tmB1, tile1(i), rank,
+        ok = i < total1 ? producer_tile<M1, KS>(ctl, smem, p1, &m.a1, &m.s1, &m.b1, tile1(i), rank,
                                             stage, phase)
-                        : producer_tile<M2>(ctl, smem, p2, &tmA2, &tmS2, &tmB2, tile2(i), rank,
+                        : producer_tile<M2, KS>(ctl, smem, p2, &m.a2, &m.s2, &m.b2, tile2(i), rank,
                                             stage, phase);
-      if (!ok && rank == 0) drain_loads<kStages>(ctl.full, stage, phase);  // both CTAs' loads
+      if (!ok && rank == 0) drain_loads<KS>(ctl.full, stage, phase);  // both CTAs' loads
     } else if (warp == 1 && rank == 0) {
-      MmaState m;
+      MmaState st;
       bool ok = true;
       for (int i = first; ok && i < total; i += stride)
-        ok = i < total1 ? mma_tile<M1>(ctl, ptx::smem_u32(smem), p1, tmem, m)
-                        : mma_tile<M2>(ctl, ptx::smem_u32(smem), p2, tmem, m);
+        ok = i < total1 ? mma_tile<M1, KS>(ctl, ptx::smem_u32(smem), p1, tmem, st)
+                        : mma_tile<M2, KS>(ctl, ptx::smem_u32(smem), p2, tmem, st);
       // no MMA may still run when TMEM is released (the same lane is elected as above)
       __syncwarp();
       if (elect_one()) ptx::umma_commit_pair(&ctl.drain, 1);
@@ -781,7 +826,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_wait(&ctl.drain, 0, &dummy, kWaitLimitNs);
       }
     }
-    else if (warp == 2 && lane == 0) {
+    else if (C::kAux && warp == 3 && lane == 0) {
+      ptx::tma_prefetch_desc(&m.aux);
+      uint32_t tiles = 0, ph = 0;
+      bool ok = true;
+      for (int i = first; ok && i < total1; i += stride)
+        ok = aux_tile(ctl, smem + C::kAuxAt, p1, &m.aux, tile1(i), tiles, ph);
+      if (!ok) {  // the load in flight, if any
+        int none = 0;
+        ptx::mbar_wait(&ctl.aux_full, ph ^ 1, &none, kWaitLimitNs);
+      }
+    } else if (warp == 2 && lane == 0) {
       uint32_t tiles = 0;
       bool ok = true;
       for (int i = first; ok && i < total1; i += stride) ok = count_tile(ctl, p1, tile1(i).e, tiles);
@@ -789,18 +844,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp < 12) {
     regs_inc<kRegsEpilogue>();
-    uint32_t tiles = 0;
+    uint32_t tiles = 0, aux_ph = 0;
     bool ok = true;
-    for (int i = first; ok && i < total; i += stride) {
-      if (i < total1) {
-        const Tile t = tile1(i);
-        if (M1 == FC2_DGRAD && i + stride < total1)
-          prefetch_a(p1, tile1(i + stride), warp - 4, lane);
-        ok = epilogue_tile<M1>(ctl, p1, t, tmem, rank, tiles, warp - 4, lane);
-      } else {
-        ok = epilogue_tile<M2>(ctl, p2, tile2(i), tmem, rank, tiles, warp - 4, lane);
-      }
-    }
+    const int ew = warp - 4;
+    const uint8_t* aux = smem + C::kAuxAt;
+    uint4* buf = reinterpret_cast<uint4*>(smem + C::kEpiAt) + ew * 128;
+    for (int i = first; ok && i < total; i += stride)
+      ok = i < total1 ? epilogue_tile<M1>(ctl, aux, buf, p1, m, tile1(i), tmem, rank, tiles, aux_ph,
+                                          ew, lane)
+                      : epilogue_tile<M2>(ctl, aux, buf, p2, m, tile2(i), tmem, rank, tiles, aux_ph,
+                                          ew, lane);
+    // the buffers and the outputs must outlive the TMA stores
+    if (lane == 0) ptx::bulk_wait_group0();
+    __syncwarp();
   } else {
     regs_dec<kRegsControl>();
     uint32_t group = 0;
@@ -827,7 +883,7 @@ cudaError_t resident_pairs(int* pairs) {
   if (e != cudaSuccess) return e;
   if (dev < 64 && (*pairs = known[dev].load()) > 0) return cudaSuccess;
   e = cudaFuncSetAttribute(grouped_gemm_fp8_kernel<M1, M2>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDynSmem);
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Chain<M1>::kDynSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[1];
@@ -836,7 +892,7 @@ cudaError_t resident_pairs(int* pairs) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(device_sm_count() / 2 * 2);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kDynSmem;
+  cfg.dynamicSmemBytes = Chain<M1>::kDynSmem;
   cfg.attrs = at;
   cfg.numAttrs = 1;
   e = cudaOccupancyMaxActiveClusters(pairs, grouped_gemm_fp8_kernel<M1, M2>, &cfg);
@@ -846,7 +902,7 @@ cudaError_t resident_pairs(int* pairs) {
 }
 
 template <int M1, int M2>
-moe_status_t launch_chain(const moe_layer_desc_t& d, const CUtensorMap (&m)[6], const KParams& p1,
+moe_status_t launch_chain(const moe_layer_desc_t& d, const Maps& m, const KParams& p1,
                           const KParams& p2, int kernel_id, bool counters_zeroed, cudaStream_t st) {
   int pairs = 0;
   cudaError_t e = resident_pairs<M1, M2>(&pairs);
@@ -869,13 +925,13 @@ moe_status_t launch_chain(const moe_layer_desc_t& d, const CUtensorMap (&m)[6], 
   at[1].val.programmaticStreamSerializationAllowed = MOE_PDL;
   cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kDynSmem;
+  cfg.dynamicSmemBytes = Chain<M1>::kDynSmem;
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 2;
   {
     LaunchScope _ls(kernel_id, st);
-    e = cudaLaunchKernelEx(&cfg, grouped_gemm_fp8_kernel<M1, M2>, m[0], m[1], m[2], m[3], m[4], m[5], p1, p2);
+    e = cudaLaunchKernelEx(&cfg, grouped_gemm_fp8_kernel<M1, M2>, m, p1, p2);
   }
   if (e != cudaSuccess) {
     set_error("grouped_gemm_fp8_kernel launch: %s", cudaGetErrorString(e));
@@ -907,11 +963,13 @@ moe_status_t launch_ffn_fwd_fp8(const moe_layer_desc_t& d, const uint8_t* xq, co
   if (N <= kFp8FewRows * d.E)
     return launch_ffn_rows_fp8(d, xq, xs, off, w, a, h, hq, hs, o, status, dep, st,
                                counters_zeroed);
-  CUtensorMap m[6];
-  if (!make_map(&m[0], xq, 2, d.H, N, 1, BM, 1) || !make_map(&m[1], xq, 2, d.H, N, 1, kABoxRows, 1) ||
-      !make_map(&m[2], w.w1q, 2, d.H, 2ll * d.E * d.F, 1, 128, 1) ||
-      !make_map(&m[3], hq, 2, d.F, N, 1, BM, 1) || !make_map(&m[4], hq, 2, d.F, N, 1, kABoxRows, 1) ||
-      !make_map(&m[5], w.w2q, 2, d.F, (long long)d.E * d.H, 1, 128, 1))
+  Maps m = {};
+  if (!make_map(&m.a1, xq, 2, d.H, N, 1, BM, 1) || !make_map(&m.s1, xq, 2, d.H, N, 1, kABoxRows, 1) ||
+      !make_map(&m.b1, w.w1q, 2, d.H, 2ll * d.E * d.F, 1, 128, 1) ||
+      !make_map(&m.a2, hq, 2, d.F, N, 1, BM, 1) || !make_map(&m.s2, hq, 2, d.F, N, 1, kABoxRows, 1) ||
+      !make_map(&m.b2, w.w2q, 2, d.F, (long long)d.E * d.H, 1, 128, 1) ||
+      !make_rows_map(&m.o3, o, N, d.H, 32) || (a && !make_rows_map(&m.o1, a, N, 2 * d.F, 32)) ||
+      (h && !make_rows_map(&m.o2, h, N, d.F, 32)))
     return MOE_ERR_CUDA;
   KParams p1 = params(d, off, status, dep), p2 = p1;
   p1.sa = xs;
@@ -932,17 +990,18 @@ moe_status_t launch_ffn_dgrad_fp8(const moe_layer_desc_t& d, const uint8_t* dq, 
                                   cudaStream_t st, bool counters_zeroed) {
   const long long N = (long long)d.T * d.k;
   if (N == 0) return MOE_OK;
-  CUtensorMap m[6];
-  if (!make_map(&m[0], dq, 2, d.H, N, 1, BM, 1) || !make_map(&m[1], dq, 2, d.H, N, 1, kABoxRows, 1) ||
-      !make_map(&m[2], w.w2q, 3, d.F, d.H, d.E, 128, 1) ||
-      !make_map(&m[3], daq, 3, d.F, 2, N, 1, BM) || !make_map(&m[4], daq, 3, d.F, 2, N, 1, kABoxRows) ||
-      !make_map(&m[5], w.w1q, 3, d.H, d.F, 2ll * d.E, 128, 1))
+  Maps m = {};
+  if (!make_map(&m.a1, dq, 2, d.H, N, 1, BM, 1) || !make_map(&m.s1, dq, 2, d.H, N, 1, kABoxRows, 1) ||
+      !make_map(&m.b1, w.w2q, 3, d.F, d.H, d.E, 128, 1) ||
+      !make_map(&m.a2, daq, 3, d.F, 2, N, 1, BM) || !make_map(&m.s2, daq, 3, d.F, 2, N, 1, kABoxRows) ||
+      !make_map(&m.b2, w.w1q, 3, d.H, d.F, 2ll * d.E, 128, 1) ||
+      !make_rows_map(&m.o3, dx_perm, N, d.H, 32) || !make_rows_map(&m.aux, a, N, 2 * d.F, BM) ||
+      (da && !make_rows_map(&m.o1, da, N, 2 * d.F, 32)))
     return MOE_ERR_CUDA;
   KParams p1 = params(d, off, status, dep), p2 = p1;
   p1.sa = ds;
   p1.sb = w.w2s;
   p1.out0 = da;
-  p1.aux = a;
   p1.q = daq;
   p1.s = das;
   p2.sa = das;
