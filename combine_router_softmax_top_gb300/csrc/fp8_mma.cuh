@@ -87,11 +87,11 @@ __device__ __forceinline__ int ld_acquire(const int* p) {
 // After an abort: waits (bounded) until the loads that a producer has issued have
 // landed, so that none writes into shared memory that is no longer this
 // kernel's. stage, phase: the producer's place in the ring.
-template <int STAGES>
-__device__ __forceinline__ void drain_loads(uint64_t* full, int stage, uint32_t phase) {
+__device__ __forceinline__ void drain_loads(uint64_t* full, int stages, int stage,
+                                            uint32_t phase) {
   int none = 0;
-  for (int s = 0; s < STAGES; ++s)
-    ptx::mbar_wait(&full[s], s < stage ? phase : phase ^ 1, &none, kWaitLimitNs / STAGES);
+  for (int s = 0; s < stages; ++s)
+    ptx::mbar_wait(&full[s], s < stage ? phase : phase ^ 1, &none, kWaitLimitNs / stages);
 }
 
 // ------------------------------------------------------------------ host side

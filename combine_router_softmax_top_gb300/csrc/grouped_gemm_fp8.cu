@@ -64,8 +64,7 @@ enum Fp8Mode {
 constexpr int BM = 128, BN = 256, BK = 128;   // BM: rows of one CTA of the pair
 constexpr int kABytes = BM * BK, kBBytes = BN / 2 * BK;
 constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kStagesMax = 6;
-constexpr int kAuxBytes = 4 * 8192;           // gate and up of both 32-column steps, 128 rows
+constexpr int kAuxBytes = 4 * 8192;           // one step: gate and up, 128 rows x 2 x 32 columns
 constexpr int kEpiBytes = 8 * 2048;           // a 32 x 32 bf16 box for each epilogue warp
 constexpr int kABoxRows = 16;                 // tiles of 64 rows or fewer load boxes of 16
 constexpr int kTmemCols = 512;
@@ -78,16 +77,22 @@ constexpr int kThreads = 512;
 constexpr int kRegsControl = 72, kRegsEpilogue = 184;
 constexpr int kMaxE = 256;
 
-// Launch-wide constants: the gradient chain gives one operand stage up for the
-// saved pre-activations of its first GEMM.
+// Launch-wide constants. The gradient's first GEMM gives two of the six operand
+// stages up for two steps of the saved pre-activations (asking L2 for them ahead
+// instead was slower: 204 against 196 us, and 184 so); its second GEMM gets them
+// back as a ring of its own (kSecond: its first barrier).
 template <int M1>
 struct Chain {
   static constexpr bool kAux = M1 == 2;
-  static constexpr int kStages = kAux ? 5 : 6;
-  static constexpr int kAuxAt = kStages * kStageBytes;
-  static constexpr int kEpiAt = kAuxAt + (kAux ? kAuxBytes : 0);
+  static constexpr int kStages1 = kAux ? 4 : 6, kStages2 = 6;
+  static constexpr int kSecond = kAux ? kStages1 : 0;
+  static constexpr int kBars = kSecond + kStages2;
+  static constexpr int kAuxAt = kStages1 * kStageBytes;
+  static constexpr int kEpiAt = kStages2 * kStageBytes;
   static constexpr size_t kDynSmem = kEpiAt + kEpiBytes + 1024;
+  static_assert(!kAux || kAuxAt + 2 * kAuxBytes <= kEpiAt, "the pre-activations' room");
 };
+constexpr int kMaxBars = 10;
 
 struct Maps {
   CUtensorMap a1, s1, b1, a2, s2, b2;  // operands: A, A in small boxes, B of both GEMMs
@@ -129,8 +134,8 @@ struct Tile {
 };
 
 struct SmemCtl {
-  uint64_t full[kStagesMax], empty[kStagesMax];
-  uint64_t aux_full, aux_empty;
+  uint64_t full[kMaxBars], empty[kMaxBars];
+  uint64_t aux_full[2], aux_empty[2];
   uint64_t sf_full[kSf], sf_empty[kSf];
   uint64_t tmem_full[2], tmem_empty[2], ovl, drain;
   uint64_t stored[2], counted[2];  // a first-GEMM tile's stores issued; counted for its expert
@@ -280,7 +285,7 @@ __device__ __forceinline__ void load_a(uint8_t* dst, const CUtensorMap* big,
 }
 
 template <int MODE, int KS>
-__device__ __forceinline__ bool producer_tile(SmemCtl& c, uint8_t* smem, const KParams& p,
+__device__ __forceinline__ bool producer_tile(SmemCtl& c, int ring, uint8_t* smem, const KParams& p,
                                               const CUtensorMap* tmA, const CUtensorMap* tmS,
                                               const CUtensorMap* tmB, const Tile& t, uint32_t rank,
                                               int& stage, uint32_t& phase) {
@@ -294,7 +299,7 @@ __device__ __forceinline__ bool producer_tile(SmemCtl& c, uint8_t* smem, const K
     asm volatile("fence.proxy.async.global;" ::: "memory");
   }
   for (int kt = 0; kt < nk; ++kt) {
-    if (!ptx::mbar_wait(&c.empty[stage], phase ^ 1, &c.abort, kWaitLimitNs)) {
+    if (!ptx::mbar_wait(&c.empty[ring + stage], phase ^ 1, &c.abort, kWaitLimitNs)) {
       flag_timeout(c, p.status, 1);
       return false;
     }
@@ -302,8 +307,9 @@ __device__ __forceinline__ bool producer_tile(SmemCtl& c, uint8_t* smem, const K
     uint8_t* sB = sA + kABytes;
     const int k0 = kt * BK;
     // both CTAs' loads complete on the even CTA's full[stage]
-    const uint32_t fb = ptx::mapa_shared(&c.full[stage], 0);
-    if (rank == 0) ptx::mbar_arrive_expect_tx(&c.full[stage], bytes);
+    uint64_t* bar = &c.full[ring + stage];
+    const uint32_t fb = ptx::mapa_shared(bar, 0);
+    if (rank == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
     if (MODE == FC1_FWD) {  // even CTA: 128 gate rows of W1, odd CTA: 128 up rows
       load_a<MODE>(sA, tmA, tmS, fb, k0, 0, row, t.rows);
       ptx::tma_load_2d_pair(sB, tmB, fb, k0, (2 * t.e + rank) * p.F + t.n0);
@@ -413,7 +419,7 @@ struct MmaState {
   uint32_t phase = 0, group = 0, tiles = 0;
 };
 template <int MODE, int KS>
-__device__ __forceinline__ bool mma_tile(SmemCtl& c, uint32_t smem, const KParams& p,
+__device__ __forceinline__ bool mma_tile(SmemCtl& c, int ring, uint32_t smem, const KParams& p,
                                          uint32_t tmem, MmaState& m) {
   constexpr uint32_t idesc = idesc_mxf8(2 * BM, BN, Mode<MODE>::kBMn);
   // one 128-byte atom wide in N (no second atom: LBO unused), or K-major
@@ -431,7 +437,7 @@ __device__ __forceinline__ bool mma_tile(SmemCtl& c, uint32_t smem, const KParam
   // the last), and last the columns it shares with the previous tile's, which come
   // free last: only they delay the first MMA
   if (!wait(&c.sf_full[m.group % kSf], (m.group / kSf) & 1, 4)) return false;
-  if (!wait(&c.full[m.stage], m.phase, 5)) return false;
+  if (!wait(&c.full[ring + m.stage], m.phase, 5)) return false;
   if (!wait(&c.tmem_empty[acc], ((m.tiles >> 1) & 1) ^ 1, 3)) return false;
   if (m.tiles > 0 && !wait(&c.ovl, (m.tiles - 1) & 1, 3)) return false;
   ptx::tc_fence_after();
@@ -444,7 +450,7 @@ __device__ __forceinline__ bool mma_tile(SmemCtl& c, uint32_t smem, const KParam
     for (int kb = 0; kb < 4; ++kb) {
       if (k0 + kb >= nk) break;
       if (k0 + kb) {
-        if (!wait(&c.full[m.stage], m.phase, 5)) return false;
+        if (!wait(&c.full[ring + m.stage], m.phase, 5)) return false;
         ptx::tc_fence_after();
       }
       const uint64_t adesc = desc0 | ((smem + m.stage * kStageBytes) >> 4);
@@ -456,7 +462,7 @@ __device__ __forceinline__ bool mma_tile(SmemCtl& c, uint32_t smem, const KParam
 #pragma unroll
         for (int kk = 1; kk < 4; ++kk)
           umma_mxf8_pair(d, adesc + kk * 2, bdesc + kk * b_adv, idesc | kb * kSel, sfa, sfa + 4, 1);
-        ptx::umma_commit_pair(&c.empty[m.stage], 3);
+        ptx::umma_commit_pair(&c.empty[ring + m.stage], 3);
         if (kb == 3 || k0 + kb == nk - 1) ptx::umma_commit_pair(&c.sf_empty[buf], 3);
         if (k0 + kb == nk - 1) ptx::umma_commit_pair(&c.tmem_full[acc], 3);
       }
@@ -489,21 +495,24 @@ __device__ __forceinline__ uint32_t pair_max(SmemCtl& c, uint32_t m, int ew, int
 // up boxes of both warps of a quarter.
 __device__ __forceinline__ bool aux_tile(SmemCtl& c, uint8_t* aux, const KParams& p,
                                          const CUtensorMap* map, const Tile& t, uint32_t& tiles,
-                                         uint32_t& ph) {
+                                         uint32_t& step) {
   const int rev = (tiles & 1) ^ 1;
   ++tiles;
   if (t.rows <= 0) return true;
-  for (int n = 0; n < 4; ++n, ph ^= 1) {
-    if (!ptx::mbar_wait(&c.aux_empty, ph ^ 1, &c.abort, kWaitLimitNs)) {
+  for (int n = 0; n < 4; ++n, ++step) {
+    const int b = step & 1;
+    if (!ptx::mbar_wait(&c.aux_empty[b], ((step >> 1) & 1) ^ 1, &c.abort, kWaitLimitNs)) {
       flag_timeout(c, p.status, 9);
       return false;
     }
-    ptx::mbar_arrive_expect_tx(&c.aux_full, kAuxBytes);
+    uint8_t* dst = aux + b * kAuxBytes;
+    uint64_t* bar = &c.aux_full[b];
+    ptx::mbar_arrive_expect_tx(bar, kAuxBytes);
     const int x = t.n0 + 128 * ((n >> 1) ^ rev) + 32 * (n & 1);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      ptx::tma_load_2d(aux + 16384 * h, map, &c.aux_full, x + 64 * h, t.row0 + t.m0);
-      ptx::tma_load_2d(aux + 16384 * h + 8192, map, &c.aux_full, p.F + x + 64 * h, t.row0 + t.m0);
+      ptx::tma_load_2d(dst + 16384 * h, map, bar, x + 64 * h, t.row0 + t.m0);
+      ptx::tma_load_2d(dst + 16384 * h + 8192, map, bar, p.F + x + 64 * h, t.row0 + t.m0);
     }
   }
   return true;
@@ -518,7 +527,7 @@ template <int MODE>
 __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const uint8_t* aux, uint4* buf,
                                               const KParams& p, const Maps& m, const Tile& t,
                                               uint32_t tmem, uint32_t rank, uint32_t& tiles,
-                                              uint32_t& aux_ph, int ew, int lane) {
+                                              uint32_t& step, int ew, int lane) {
   const int q = ew & 3, hf = ew >> 2;
   const int acc = tiles & 1, rev = acc ^ 1;
   const size_t row0 = (size_t)t.row0 + t.m0 + q * 32, row = row0 + lane;  // this warp's, thread's
@@ -535,13 +544,13 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const uint8_t* aux, ui
     if (hf == rev) release(&c.ovl, rank, lane);
     release(&c.tmem_empty[acc], rank, lane);
     if (MODE == FC2_DGRAD && t.rows > 0) {  // the other quarters' pre-activations pass by
-      for (int n = 0; n < 4; ++n, aux_ph ^= 1) {
-        if (!ptx::mbar_wait(&c.aux_full, aux_ph, &c.abort, kWaitLimitNs)) {
+      for (int n = 0; n < 4; ++n, ++step) {
+        if (!ptx::mbar_wait(&c.aux_full[step & 1], (step >> 1) & 1, &c.abort, kWaitLimitNs)) {
           if (lane == 0) flag_timeout(c, p.status, 11);
           return false;
         }
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&c.aux_empty);
+        if (lane == 0) ptx::mbar_arrive(&c.aux_empty[step & 1]);
       }
     }
   } else if (MODE == FC1_FWD) {
@@ -608,11 +617,12 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const uint8_t* aux, ui
       if (hi == 0 && hf == rev) release(&c.ovl, rank, lane);
       if (hi == 1) release(&c.tmem_empty[acc], rank, lane);
 #pragma unroll
-      for (int i = 0; i < 2; ++i, aux_ph ^= 1) {
+      for (int i = 0; i < 2; ++i, ++step) {
         const int f = t.n0 + 128 * half + 64 * hf + 32 * i;
         const bool ok = f < p.F;
         // the step's gate and up boxes: 64-byte rows, 16-byte chunk j of row r at j ^ ((r >> 1) & 3)
-        if (!ptx::mbar_wait(&c.aux_full, aux_ph, &c.abort, kWaitLimitNs)) {
+        const int b = step & 1;
+        if (!ptx::mbar_wait(&c.aux_full[b], (step >> 1) & 1, &c.abort, kWaitLimitNs)) {
           if (lane == 0) flag_timeout(c, p.status, 12);
           return false;
         }
@@ -620,12 +630,12 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const uint8_t* aux, ui
         const int r = q * 32 + lane;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int at = 16384 * hf + r * 64 + ((j ^ ((r >> 1) & 3)) * 16);
+          const int at = b * kAuxBytes + 16384 * hf + r * 64 + ((j ^ ((r >> 1) & 3)) * 16);
           gc[j] = *reinterpret_cast<const uint4*>(aux + at);
           uc[j] = *reinterpret_cast<const uint4*>(aux + 8192 + at);
         }
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&c.aux_empty);
+        if (lane == 0) ptx::mbar_arrive(&c.aux_empty[b]);
         const uint32_t* ag = reinterpret_cast<const uint32_t*>(gc);
         const uint32_t* au = reinterpret_cast<const uint32_t*>(uc);
 #pragma unroll
@@ -725,7 +735,6 @@ template <int M1, int M2>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_gemm_fp8_kernel(const __grid_constant__ Maps m, const KParams p1, const KParams p2) {
   using C = Chain<M1>;
-  constexpr int KS = C::kStages;
   extern __shared__ uint8_t dyn_smem[];
   __shared__ SmemCtl ctl;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) &
@@ -733,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = p1.E;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < KS; ++s) {
+    for (int s = 0; s < C::kBars; ++s) {
       ptx::mbar_init(&ctl.full[s], 1);
       ptx::mbar_init(&ctl.empty[s], 1);
     }
@@ -744,12 +753,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(&ctl.stored[a], 8);  // this CTA's epilogue warps
       ptx::mbar_init(&ctl.counted[a], 1);
+      ptx::mbar_init(&ctl.aux_full[a], 1);
+      ptx::mbar_init(&ctl.aux_empty[a], 8);
       ptx::mbar_init(&ctl.tmem_full[a], 1);
       ptx::mbar_init(&ctl.tmem_empty[a], 16);  // both CTAs' epilogue warps
     }
     ptx::mbar_init(&ctl.ovl, 8);  // the four warps of each CTA that hold the shared columns
-    ptx::mbar_init(&ctl.aux_full, 1);
-    ptx::mbar_init(&ctl.aux_empty, 8);
     ptx::mbar_init(&ctl.drain, 1);
     ctl.abort = 0;
     ptx::fence_mbar_init();
@@ -803,21 +812,46 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     regs_dec<kRegsControl>();
     if (warp == 0 && lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
+      int stage = 0, i = first;
+      uint32_t phase = 0, steps = 0;
       bool ok = true;
-      for (int i = first; ok && i < total; i += stride)
-        ok = i < total1 ? producer_tile<M1, KS>(ctl, smem, p1, &m.a1, &m.s1, &m.b1, tile1(i), rank,
-                                            stage, phase)
-                        : producer_tile<M2, KS>(ctl, smem, p2, &m.a2, &m.s2, &m.b2, tile2(i), rank,
-                                            stage, phase);
-      if (!ok && rank == 0) drain_loads<KS>(ctl.full, stage, phase);  // both CTAs' loads
+      for (; ok && i < total1; i += stride) {
+        const Tile t = tile1(i);
+        steps += t.rows > 0 ? 4 : 0;
+        ok = producer_tile<M1, C::kStages1>(ctl, 0, smem, p1, &m.a1, &m.s1, &m.b1, t, rank, stage,
+                                            phase);
+      }
+      int ring = 0, ring_stages = C::kStages1;
+      if (ok && C::kAux && i < total) {
+        // the second ring takes the first one's memory and the pre-activations':
+        // wait until every stage and both steps have been read
+        for (int s = 0; ok && s < C::kStages1; ++s)
+          ok = ptx::mbar_wait(&ctl.empty[s], s < stage ? phase : phase ^ 1, &ctl.abort,
+                              kWaitLimitNs);
+        for (uint32_t n = steps > 2 ? steps - 2 : 0; ok && n < steps; ++n)
+          ok = ptx::mbar_wait(&ctl.aux_empty[n & 1], (n >> 1) & 1, &ctl.abort, kWaitLimitNs);
+        if (!ok) flag_timeout(ctl, p1.status, 13);
+        ring = C::kSecond;
+        ring_stages = C::kStages2;
+        stage = 0;
+        phase = 0;
+      }
+      for (; ok && i < total; i += stride)
+        ok = producer_tile<M2, C::kStages2>(ctl, C::kSecond, smem, p2, &m.a2, &m.s2, &m.b2,
+                                            tile2(i), rank, stage, phase);
+      if (!ok && rank == 0) drain_loads(ctl.full + ring, ring_stages, stage, phase);  // both CTAs'
     } else if (warp == 1 && rank == 0) {
       MmaState st;
+      int i = first;
       bool ok = true;
-      for (int i = first; ok && i < total; i += stride)
-        ok = i < total1 ? mma_tile<M1, KS>(ctl, ptx::smem_u32(smem), p1, tmem, st)
-                        : mma_tile<M2, KS>(ctl, ptx::smem_u32(smem), p2, tmem, st);
+      for (; ok && i < total1; i += stride)
+        ok = mma_tile<M1, C::kStages1>(ctl, 0, ptx::smem_u32(smem), p1, tmem, st);
+      if (C::kAux) {
+        st.stage = 0;
+        st.phase = 0;
+      }
+      for (; ok && i < total; i += stride)
+        ok = mma_tile<M2, C::kStages2>(ctl, C::kSecond, ptx::smem_u32(smem), p2, tmem, st);
       // no MMA may still run when TMEM is released (the same lane is elected as above)
       __syncwarp();
       if (elect_one()) ptx::umma_commit_pair(&ctl.drain, 1);
@@ -828,13 +862,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     else if (C::kAux && warp == 3 && lane == 0) {
       ptx::tma_prefetch_desc(&m.aux);
-      uint32_t tiles = 0, ph = 0;
+      uint32_t tiles = 0, step = 0;
       bool ok = true;
       for (int i = first; ok && i < total1; i += stride)
-        ok = aux_tile(ctl, smem + C::kAuxAt, p1, &m.aux, tile1(i), tiles, ph);
-      if (!ok) {  // the load in flight, if any
+        ok = aux_tile(ctl, smem + C::kAuxAt, p1, &m.aux, tile1(i), tiles, step);
+      // after an abort: the loads of the last two steps have landed
+      for (uint32_t n = step > 2 ? step - 2 : 0; !ok && n < step; ++n) {
         int none = 0;
-        ptx::mbar_wait(&ctl.aux_full, ph ^ 1, &none, kWaitLimitNs);
+        ptx::mbar_wait(&ctl.aux_full[n & 1], (n >> 1) & 1, &none, kWaitLimitNs);
       }
     } else if (warp == 2 && lane == 0) {
       uint32_t tiles = 0;
@@ -844,15 +879,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp < 12) {
     regs_inc<kRegsEpilogue>();
-    uint32_t tiles = 0, aux_ph = 0;
+    uint32_t tiles = 0, step = 0;
     bool ok = true;
     const int ew = warp - 4;
     const uint8_t* aux = smem + C::kAuxAt;
     uint4* buf = reinterpret_cast<uint4*>(smem + C::kEpiAt) + ew * 128;
     for (int i = first; ok && i < total; i += stride)
-      ok = i < total1 ? epilogue_tile<M1>(ctl, aux, buf, p1, m, tile1(i), tmem, rank, tiles, aux_ph,
+      ok = i < total1 ? epilogue_tile<M1>(ctl, aux, buf, p1, m, tile1(i), tmem, rank, tiles, step,
                                           ew, lane)
-                      : epilogue_tile<M2>(ctl, aux, buf, p2, m, tile2(i), tmem, rank, tiles, aux_ph,
+                      : epilogue_tile<M2>(ctl, aux, buf, p2, m, tile2(i), tmem, rank, tiles, step,
                                           ew, lane);
     // the buffers and the outputs must outlive the TMA stores
     if (lane == 0) ptx::bulk_wait_group0();

@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = i < total1
                  ? producer_tile<kFc1>(ctl, smem, p, &tmW1, &tmX1, &tmS1, tile1(i), stage, phase)
                  : producer_tile<kFc2>(ctl, smem, p, &tmW2, &tmX2, &tmS2, tile2(i), stage, phase);
-      if (!ok) drain_loads<kStages>(ctl.full, stage, phase);
+      if (!ok) drain_loads(ctl.full, kStages, stage, phase);
     }
     __syncwarp();
   } else if (warp == 1) {
