@@ -123,27 +123,37 @@ __global__ void __launch_bounds__(256) permute_fp8_kernel(const bf16* __restrict
 // ds (and as bf16 when d_o is given); dgates[t,j] = <dy[t], o[slot[t,j]]>.
 // Rounding to bf16 and multiplying by |g| both keep order, so a block's largest
 // |bf16(g dy)| is bf16(|g| max|dy|): one reduction over dy's block serves all k
-// rows. 256 / tpr tokens a group; thread `sub` of a token takes 8 columns, 16
+// rows. 128 / tpr tokens a group; thread `sub` of a token takes 8 columns, 16
 // threads a block. Groups are taken in turn, the next group's routing state
 // loaded beside the current rows.
-constexpr int kRowsInFlight = 8;
+//
+// A group's phases (loads, arithmetic and stores, the dot product's reduction) do
+// not overlap within a block, so many small blocks do better than few large ones:
+// on the 4096-token layer with d_o, 128 threads x 8 blocks an SM with 4 rows in
+// flight 63.5 us, 256 x 3 with 8 rows 65.1 us, 256 x 2 78 us, 64 x 12 68 us; one
+// token's 8 columns a thread over 256 threads 67 us. 353 MB at 5.56 TB/s: 0.82 of
+// the copy rate, as the bf16 gathers of this layer reach.
+constexpr int kRowsInFlight = 4;
+constexpr int kCombineThreads = 128;
+constexpr int kCombineBlocks = 8;  // resident blocks an SM, k <= 8
 
 template <int KMAX>
-__global__ void __launch_bounds__(256, KMAX <= 8 ? 3 : 1) combine_bwd_fp8_kernel(
+__global__ void __launch_bounds__(kCombineThreads, KMAX <= 8 ? kCombineBlocks : 1) combine_bwd_fp8_kernel(
     const bf16* __restrict__ dy, const bf16* __restrict__ o, const int32_t* __restrict__ slot,
     const float* __restrict__ gates, bf16* __restrict__ d_o, uint8_t* __restrict__ dq,
-    uint8_t* __restrict__ ds, float* __restrict__ dgates, int T, int H, int k, long long N, int tpr,
+    uint32_t* __restrict__ ds, float* __restrict__ dgates, int T, int H, int k, long long N, int tpr,
     int* __restrict__ zero, int nzero) {
   pdl_wait();
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < nzero; i += blockDim.x) zero[i] = 0;
-  __shared__ float s_part[8][KMAX];
-  __shared__ int s_slot[2][32 * KMAX];  // tpr >= 8: at most 32 tokens a group
-  __shared__ float s_g[2][32 * KMAX];
+  __shared__ float s_part[kCombineThreads / 32][KMAX];
+  __shared__ uint32_t s_scale[KMAX * 32];  // the group's scale words [token][j][word]: tokens x words <= 32
+  __shared__ int s_slot[2][kCombineThreads / 8 * KMAX];  // tpr >= 8
+  __shared__ float s_g[2][kCombineThreads / 8 * KMAX];
   const int tpb = blockDim.x / tpr;
   const int lt = threadIdx.x / tpr, sub = threadIdx.x % tpr;
   const int cpr = H / 8;
-  const int nb = (H + kFp8Block - 1) / kFp8Block;
+  const int nw = (H + 4 * kFp8Block - 1) / (4 * kFp8Block);  // scale words of a row
   const int ngroups = (T + tpb - 1) / tpb;
   const int nent = tpb * k;
   auto stage = [&](int buf, int grp) {
@@ -174,6 +184,9 @@ __global__ void __launch_bounds__(256, KMAX <= 8 ? 3 : 1) combine_bwd_fp8_kernel
 #pragma unroll
     for (int j = 0; j < KMAX; ++j) dot[j] = 0.f;
     bool next_staged = false;
+    // the last word's bytes past the row's blocks stay 0
+    for (int j = sub; j < k; j += tpr) s_scale[(lt * k + j) * nw + nw - 1] = 0;
+    __syncthreads();
     for (int c0 = 0; c0 < cpr; c0 += tpr) {  // the same trips for every thread: they shuffle
       const int c = c0 + sub;
       const bool ok = active && c < cpr;
@@ -223,13 +236,8 @@ __global__ void __launch_bounds__(256, KMAX <= 8 ? 3 : 1) combine_bwd_fp8_kernel
           const float inv = fp8_inv_scale(b);
           *reinterpret_cast<uint2*>(dq + (size_t)sv * H + 8 * c) =
               make_uint2(fp8x4_of_bf16(pw[0], pw[1], inv), fp8x4_of_bf16(pw[2], pw[3], inv));
-          if ((c & 15) == 0) {
-            const int kb = c >> 4;
-            ds[((size_t)(kb >> 2) * N + sv) * 4 + (kb & 3)] = (uint8_t)b;
-            if (kb == nb - 1)  // the bytes that fill up the last word
-              for (int z = kb + 1; z & 3; ++z)
-                ds[((size_t)(kb >> 2) * N + sv) * 4 + (z & 3)] = 0;
-          }
+          if ((c & 15) == 0)
+            reinterpret_cast<uint8_t*>(s_scale)[(lt * k + j) * 4 * nw + (c >> 4)] = (uint8_t)b;
           if (d_o)
             __stcs(reinterpret_cast<uint4*>(d_o + (size_t)sv * H) + c,
                    make_uint4(pw[0], pw[1], pw[2], pw[3]));
@@ -263,6 +271,12 @@ __global__ void __launch_bounds__(256, KMAX <= 8 ? 3 : 1) combine_bwd_fp8_kernel
         dgates[(size_t)t * k + sub] = sum;
       }
     }
+    if (tpr <= 32) __syncthreads();  // (longer rows have met above)
+    // whole scale words: their bytes come from several warps
+    for (int i = threadIdx.x; i < nent * nw; i += blockDim.x) {
+      const int ent = i / nw, w = i % nw, sv = s_slot[buf][ent];
+      if (sv >= 0) ds[(size_t)w * N + sv] = s_scale[i];
+    }
     __syncthreads();
   }
 }
@@ -273,9 +287,10 @@ cudaError_t launch_combine_bwd_fp8_t(const moe_layer_desc_t& d, int groups, cons
                                      bf16* d_o, uint8_t* dq, uint8_t* ds, float* dgates, int tpr,
                                      int* zero, int nzero, cudaStream_t st) {
   // one wave of resident blocks, each taking token groups in turn
-  const int grid = std::min(groups, (KMAX <= 8 ? 3 : 1) * device_sm_count());
-  return launch_k(combine_bwd_fp8_kernel<KMAX>, grid, 256, 0, st, dy, o, slot, gates, d_o, dq, ds,
-                  dgates, d.T, d.H, d.k, (long long)d.T * d.k, tpr, zero, nzero);
+  const int grid = std::min(groups, (KMAX <= 8 ? kCombineBlocks : 1) * device_sm_count());
+  return launch_k(combine_bwd_fp8_kernel<KMAX>, grid, kCombineThreads, 0, st, dy, o, slot, gates, d_o, dq,
+                  reinterpret_cast<uint32_t*>(ds), dgates, d.T, d.H, d.k, (long long)d.T * d.k, tpr,
+                  zero, nzero);
 }
 
 moe_status_t launched(cudaError_t e, const char* what) {
@@ -324,9 +339,11 @@ moe_status_t launch_combine_bwd_fp8(const moe_layer_desc_t& d, const bf16* dy, c
                                     uint8_t* dq, uint8_t* ds, float* dgates, cudaStream_t st,
                                     int* zero, int nzero) {
   if (d.T == 0) return MOE_OK;
-  int tpr = 8;  // threads of a token: a power of two >= H / 8, at most 256
-  while (tpr < d.H / 8 && tpr < 256) tpr <<= 1;
-  const int groups = ceil_div(d.T, 256 / tpr);
+  // threads of a token: a power of two >= H / 16, at most a block, at least the 16
+  // that hold a block of 128 columns
+  int tpr = d.H > 64 ? 16 : 8;
+  while (tpr < d.H / 16 && tpr < kCombineThreads) tpr <<= 1;
+  const int groups = ceil_div(d.T, kCombineThreads / tpr);
   cudaError_t e;
   {
     LaunchScope _ls(K_FP8_COMBINE_BWD, st);
