@@ -356,33 +356,34 @@ def _fp8_refuse(what, name, t, dt, n, dev):
     raise MoeError(MOE_ERR_INVALID_ARG, what, f"{name} {why}")
 
 
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _fp8_args(what: str, *args):
     """Checks (name, tensor, dtype, least number of elements) of a call: contiguous
     tensors of that type on the current device, or None where the size is negative
     (optional). Returns their addresses."""
-    dev, out = None, []
+    first = args[0][1]
+    dev = _get_device() if first is not None and first.is_cuda else -2
+    out = []
     for name, t, dt, n in args:
         if t is None:
             if n >= 0:
                 _fp8_refuse(what, name, t, dt, n, dev)
             out.append(None)
-            continue
-        if dev is None:
-            dev = torch.cuda.current_device() if t.is_cuda else -2
-        if (t.dtype is not dt or t.get_device() != dev or not t.is_contiguous()
-                or t.numel() < abs(n)):
+        elif (t.dtype is dt and t.get_device() == dev and t.is_contiguous()
+              and t.numel() >= (n if n >= 0 else -n)):
+            out.append(t.data_ptr())
+        else:
             _fp8_refuse(what, name, t, dt, n, dev)
-        out.append(t.data_ptr())
     return out
-
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _fp8_stream(stream):
     """As _s, without building a Stream object for the current stream (2 us less a call)."""
     if stream is None and _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_get_device())
     return _s(stream)
 
 

@@ -36,11 +36,6 @@ __device__ __forceinline__ uint32_t fp8_scale_byte(uint32_t amax_bits) {
   const uint32_t e = (amax_bits + 0x1FFFFFu) >> 23;
   return e > 8u ? e - 8u : 0u;
 }
-// 1 / scale, exact for b <= 247 (no finite block needs more); NaN for b = 255,
-// which turns every value of the block into e4m3's NaN.
-__device__ __forceinline__ float fp8_inv_scale(uint32_t b) {
-  return __uint_as_float(b == 255u ? 0x7FFFFFFFu : (254u - b) << 23);
-}
 __device__ __forceinline__ uint32_t fp8x4(float a, float b, float c, float d) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
@@ -48,18 +43,30 @@ __device__ __forceinline__ uint32_t fp8x4(float a, float b, float c, float d) {
 }
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-// four bf16 (two words) scaled by inv -> four e4m3
-__device__ __forceinline__ uint32_t fp8x4_of_bf16(uint32_t w0, uint32_t w1, float inv) {
-  return fp8x4(bf16_lo(w0) * inv, bf16_hi(w0) * inv, bf16_lo(w1) * inv, bf16_hi(w1) * inv);
+// 1 / scale as two packed bf16, exact for b <= 247 (no finite block needs more):
+// 2^(127 - b) has an exponent field of 254 - b >= 7. NaN for b = 255, which turns
+// every value of the block into e4m3's NaN.
+__device__ __forceinline__ uint32_t fp8_inv_scale2(uint32_t b) {
+  return b == 255u ? 0x7FFF7FFFu : (254u - b) * 0x00800080u;
 }
-// Largest magnitude of two packed pairs of bf16, as packed bit patterns: with
-// the sign cleared, bf16 patterns order like unsigned integers, NaN on top.
+// Four bf16 (two words) scaled by inv2 -> four e4m3. The bf16 products are exact:
+// a power of two moves exponents alone, and what falls below bf16's normal range
+// is far below e4m3's smallest step.
+__device__ __forceinline__ uint32_t fp8x4_of_bf16(uint32_t w0, uint32_t w1, uint32_t inv2) {
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(w0) : "r"(inv2));
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(w1) : "r"(inv2));
+  return fp8x4(bf16_lo(w0), bf16_hi(w0), bf16_lo(w1), bf16_hi(w1));
+}
+// Larger magnitude in each half of two packed pairs of bf16 (its sign bit is
+// arbitrary); NaN if either is.
 __device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t m, uint32_t w) {
-  return __vmaxu2(m, w & 0x7FFF7FFFu);
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w));
+  return m;
 }
-// fp32 bits of the larger half of a packed maximum
+// fp32 bits of the larger half of a packed maximum: without signs, bf16 patterns
+// order like unsigned integers, NaN on top
 __device__ __forceinline__ uint32_t absmax_bits(uint32_t m) {
-  const uint32_t lo = m << 16, hi = m & 0xFFFF0000u;
+  const uint32_t lo = (m << 16) & 0x7FFF0000u, hi = m & 0x7FFF0000u;
   return lo > hi ? lo : hi;
 }
 

@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(WeightMat m1, Wei
 #pragma unroll
   for (int i = 0; i < 8; ++i) mx = max(mx, s_max[i]);
   const uint32_t b = fp8_scale_byte(mx);
-  const float inv = fp8_inv_scale(b);
+  const uint32_t inv = fp8_inv_scale2(b);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (cok && row + 32 * i < m.R) {
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(256) permute_fp8_kernel(const bf16* __restrict
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     const uint32_t b = fp8_scale_byte(m);
-    const float inv = fp8_inv_scale(b);
+    const uint32_t inv = fp8_inv_scale2(b);
     const uint4 q = make_uint4(fp8x4_of_bf16(a.x, a.y, inv), fp8x4_of_bf16(a.z, a.w, inv),
                                fp8x4_of_bf16(c.x, c.y, inv), fp8x4_of_bf16(c.z, c.w, inv));
     uint32_t word = 0;
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kCombineThreads, KMAX <= 8 ? kCombineBlocks : 
           dot[j] += d;
           const float pm = __bfloat162float(__float2bfloat16_rn(fabsf(gj) * ymax));
           const uint32_t b = fp8_scale_byte(__float_as_uint(pm) & 0x7FFFFFFFu);
-          const float inv = fp8_inv_scale(b);
+          const uint32_t inv = fp8_inv_scale2(b);
           *reinterpret_cast<uint2*>(dq + (size_t)sv * H + 8 * c) =
               make_uint2(fp8x4_of_bf16(pw[0], pw[1], inv), fp8x4_of_bf16(pw[2], pw[3], inv));
           if ((c & 15) == 0)
@@ -343,6 +343,10 @@ moe_status_t launch_combine_bwd_fp8(const moe_layer_desc_t& d, const bf16* dy, c
   // that hold a block of 128 columns
   int tpr = d.H > 64 ? 16 : 8;
   while (tpr < d.H / 16 && tpr < kCombineThreads) tpr <<= 1;
+  // while all tokens fit one wave, twice the threads: latency counts, not the rate
+  if (tpr < d.H / 8 && tpr < kCombineThreads &&
+      ceil_div(d.T, kCombineThreads / (2 * tpr)) <= kCombineBlocks * device_sm_count() / 2)
+    tpr *= 2;
   const int groups = ceil_div(d.T, kCombineThreads / tpr);
   cudaError_t e;
   {

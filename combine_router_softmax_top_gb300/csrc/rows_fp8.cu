@@ -53,6 +53,7 @@ struct RowsParams {
   uint8_t *hq, *hs;
   bf16* o;
   int *status, *dep;
+  int w2;             // FC2 columns of a tile: 256, or 128 when there are few tiles (set on the device)
 };
 
 struct Tile {
@@ -78,7 +79,7 @@ __device__ __forceinline__ int kblocks(const RowsParams& p) {
 }
 template <int G>
 __device__ __forceinline__ int ncols(const RowsParams& p) {  // column blocks of an expert
-  return G == kFc1 ? (p.F + 127) / 128 : (p.H + 255) / 256;
+  return G == kFc1 ? (p.F + 127) / 128 : (p.H + p.w2 - 1) / p.w2;
 }
 
 template <int G>
@@ -90,7 +91,7 @@ __device__ __forceinline__ Tile tile_at(const RowsParams& p, const SmemCtl& c, i
   const int cnt = c.off[cursor + 1] - c.off[cursor];
   const int local = i - c.rtile[cursor] * nc, nt = (cnt + NT - 1) / NT;
   const int r = (local % nt) * NT;  // row tiles fastest: they share the weights
-  t.n0 = (local / nt) * (G == kFc1 ? 128 : 256);
+  t.n0 = (local / nt) * (G == kFc1 ? 128 : p.w2);
   t.row = (long long)c.off[cursor] + r;
   t.rows = min(NT, cnt - r);
   return t;
@@ -118,7 +119,7 @@ __device__ __forceinline__ bool wait_expert(SmemCtl& c, const RowsParams& p, int
 // M tiles of a tile: the second one is past the edge when 128 columns or fewer are left
 template <int G>
 __device__ __forceinline__ int mtiles(const RowsParams& p, const Tile& t) {
-  return G == kFc1 || t.n0 + 128 < p.H ? 2 : 1;
+  return G == kFc1 || (p.w2 == 256 && t.n0 + 128 < p.H) ? 2 : 1;
 }
 
 template <int G>
@@ -319,7 +320,7 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const RowsParams& p, c
       const uint32_t m = max(max((uint32_t)c.amax[0][r], (uint32_t)c.amax[1][r]),
                              max((uint32_t)c.amax[2][r], (uint32_t)c.amax[3][r]));
       const uint32_t b = fp8_scale_byte(m << 16);
-      const float inv = fp8_inv_scale(b);
+      const uint32_t inv = fp8_inv_scale2(b);
       const size_t row = (size_t)(t.row + r);
       if (t.n0 + cc < p.F) {
         const uint4 v0 = c.h[r][(i & 7) * 2], v1 = c.h[r][(i & 7) * 2 + 1];
@@ -340,9 +341,9 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const RowsParams& p, c
       atomicAdd(p.dep + t.e, 1);
     }
   } else {
-    for (int m = 0; m < 2; ++m) {
+    const int mt = mtiles<G>(p, t);
+    for (int m = 0; m < mt; ++m) {
       const int h = t.n0 + 128 * m + col;
-      if (t.n0 + 128 * m >= p.H) break;
       for (int r0 = 0; r0 < t.rows; r0 += 8) {
         uint32_t v[8];
         tmem_ld_x8(tbase + NT * m + r0, v);
@@ -365,11 +366,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap tmS1,
                         const __grid_constant__ CUtensorMap tmW2,
                         const __grid_constant__ CUtensorMap tmX2,
-                        const __grid_constant__ CUtensorMap tmS2, const RowsParams p) {
+                        const __grid_constant__ CUtensorMap tmS2, const RowsParams args) {
   extern __shared__ uint8_t dyn_smem[];
   __shared__ SmemCtl ctl;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) &
                                              ~uintptr_t(1023));
+  RowsParams p = args;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -417,6 +419,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
+  // one token of the 128-expert layer has 64 second tiles of 256 columns: half of
+  // the SMs would have none
+  p.w2 = ctl.rtile[p.E] * ((p.H + 255) / 256) < (int)gridDim.x ? 128 : 256;
   const int total1 = ctl.rtile[p.E] * ncols<kFc1>(p);
   const int total = total1 + ctl.rtile[p.E] * ncols<kFc2>(p);
   int cur1 = 0, cur2 = 0;
@@ -501,13 +506,13 @@ moe_status_t launch_ffn_rows_fp8(const moe_layer_desc_t& d, const uint8_t* xq, c
       !make_map(&m[3], w.w2q, 2, d.F, (long long)d.E * d.H, 1, 128, 1) ||
       !make_map(&m[4], hq, 2, d.F, N, 1, NT, 1) || !make_map(&m[5], hq, 2, d.F, N, 1, kSmallBox, 1))
     return MOE_ERR_CUDA;
-  const RowsParams p = {d.E, d.H, d.F, N, off, xs, w, a, h, hq, hs, o, status, dep};
+  const RowsParams p = {d.E, d.H, d.F, N, off, xs, w, a, h, hq, hs, o, status, dep, 0};
   cudaError_t e = set_up();
   if (e == cudaSuccess && !counters_zeroed) e = launch_zero_counters(dep, d.E, st);
   // one CTA per SM (all resident: second tiles wait for first ones), fewer when
   // there cannot be as many tiles
   const long long rows = N / NT + std::min<long long>(N, d.E);
-  const long long tiles = rows * (fp8_blocks(d.F) + ceil_div(d.H, 256));
+  const long long tiles = rows * (fp8_blocks(d.F) + fp8_blocks(d.H));
   const int grid = (int)std::min<long long>(device_sm_count(), tiles);
   if (e == cudaSuccess) {
     LaunchScope _ls(K_FP8_ROWS_FFN, st);
