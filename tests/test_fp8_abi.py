@@ -58,6 +58,16 @@ def test_small_workspace(L, name):
     assert b"workspace" in L.moe_last_error()
 
 
+@pytest.mark.parametrize("name,at", [("moe_expert_ffn_fwd_fp8", (7, 8, 9, 11)),
+                                     ("moe_expert_ffn_bwd_dgrad_fp8", (2, 8, 9, 11))])
+def test_rows_moved_in_sectors_are_32_byte_aligned(L, name, at):
+    for i in at:
+        args = [P] * 13
+        args[i] = ctypes.c_void_p(4096 + 16)
+        assert call(L, name, args) == moe.MOE_ERR_INVALID_ARG, i
+        assert b"32-byte aligned" in L.moe_last_error()
+
+
 def test_scale_bytes(L):
     assert moe.moe_fp8_scale_bytes(10, 1) == 40 and moe.moe_fp8_scale_bytes(10, 4) == 40
     assert moe.moe_fp8_scale_bytes(10, 5) == 80 and moe.moe_fp8_scale_bytes(0, 5) == 0

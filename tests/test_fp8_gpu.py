@@ -153,6 +153,19 @@ CASES = {
     "max_inner": dict(T=40, H=128, E=2, k=2, F=16384),
     "few_rows_odd": dict(T=3, H=704, E=12, k=5, F=320),
     "long_expert": dict(T=700, H=256, E=2, k=2, F=384),
+    # few rows an expert on average, a hundred at some: several row tiles
+    "few_rows_skewed": dict(T=100, H=320, E=32, k=8, F=448),
+    # more than few on average: the 256-row tiles at the largest sizes
+    "max_hidden_many_rows": dict(T=64, H=16384, E=1, k=1, F=64),
+    "max_inner_many_rows": dict(T=64, H=64, E=1, k=1, F=16384),
+    # exactly a tile, one row less and one more
+    "tile_256": dict(T=256, H=128, E=1, k=1, F=128),
+    "tile_255": dict(T=255, H=128, E=1, k=1, F=192),
+    "tile_257": dict(T=257, H=192, E=1, k=1, F=128),
+    "tile_129": dict(T=129, H=128, E=1, k=1, F=320),
+    # many tiles a CTA pair: every ring and accumulator wraps
+    "many_tiles": dict(T=3000, H=512, E=8, k=2, F=576),
+    "empty_and_long": dict(T=1500, H=256, E=24, k=1, F=256),
 }
 
 
@@ -513,6 +526,87 @@ def test_captured_and_replayed(T):
         torch.cuda.synchronize()
         for x, y in zip(got, (c.o, c.dgates, c.dx)):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("wgrad", [True, False])
+def test_layer_captured_and_replayed(wgrad):
+    """Forward and backward of the layer (the side stream's fork and join inside) in one graph."""
+    inp = moe_synth.make_inputs(T=200, H=128, E=8, k=2, F=192, seed=38)
+    d = moe.LayerDesc.of(**inp.shape_dict())
+    b, q = moe.LayerBuffers(d), moe.Fp8Buffers(d)
+    b.load_inputs(inp)
+    q.quantize_weights(b.w1, b.w2)
+
+    def run():
+        moe.moe_layer_forward_fp8(d, b, q)
+        moe.moe_layer_backward_fp8(d, b, q, run_wgrad=wgrad)
+
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    other = moe_synth.make_inputs(T=200, H=128, E=8, k=2, F=192, seed=39)
+    b.x.copy_(other.x)
+    b.dy.copy_(other.dy)
+    g.replay()
+    torch.cuda.synchronize()
+    got = [t.clone() for t in (b.y, b.dx, b.dw_r, b.dw1, b.dw2)]
+    run()
+    torch.cuda.synchronize()
+    assert moe.moe_device_status(d, b.ws) == moe.MOE_OK
+    for x, y in zip(got, (b.y, b.dx, b.dw_r, b.dw1, b.dw2)):
+        assert torch.equal(x, y)
+
+
+# ----------------------------------------------------------------------------- offsets past 32 bits
+def test_buffers_past_32_bits():
+    """Rows whose element offsets pass 2^31 in every buffer: the last rows against the oracle."""
+    T, H, E, k, F = 75000, 4096, 8, 8, 64
+    N = T * k
+    assert N * H > 2 ** 31
+    d = moe.LayerDesc.of(T, H, E, k, F)
+    g = torch.Generator(device="cuda").manual_seed(40)
+    rnd = lambda *s, std=1.0: (torch.randn(*s, generator=g, device="cuda") * std).to(torch.bfloat16)  # noqa: E731
+    q = moe.Fp8Buffers(d)
+    q.quantize_weights(rnd(E, 2 * F, H, std=0.02), rnd(E, H, F, std=0.05))
+    x = rnd(T, H)
+    # every token to every expert: row s of expert e is token s - e T
+    off = (torch.arange(E + 1, device="cuda") * T).to(torch.int32)
+    slot = (torch.arange(T, device="cuda")[:, None] + T * torch.arange(E, device="cuda")).to(torch.int32)
+    gates = torch.full((T, k), 0.125, device="cuda")
+    new = lambda c: torch.zeros(N, c, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    a, h, o, d_o, dx = new(2 * F), new(F), new(H), new(H), new(H)
+    dgates = torch.zeros(T, k, device="cuda")
+    ws = torch.zeros(moe.moe_workspace_size(d), dtype=torch.uint8, device="cuda")
+    w = (q.w1q, q.w1s, q.w2q, q.w2s)
+    moe.moe_permute_fp8(d, x, slot, q.xq, q.xs)
+    moe.moe_expert_ffn_fwd_fp8(d, q.xq, q.xs, off, *w, a, h, q.hq, q.hs, o, ws)
+    moe.moe_combine_bwd_fp8(d, x, o, slot, gates, d_o, q.dq, q.ds, dgates)
+    moe.moe_expert_ffn_bwd_dgrad_fp8(d, q.dq, q.ds, a, off, *w, None, q.daq, q.das, dx, ws)
+    assert moe.moe_device_status(d, ws) == moe.MOE_OK
+    rows = np.r_[N - 40:N]  # of the last expert
+    w1 = O.values_weights(q64(q.w1q[-1]).reshape(2, F, H), q.w1s[-1].cpu().numpy().astype(np.int64)).reshape(1, 2 * F, H)
+    w2 = O.values_weights(q64(q.w2q[-1:]), q.w2s[-1:].cpu().numpy().astype(np.int64))
+    one = np.array([0, len(rows)])
+    tail = lambda t: np64(t[N - 40:])  # noqa: E731
+    scales = lambda s, nb: O.unpack_words(s[:, N - 40:].cpu().numpy(), nb)  # noqa: E731
+    ref, b = O.quantize_rows(np64(x[T - 40:]))
+    same("xq", q64(q.xq[N - 40:]), ref)
+    same("xs", scales(q.xs, H // 128), b)
+    xv = O.values_rows(ref, b)
+    close("a", tail(a), O.grouped(xv, one, w1), H * U32 * O.grouped(np.abs(xv), one, np.abs(w1)))
+    hq, hb = O.quantize_rows(tail(h))
+    same("hq", q64(q.hq[N - 40:]), hq)
+    hv = O.values_rows(hq, hb)
+    close("o", tail(o), O.grouped(hv, one, w2), F * U32 * O.grouped(np.abs(hv), one, np.abs(w2)))
+    same("d_o", tail(d_o), O.bf16(0.125 * np64(x[T - 40:])))
+    dq, db = O.quantize_rows(tail(d_o))
+    same("dq", q64(q.dq[N - 40:]), dq)
+    same("ds", scales(q.ds, H // 128), db)
+    dv = O.values_rows(q64(q.daq[N - 40:]).reshape(80, F), scales(q.das, 2).reshape(80, 1)).reshape(40, 2 * F)
+    w1t = np.swapaxes(w1, 1, 2)
+    close("dx", tail(dx), O.grouped(dv, one, w1t), 2 * F * U32 * O.grouped(np.abs(dv), one, np.abs(w1t)))
 
 
 # ----------------------------------------------------------------------------- the whole layer
