@@ -91,7 +91,7 @@ struct Fp8Weights {
 moe_status_t launch_ffn_fwd_fp8(const moe_layer_desc_t& d, const uint8_t* xq, const uint8_t* xs,
                                 const int32_t* off, const Fp8Weights& w, bf16* a, bf16* h,
                                 uint8_t* hq, uint8_t* hs, bf16* o, int* status, int* dep,
-                                cudaStream_t st, bool counters_zeroed = false);
+                                cudaStream_t st);
 // The forward for few rows an expert (rows_fp8.cu), which launch_ffn_fwd_fp8 takes
 // up to kFp8FewRows rows an expert on average. Measured, this kernel against the
 // GEMM chain, us: 128 experts (H 2048, F 768) at 4 rows an expert 90 / 114, 16
@@ -101,11 +101,11 @@ constexpr long long kFp8FewRows = 48;
 moe_status_t launch_ffn_rows_fp8(const moe_layer_desc_t& d, const uint8_t* xq, const uint8_t* xs,
                                  const int32_t* off, const Fp8Weights& w, bf16* a, bf16* h,
                                  uint8_t* hq, uint8_t* hs, bf16* o, int* status, int* dep,
-                                 cudaStream_t st, bool counters_zeroed);
+                                 cudaStream_t st);
 // Expert FFN activation gradient: da (bf16) is written when given.
 moe_status_t launch_ffn_dgrad_fp8(const moe_layer_desc_t& d, const uint8_t* dq, const uint8_t* ds,
                                   const bf16* a, const int32_t* off, const Fp8Weights& w, bf16* da,
                                   uint8_t* daq, uint8_t* das, bf16* dx_perm, int* status, int* dep,
-                                  cudaStream_t st, bool counters_zeroed = false);
+                                  cudaStream_t st);
 
 }  // namespace moe

@@ -153,10 +153,8 @@ moe_status_t moe_layer_forward_fp8(const moe_layer_desc_t* d, const moe_mb_bufs_
   const WsLayout w = ws_layout(*d);
   char* ws = static_cast<char*>(b->ws);
   cudaStream_t st = S(stream);
-  bool zeroed = false;  // the fused dispatch clears the expert products' counters
   if (save) {
     MOE_CHECK(op_dispatch(*d, b, st));
-    zeroed = d->T > 0 && d->E <= 128;
   } else {
     float* z = b->logits ? b->logits : reinterpret_cast<float*>(ws + w.logits);
     MOE_CHECK(launch_route(*d, BF(b->x), BF(b->w_r), b->bias, z, b->idx, b->gates,
@@ -168,7 +166,7 @@ moe_status_t moe_layer_forward_fp8(const moe_layer_desc_t* d, const moe_mb_bufs_
   MOE_CHECK(launch_permute_fp8(*d, BF(b->x), b->slot, q->xq, q->xs, st));
   MOE_CHECK(launch_ffn_fwd_fp8(*d, q->xq, q->xs, b->off, weights(q), save ? BFW(b->a) : nullptr,
                                save ? BFW(b->h) : nullptr, q->hq, q->hs, BFW(b->o),
-                               status_of(b->ws), dep_of(*d, b->ws), st, zeroed));
+                               status_of(b->ws), dep_of(*d, b->ws), st));
   return op_combine_mb(*d, b, st);
 }
 
@@ -191,12 +189,12 @@ moe_status_t moe_layer_backward_fp8(const moe_layer_desc_t* d, const moe_mb_bufs
   }
   MOE_CHECK(check_ws(*d, b->ws, b->ws_bytes));
   cudaStream_t st = S(stream);
-  // it clears the counters of the chain and of dW_r that follow
+  // it clears dW_r's chunk counters, which follow the experts' counters
   MOE_CHECK(launch_combine_bwd_fp8(*d, BF(b->dy), BF(b->o), b->slot, b->gates, BFW(b->d_o), q->dq,
-                                   q->ds, b->dgates, st, dep_of(*d, b->ws), dep_ints(*d)));
+                                   q->ds, b->dgates, st, dep_of(*d, b->ws) + d->E, dep_ints(*d) - d->E));
   MOE_CHECK(launch_ffn_dgrad_fp8(*d, q->dq, q->ds, BF(b->a), b->off, weights(q), BFW(b->da),
                                  q->daq, q->das, BFW(b->dx_perm), status_of(b->ws),
-                                 dep_of(*d, b->ws), st, true));
+                                 dep_of(*d, b->ws), st));
   if (!run_wgrad) return op_dispatch_bwd_mb(*d, b, st);
   if (profiling_active()) {
     MOE_CHECK(op_dispatch_bwd_mb(*d, b, st));

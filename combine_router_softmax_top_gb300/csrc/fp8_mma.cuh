@@ -84,6 +84,24 @@ __device__ __forceinline__ int ld_acquire(const int* p) {
   asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
+// As ptx::mbar_wait, acquiring what another CTA of the cluster released.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
+                                                  volatile int* abort) {
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(ptx::smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((i & 63) == 0 && (*abort || ptx::globaltimer_ns() - t0 > kWaitLimitNs)) return false;
+  }
+}
+
 // After an abort: waits (bounded) until the loads that a producer has issued have
 // landed, so that none writes into shared memory that is no longer this
 // kernel's. stage, phase: the producer's place in the ring.
@@ -160,8 +178,10 @@ inline bool make_rows_map(CUtensorMap* m, const void* base, long long rows, long
   return true;
 }
 
-// Clears n <= 256 counters on the stream.
-cudaError_t launch_zero_counters(int* dep, int n, cudaStream_t st);
+// Clears n <= 256 counters and the tile counter on the stream.
+cudaError_t launch_zero_counters(int* dep, int n, int* tile, cudaStream_t st);
+// The tile counter of a workspace: a word after the status words, in their area.
+inline int* tile_counter(int* status) { return status + 2 * ST_NUM; }
 
 }  // namespace fp8
 }  // namespace moe

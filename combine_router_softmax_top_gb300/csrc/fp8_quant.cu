@@ -366,16 +366,17 @@ namespace {
 
 // Clears the counters. A kernel rather than a memset, so that the chain's set-up
 // overlaps it (programmatic dependent launch).
-__global__ void __launch_bounds__(256) zero_counters_kernel(int* dep, int n) {
+__global__ void __launch_bounds__(256) zero_counters_kernel(int* dep, int n, int* tile) {
   pdl_wait();
+  if (threadIdx.x == 0) *tile = 0;
   if ((int)threadIdx.x < n) dep[threadIdx.x] = 0;
 }
 
 }  // namespace
 
-cudaError_t launch_zero_counters(int* dep, int n, cudaStream_t st) {
+cudaError_t launch_zero_counters(int* dep, int n, int* tile, cudaStream_t st) {
   LaunchScope _ls(K_FP8_ZERO, st);
-  return launch_k(zero_counters_kernel, 1, 256, 0, st, dep, n);
+  return launch_k(zero_counters_kernel, 1, 256, 0, st, dep, n, tile);
 }
 
 }  // namespace fp8

@@ -24,10 +24,11 @@
 //   warps 4..11 epilogue: TMEM -> registers -> SwiGLU (or its gradient),
 //               rounding, block maxima, e4m3 -> global; two warps per TMEM lane
 //               quarter, each owning 64 of every 128 columns
-// The first GEMM's tiles come first; a tile of the second starts once every
-// tile of its expert in the first has been stored (per-expert counters). All
-// CTAs are resident and meet their first tiles before any second, so the waits
-// end.
+// Tiles are claimed in order from a counter, the first GEMM's before the second's
+// (the odd CTA's warp 1 claims for the pair, two tiles ahead). A tile of the second
+// GEMM starts once every tile of its expert in the first has been stored
+// (per-expert counters): those have been claimed before it by pairs that are
+// running, so the wait ends however many pairs are resident beside other work.
 //
 // TMEM: two 256-column accumulators and four buffers of 12 scale columns do not
 // fit 512 columns, so the accumulators share 64: columns 0..255 and 192..447.
@@ -112,6 +113,7 @@ struct KParams {
   uint8_t* s;         // hs | das
   int* status;
   int* dep;           // per-expert count of first-GEMM tiles stored, by CTA
+  int* tile;          // tiles claimed
   int halves;         // FC2 dgrad: 128-column halves that a tile's epilogue stores (set on the device)
 };
 
@@ -138,8 +140,11 @@ struct Tile {
 struct SmemCtl {
   uint64_t full[kMaxBars], empty[kMaxBars];
   uint64_t aux_full[2], aux_empty[2];
+  uint64_t paired[4];  // both warps of a quarter have left their block maxima
   uint64_t sf_full[kSf], sf_empty[kSf];
   uint64_t tmem_full[2], tmem_empty[2], ovl, drain;
+  uint64_t sched_full[2], sched_empty[2];  // claimed tiles
+  int sched[2];
   uint64_t stored[2], counted[2];  // a first-GEMM tile's stores issued; counted for its expert
   uint32_t tmem_base;
   int abort;
@@ -264,6 +269,49 @@ __device__ __forceinline__ bool wait_expert(SmemCtl& c, const KParams& p, int e)
   return true;
 }
 
+// ================================================================ tiles
+// What reads the claimed tiles: producer, counting warp, scale and epilogue warps
+// in both CTAs, the MMA issuer in one (and the gradient's aux loaders).
+constexpr int kReaders = 2 * (1 + 1 + 4 + 8) + 1;
+__device__ __forceinline__ void arrive_remote(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
+               : "memory");
+}
+// The n-th tile claimed for this pair (past the last: none is left; -1: gave up).
+// Every lane of a warp that passes warp = true calls it together.
+__device__ __forceinline__ int next_tile(SmemCtl& c, uint32_t n, int* status, bool warp) {
+  bool ok = mbar_wait_cluster(&c.sched_full[n & 1], (n >> 1) & 1, &c.abort);
+  if (warp) ok = __all_sync(0xffffffffu, ok);
+  if (!ok) {
+    flag_timeout(c, status, 14);
+    return -1;
+  }
+  const int i = *(volatile int*)&c.sched[n & 1];
+  if (warp) __syncwarp();
+  // the slot is free once it has been read: the address depends on what was (never
+  // negative), so that the relaxed arrival cannot pass the load
+  if (!warp || (threadIdx.x & 31) == 0)
+    arrive_remote(ptx::mapa_shared(&c.sched_empty[n & 1], 1) + (uint32_t)min(i, 0));
+  return i;
+}
+// Claims tiles for the pair until none is left (one thread of the odd CTA).
+__device__ __forceinline__ void claim_tiles(SmemCtl& c, const KParams& p, int total) {
+  for (uint32_t n = 0;; ++n) {
+    if (!mbar_wait_cluster(&c.sched_empty[n & 1], ((n >> 1) & 1) ^ 1, &c.abort)) {
+      flag_timeout(c, p.status, 15);
+      return;
+    }
+    const int i = min(atomicAdd(p.tile, 1), total);
+    c.sched[n & 1] = i;
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(ptx::mapa_shared(&c.sched[n & 1], 0)),
+                 "r"(i)
+                 : "memory");
+    ptx::mbar_arrive_cluster(ptx::mapa_shared(&c.sched_full[n & 1], 0));
+    ptx::mbar_arrive_cluster(ptx::mapa_shared(&c.sched_full[n & 1], 1));
+    if (i == total) return;
+  }
+}
+
 // ================================================================ producer
 // Bytes of A loaded for a CTA's `rows` valid rows: rows that no expert has are not
 // fetched (what the buffer held stays in the unused rows of the product).
@@ -335,13 +383,9 @@ __device__ __forceinline__ bool producer_tile(SmemCtl& c, int ring, uint8_t* sme
 }
 
 // ================================================================ scales
-// What these arrivals order are TMEM accesses, complete when their waits return:
-// no earlier memory operation needs to be released to the other CTA.
-__device__ __forceinline__ void arrive_remote(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
-               : "memory");
-}
-// One arrival on the even CTA's barrier, after this warp's TMEM accesses.
+// One arrival on the even CTA's barrier, after this warp's TMEM accesses. Those are
+// complete when their waits return: no earlier memory operation needs to be
+// released to the other CTA.
 __device__ __forceinline__ void release(uint64_t* bar, uint32_t rank, int lane) {
   ptx::tc_fence_before();
   __syncwarp();
@@ -484,10 +528,17 @@ __device__ __forceinline__ bool mma_tile(SmemCtl& c, int ring, uint32_t smem, co
 // Larger of this thread's and its partner warp's block maximum (the same row,
 // the other 64 columns), as fp32 bits. buf alternates between calls, so that a
 // warp never overwrites a value that its partner has yet to read: it passes the
-// next call's barrier only after the partner has read this call's.
-__device__ __forceinline__ uint32_t pair_max(SmemCtl& c, uint32_t m, int ew, int lane, int buf) {
+// next call's barrier only after the partner has read this call's. (An mbarrier, as
+// its wait ends after an abort when the partner does not come. n counts the calls.)
+__device__ __forceinline__ uint32_t pair_max(SmemCtl& c, const KParams& p, uint32_t m, int ew,
+                                             int lane, uint32_t& n) {
+  const int buf = n & 1;
+  uint64_t* bar = &c.paired[ew & 3];
   c.amax[buf][ew][lane] = m;
-  asm volatile("bar.sync %0, 64;" ::"r"(1 + (ew & 3)) : "memory");
+  __syncwarp();
+  if (lane == 0) ptx::mbar_arrive(bar);
+  if (!ptx::mbar_wait(bar, buf, &c.abort, kWaitLimitNs)) flag_timeout(c, p.status, 16);
+  ++n;
   return max(m, c.amax[buf][ew ^ 4][lane]);
 }
 
@@ -529,7 +580,7 @@ template <int MODE>
 __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const uint8_t* aux, uint4* buf,
                                               const KParams& p, const Maps& m, const Tile& t,
                                               uint32_t tmem, uint32_t rank, uint32_t& tiles,
-                                              uint32_t& step, int ew, int lane) {
+                                              uint32_t& step, uint32_t& pairs, int ew, int lane) {
   const int q = ew & 3, hf = ew >> 2;
   const int acc = tiles & 1, rev = acc ^ 1;
   const size_t row0 = (size_t)t.row0 + t.m0 + q * 32, row = row0 + lane;  // this warp's, thread's
@@ -595,7 +646,7 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const uint8_t* aux, ui
         if (p.out1) store_box(out, &m.o2, hw + 16 * i, p.out1, row0, p.F, f);
       }
     }
-    const uint32_t b = fp8_scale_byte(pair_max(c, absmax_bits(mx), ew, lane, acc));
+    const uint32_t b = fp8_scale_byte(pair_max(c, p, absmax_bits(mx), ew, lane, pairs));
     const uint32_t inv = fp8_inv_scale2(b);
     const int f = t.n0 + 64 * hf, fb = t.n0 / 128;
     if (rok && f < p.F) {
@@ -698,8 +749,8 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const uint8_t* aux, ui
           st_sector(da + p.F + 16, uw + 16 * i + 8);
         }
       }
-      const uint32_t bg = fp8_scale_byte(pair_max(c, absmax_bits(mg), ew, lane, 0));
-      const uint32_t bu = fp8_scale_byte(pair_max(c, absmax_bits(mu), ew, lane, 1));
+      const uint32_t bg = fp8_scale_byte(pair_max(c, p, absmax_bits(mg), ew, lane, pairs));
+      const uint32_t bu = fp8_scale_byte(pair_max(c, p, absmax_bits(mu), ew, lane, pairs));
       const uint32_t ig = fp8_inv_scale2(bg), iu = fp8_inv_scale2(bu);
       const int f = t.n0 + 128 * half + 64 * hf;
       if (rok && f < p.F) {
@@ -792,6 +843,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&ctl.sf_empty[b], 1);
     }
     for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(&ctl.sched_full[a], 1);
+      ptx::mbar_init(&ctl.sched_empty[a], kReaders + (C::kAux ? 2 : 0));
       ptx::mbar_init(&ctl.stored[a], 8);  // this CTA's epilogue warps
       ptx::mbar_init(&ctl.counted[a], 1);
       ptx::mbar_init(&ctl.aux_full[a], 1);
@@ -799,6 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&ctl.tmem_full[a], 1);
       ptx::mbar_init(&ctl.tmem_empty[a], 16);  // both CTAs' epilogue warps
     }
+    for (int q = 0; q < 4; ++q) ptx::mbar_init(&ctl.paired[q], 2);
     ptx::mbar_init(&ctl.ovl, 8);  // the four warps of each CTA that hold the shared columns
     ptx::mbar_init(&ctl.drain, 1);
     ctl.abort = 0;
@@ -857,53 +911,65 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctl.tmem_base;
   const uint32_t rank = ptx::cluster_ctarank();
   const int total1 = ctl.tstart[0][E], total = total1 + ctl.tstart[1][E];
-  const int first = (int)ptx::cluster_id_x(), stride = (int)ptx::cluster_count_x();
   int cur1 = 0, cur2 = 0;
   auto tile1 = [&](int i) { return tile_at<M1>(p1, ctl, i, cur1, rank); };
   auto tile2 = [&](int i) { return tile_at<M2>(p2, ctl, i - total1, cur2, rank); };
   if (warp < 4) {
     regs_dec<kRegsControl>();
     if (warp == 0 && lane == 0) {
-      int stage = 0, i = first;
+      int stage = 0;
       uint32_t phase = 0, steps = 0;
-      bool ok = true;
-      for (; ok && i < total1; i += stride) {
-        const Tile t = tile1(i);
-        steps += t.rows > 0 ? 2 * p1.halves : 0;
-        ok = producer_tile<M1, C::kStages1>(ctl, 0, smem, p1, &m.a1, &m.s1, &m.b1, t, rank, stage,
-                                            phase);
-      }
+      bool ok = true, second = !C::kAux;
       int ring = 0, ring_stages = C::kStages1;
-      if (ok && C::kAux && i < total) {
-        // the second ring takes the first one's memory and the pre-activations':
-        // wait until every stage and both steps have been read
-        for (int s = 0; ok && s < C::kStages1; ++s)
-          ok = ptx::mbar_wait(&ctl.empty[s], s < stage ? phase : phase ^ 1, &ctl.abort,
-                              kWaitLimitNs);
-        for (uint32_t n = steps > 2 ? steps - 2 : 0; ok && n < steps; ++n)
-          ok = ptx::mbar_wait(&ctl.aux_empty[n & 1], (n >> 1) & 1, &ctl.abort, kWaitLimitNs);
-        if (!ok) flag_timeout(ctl, p1.status, 13);
-        ring = C::kSecond;
-        ring_stages = C::kStages2;
-        stage = 0;
-        phase = 0;
-      }
-      for (; ok && i < total; i += stride)
+      for (uint32_t n = 0; ok; ++n) {
+        const int i = next_tile(ctl, n, p1.status, false);
+        ok = i >= 0;
+        if (!ok || i >= total) break;
+        if (i < total1) {
+          const Tile t = tile1(i);
+          steps += t.rows > 0 ? 2 * p1.halves : 0;
+          ok = producer_tile<M1, C::kStages1>(ctl, 0, smem, p1, &m.a1, &m.s1, &m.b1, t, rank,
+                                              stage, phase);
+          continue;
+        }
+        if (!second) {
+          // the second ring takes the first one's memory and the pre-activations':
+          // wait until every stage and both steps have been read
+          for (int s = 0; ok && s < C::kStages1; ++s)
+            ok = ptx::mbar_wait(&ctl.empty[s], s < stage ? phase : phase ^ 1, &ctl.abort,
+                                kWaitLimitNs);
+          for (uint32_t b = steps > 2 ? steps - 2 : 0; ok && b < steps; ++b)
+            ok = ptx::mbar_wait(&ctl.aux_empty[b & 1], (b >> 1) & 1, &ctl.abort, kWaitLimitNs);
+          if (!ok) {
+            flag_timeout(ctl, p1.status, 13);
+            break;
+          }
+          second = true;
+          ring = C::kSecond;
+          ring_stages = C::kStages2;
+          stage = 0;
+          phase = 0;
+        }
         ok = producer_tile<M2, C::kStages2>(ctl, C::kSecond, smem, p2, &m.a2, &m.s2, &m.b2,
                                             tile2(i), rank, stage, phase);
+      }
       if (!ok && rank == 0) drain_loads(ctl.full + ring, ring_stages, stage, phase);  // both CTAs'
     } else if (warp == 1 && rank == 0) {
       MmaState st;
-      int i = first;
-      bool ok = true;
-      for (; ok && i < total1; i += stride)
-        ok = mma_tile<M1, C::kStages1>(ctl, 0, ptx::smem_u32(smem), p1, tmem, st);
-      if (C::kAux) {
-        st.stage = 0;
-        st.phase = 0;
+      bool ok = true, second = !C::kAux;
+      for (uint32_t n = 0; ok; ++n) {
+        const int i = next_tile(ctl, n, p1.status, true);
+        ok = i >= 0;
+        if (!ok || i >= total) break;
+        if (i >= total1 && !second) {
+          second = true;
+          st.stage = 0;
+          st.phase = 0;
+        }
+        ok = i < total1 ? mma_tile<M1, C::kStages1>(ctl, 0, ptx::smem_u32(smem), p1, tmem, st)
+                        : mma_tile<M2, C::kStages2>(ctl, C::kSecond, ptx::smem_u32(smem), p2, tmem,
+                                                    st);
       }
-      for (; ok && i < total; i += stride)
-        ok = mma_tile<M2, C::kStages2>(ctl, C::kSecond, ptx::smem_u32(smem), p2, tmem, st);
       // no MMA may still run when TMEM is released (the same lane is elected as above)
       __syncwarp();
       if (elect_one()) ptx::umma_commit_pair(&ctl.drain, 1);
@@ -911,13 +977,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         int dummy = 0;
         ptx::mbar_wait(&ctl.drain, 0, &dummy, kWaitLimitNs);
       }
-    }
-    else if (C::kAux && warp == 3 && lane == 0) {
+    } else if (warp == 1 && lane == 0) {
+      claim_tiles(ctl, p1, total);
+    } else if (C::kAux && warp == 3 && lane == 0) {
       ptx::tma_prefetch_desc(&m.aux);
       uint32_t tiles = 0, step = 0;
       bool ok = true;
-      for (int i = first; ok && i < total1; i += stride)
-        ok = aux_tile(ctl, smem + C::kAuxAt, p1, &m.aux, tile1(i), tiles, step);
+      for (uint32_t n = 0; ok; ++n) {
+        const int i = next_tile(ctl, n, p1.status, false);
+        ok = i >= 0;
+        if (!ok || i >= total) break;
+        if (i < total1) ok = aux_tile(ctl, smem + C::kAuxAt, p1, &m.aux, tile1(i), tiles, step);
+      }
       // after an abort: the loads of the last two steps have landed
       for (uint32_t n = step > 2 ? step - 2 : 0; !ok && n < step; ++n) {
         int none = 0;
@@ -926,21 +997,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 2 && lane == 0) {
       uint32_t tiles = 0;
       bool ok = true;
-      for (int i = first; ok && i < total1; i += stride) ok = count_tile(ctl, p1, tile1(i).e, tiles);
+      for (uint32_t n = 0; ok; ++n) {
+        const int i = next_tile(ctl, n, p1.status, false);
+        ok = i >= 0;
+        if (!ok || i >= total) break;
+        if (i < total1) ok = count_tile(ctl, p1, tile1(i).e, tiles);
+      }
     }
     __syncwarp();
   } else if (warp < 12) {
     regs_inc<kRegsEpilogue>();
-    uint32_t tiles = 0, step = 0;
+    uint32_t tiles = 0, step = 0, pairs = 0;
     bool ok = true;
     const int ew = warp - 4;
     const uint8_t* aux = smem + C::kAuxAt;
     uint4* buf = reinterpret_cast<uint4*>(smem + C::kEpiAt) + ew * 128;
-    for (int i = first; ok && i < total; i += stride)
+    for (uint32_t n = 0; ok; ++n) {
+      const int i = next_tile(ctl, n, p1.status, true);
+      ok = i >= 0;
+      if (!ok || i >= total) break;
       ok = i < total1 ? epilogue_tile<M1>(ctl, aux, buf, p1, m, tile1(i), tmem, rank, tiles, step,
-                                          ew, lane)
+                                          pairs, ew, lane)
                       : epilogue_tile<M2>(ctl, aux, buf, p2, m, tile2(i), tmem, rank, tiles, step,
-                                          ew, lane);
+                                          pairs, ew, lane);
+    }
     // the buffers and the outputs must outlive the TMA stores
     if (lane == 0) ptx::bulk_wait_group0();
     __syncwarp();
@@ -948,9 +1028,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_dec<kRegsControl>();
     uint32_t group = 0;
     bool ok = true;
-    for (int i = first; ok && i < total; i += stride)
+    for (uint32_t n = 0; ok; ++n) {
+      const int i = next_tile(ctl, n, p1.status, true);
+      ok = i >= 0;
+      if (!ok || i >= total) break;
       ok = i < total1 ? scales_tile<M1>(ctl, p1, tile1(i), tmem, rank, group, warp - 12, lane)
                       : scales_tile<M2>(ctl, p2, tile2(i), tmem, rank, group, warp - 12, lane);
+    }
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -990,16 +1074,15 @@ cudaError_t resident_pairs(int* pairs) {
 
 template <int M1, int M2>
 moe_status_t launch_chain(const moe_layer_desc_t& d, const Maps& m, const KParams& p1,
-                          const KParams& p2, int kernel_id, bool counters_zeroed, cudaStream_t st) {
+                          const KParams& p2, int kernel_id, cudaStream_t st) {
   int pairs = 0;
   cudaError_t e = resident_pairs<M1, M2>(&pairs);
-  if (e == cudaSuccess && !counters_zeroed) e = launch_zero_counters(p1.dep, d.E, st);
+  if (e == cudaSuccess) e = launch_zero_counters(p1.dep, d.E, p1.tile, st);
   if (e != cudaSuccess) {
     set_error("grouped_gemm_fp8_kernel set-up: %s", cudaGetErrorString(e));
     return MOE_ERR_CUDA;
   }
-  // at most as many pairs as can be resident (second-GEMM tiles wait for
-  // first-GEMM tiles of other pairs), and no more than there can be tiles
+  // one pair for every two SMs, and no more than there can be tiles
   const long long n1 = ceil_div(d.F, 128);
   const long long rows = p1.N / (2 * BM) + std::min<long long>(p1.N, d.E);
   pairs = (int)std::min<long long>(pairs, rows * (n1 + ceil_div(d.H, BN)));
@@ -1036,6 +1119,7 @@ KParams params(const moe_layer_desc_t& d, const int32_t* off, int* status, int* 
   p.off = off;
   p.status = status;
   p.dep = dep;
+  p.tile = tile_counter(status);
   p.halves = 2;
   return p;
 }
@@ -1045,12 +1129,11 @@ KParams params(const moe_layer_desc_t& d, const int32_t* off, int* status, int* 
 moe_status_t launch_ffn_fwd_fp8(const moe_layer_desc_t& d, const uint8_t* xq, const uint8_t* xs,
                                 const int32_t* off, const Fp8Weights& w, bf16* a, bf16* h,
                                 uint8_t* hq, uint8_t* hs, bf16* o, int* status, int* dep,
-                                cudaStream_t st, bool counters_zeroed) {
+                                cudaStream_t st) {
   const long long N = (long long)d.T * d.k;
   if (N == 0) return MOE_OK;
   if (N <= kFp8FewRows * d.E)
-    return launch_ffn_rows_fp8(d, xq, xs, off, w, a, h, hq, hs, o, status, dep, st,
-                               counters_zeroed);
+    return launch_ffn_rows_fp8(d, xq, xs, off, w, a, h, hq, hs, o, status, dep, st);
   Maps m = {};
   if (!make_map(&m.a1, xq, 2, d.H, N, 1, BM, 1) || !make_map(&m.s1, xq, 2, d.H, N, 1, kABoxRows, 1) ||
       !make_map(&m.b1, w.w1q, 2, d.H, 2ll * d.E * d.F, 1, 128, 1) ||
@@ -1069,13 +1152,13 @@ moe_status_t launch_ffn_fwd_fp8(const moe_layer_desc_t& d, const uint8_t* xq, co
   p2.sa = hs;
   p2.sb = w.w2s;
   p2.out0 = o;
-  return launch_chain<FC1_FWD, FC2_FWD>(d, m, p1, p2, K_FP8_FFN_FWD, counters_zeroed, st);
+  return launch_chain<FC1_FWD, FC2_FWD>(d, m, p1, p2, K_FP8_FFN_FWD, st);
 }
 
 moe_status_t launch_ffn_dgrad_fp8(const moe_layer_desc_t& d, const uint8_t* dq, const uint8_t* ds,
                                   const bf16* a, const int32_t* off, const Fp8Weights& w, bf16* da,
                                   uint8_t* daq, uint8_t* das, bf16* dx_perm, int* status, int* dep,
-                                  cudaStream_t st, bool counters_zeroed) {
+                                  cudaStream_t st) {
   const long long N = (long long)d.T * d.k;
   if (N == 0) return MOE_OK;
   Maps m = {};
@@ -1095,7 +1178,7 @@ moe_status_t launch_ffn_dgrad_fp8(const moe_layer_desc_t& d, const uint8_t* dq, 
   p2.sa = das;
   p2.sb = w.w1s;
   p2.out0 = dx_perm;
-  return launch_chain<FC2_DGRAD, FC1_DGRAD>(d, m, p1, p2, K_FP8_FFN_DGRAD, counters_zeroed, st);
+  return launch_chain<FC2_DGRAD, FC1_DGRAD>(d, m, p1, p2, K_FP8_FFN_DGRAD, st);
 }
 
 }  // namespace moe

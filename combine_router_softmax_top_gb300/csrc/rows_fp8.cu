@@ -10,7 +10,8 @@
 // ring holds 6 stages of weights instead of the rows' padding.
 //
 // One persistent launch, one CTA per SM, both products' tiles as in the GEMM
-// chain (a tile of the second waits for its expert's tiles of the first):
+// chain (claimed in order from a counter, by warp 2; a tile of the second waits
+// for its expert's tiles of the first):
 //   FC1 tile: (expert, 128 columns of h, 32 rows): 128 gate and 128 up rows of W1
 //   FC2 tile: (expert, 256 columns of o, 32 rows): two times 128 rows of W2
 //   warp 0      TMA producer: 2 x 16 KB of weights and up to 4 KB of rows a stage
@@ -52,7 +53,7 @@ struct RowsParams {
   bf16 *a, *h;
   uint8_t *hq, *hs;
   bf16* o;
-  int *status, *dep;
+  int *status, *dep, *tile;
   int w2;             // FC2 columns of a tile: 256, or 128 when there are few tiles (set on the device)
 };
 
@@ -65,6 +66,8 @@ struct Tile {
 struct SmemCtl {
   uint64_t full[kStages], empty[kStages];
   uint64_t sf_full[2], sf_empty[2], tmem_full[2], tmem_empty[2], drain;
+  uint64_t sched_full[2], sched_empty[2];  // claimed tiles
+  int sched[2];
   uint32_t tmem_base;
   int abort;
   uint16_t rtile[kMaxE + 1];      // first row tile of each expert
@@ -114,6 +117,34 @@ __device__ __forceinline__ bool wait_expert(SmemCtl& c, const RowsParams& p, int
     }
   }
   return true;
+}
+
+// The n-th tile claimed for this CTA (past the last: none is left; -1: gave up),
+// for the 10 warps that read it: producer, MMA issuer, scales, epilogue.
+constexpr int kReaders = 10;
+__device__ __forceinline__ int next_tile(SmemCtl& c, uint32_t n, int* status, bool warp) {
+  bool ok = ptx::mbar_wait(&c.sched_full[n & 1], (n >> 1) & 1, &c.abort, kWaitLimitNs);
+  if (warp) ok = __all_sync(0xffffffffu, ok);
+  if (!ok) {
+    flag_timeout(c, status, 27);
+    return -1;
+  }
+  const int i = *(volatile int*)&c.sched[n & 1];
+  if (warp) __syncwarp();
+  if (!warp || (threadIdx.x & 31) == 0) ptx::mbar_arrive(&c.sched_empty[n & 1]);
+  return i;
+}
+__device__ __forceinline__ void claim_tiles(SmemCtl& c, const RowsParams& p, int total) {
+  for (uint32_t n = 0;; ++n) {
+    if (!ptx::mbar_wait(&c.sched_empty[n & 1], ((n >> 1) & 1) ^ 1, &c.abort, kWaitLimitNs)) {
+      flag_timeout(c, p.status, 28);
+      return;
+    }
+    const int i = min(atomicAdd(p.tile, 1), total);
+    *(volatile int*)&c.sched[n & 1] = i;
+    ptx::mbar_arrive(&c.sched_full[n & 1]);
+    if (i == total) return;
+  }
 }
 
 // M tiles of a tile: the second one is past the edge when 128 columns or fewer are left
@@ -279,10 +310,8 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const RowsParams& p, c
                                               uint32_t tmem, uint32_t& tiles, int q, int lane) {
   const int acc = tiles & 1, col = q * 32 + lane;  // this thread's weight row
   const bool got = ptx::mbar_wait(&c.tmem_full[acc], (tiles >> 1) & 1, &c.abort, kWaitLimitNs);
-  // all four warps leave together: the others would wait for them below
-  if (!__all_sync(0xffffffffu, got)) {
-    if (lane == 0) flag_timeout(c, p.status, 26);
-  }
+  // (after an abort the tile is gone through all the same: the others wait below)
+  if (!__all_sync(0xffffffffu, got) && lane == 0) flag_timeout(c, p.status, 26);
   ptx::tc_fence_after();
   const uint32_t tbase = tmem + acc * kAccCols + ((uint32_t)(q * 32) << 16);
   if (G == kFc1) {
@@ -383,6 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&ctl.sf_empty[b], 1);
       ptx::mbar_init(&ctl.tmem_full[b], 1);
       ptx::mbar_init(&ctl.tmem_empty[b], 4);
+      ptx::mbar_init(&ctl.sched_full[b], 1);
+      ptx::mbar_init(&ctl.sched_empty[b], kReaders);
     }
     ptx::mbar_init(&ctl.drain, 1);
     ctl.abort = 0;
@@ -427,24 +458,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   int cur1 = 0, cur2 = 0;
   auto tile1 = [&](int i) { return tile_at<kFc1>(p, ctl, i, cur1); };
   auto tile2 = [&](int i) { return tile_at<kFc2>(p, ctl, i - total1, cur2); };
-  const int first = blockIdx.x, stride = gridDim.x;
   bool ok = true;
   if (warp == 0) {
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
-      for (int i = first; ok && i < total; i += stride)
+      for (uint32_t n = 0; ok; ++n) {
+        const int i = next_tile(ctl, n, p.status, false);
+        ok = i >= 0;
+        if (!ok || i >= total) break;
         ok = i < total1
                  ? producer_tile<kFc1>(ctl, smem, p, &tmW1, &tmX1, &tmS1, tile1(i), stage, phase)
                  : producer_tile<kFc2>(ctl, smem, p, &tmW2, &tmX2, &tmS2, tile2(i), stage, phase);
+      }
       if (!ok) drain_loads(ctl.full, kStages, stage, phase);
     }
     __syncwarp();
   } else if (warp == 1) {
     MmaState m;
-    for (int i = first; ok && i < total; i += stride)
+    for (uint32_t n = 0; ok; ++n) {
+      const int i = next_tile(ctl, n, p.status, true);
+      ok = i >= 0;
+      if (!ok || i >= total) break;
       ok = i < total1 ? mma_tile<kFc1>(ctl, ptx::smem_u32(smem), p, tile1(i), tmem, m)
                       : mma_tile<kFc2>(ctl, ptx::smem_u32(smem), p, tile2(i), tmem, m);
+    }
     __syncwarp();
     if (elect_one()) ptx::umma_commit(&ctl.drain);  // no MMA may still run when TMEM is released
     if (!ptx::mbar_wait(&ctl.drain, 0, &ctl.abort, kWaitLimitNs)) {
@@ -452,25 +490,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_wait(&ctl.drain, 0, &dummy, kWaitLimitNs);
     }
     __syncwarp();
+  } else if (warp == 2) {
+    if (lane == 0) claim_tiles(ctl, p, total);
+    __syncwarp();
   } else if (warp >= 8) {
     uint32_t group = 0;
-    for (int i = first; ok && i < total; i += stride)
+    for (uint32_t n = 0; ok; ++n) {
+      const int i = next_tile(ctl, n, p.status, true);
+      ok = i >= 0;
+      if (!ok || i >= total) break;
       ok = i < total1 ? scales_tile<kFc1>(ctl, p, tile1(i), tmem, group, warp - 8, lane)
                       : scales_tile<kFc2>(ctl, p, tile2(i), tmem, group, warp - 8, lane);
+    }
   } else if (warp >= 4) {
     uint32_t tiles = 0;
-    for (int i = first; i < total; i += stride) {
-      const bool fine = i < total1 ? epilogue_tile<kFc1>(ctl, p, tile1(i), tmem, tiles, warp - 4, lane)
-                                   : epilogue_tile<kFc2>(ctl, p, tile2(i), tmem, tiles, warp - 4, lane);
-      // the four warps agree (they meet at barriers inside a tile)
-      if (!__all_sync(0xffffffffu, fine)) ok = false;
+    for (uint32_t n = 0;; ++n) {
+      const int i = next_tile(ctl, n, p.status, true);
+      // the four warps enter a tile together or not at all: they meet at barriers in it
       int stop;
       asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
                    "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
                    : "=r"(stop)
-                   : "r"(ok ? 0 : 1)
+                   : "r"((int)(i < 0 || i >= total || !ok))
                    : "memory");
       if (stop) break;
+      ok = i < total1 ? epilogue_tile<kFc1>(ctl, p, tile1(i), tmem, tiles, warp - 4, lane)
+                      : epilogue_tile<kFc2>(ctl, p, tile2(i), tmem, tiles, warp - 4, lane);
     }
   }
   ptx::tc_fence_before();
@@ -498,7 +543,7 @@ cudaError_t set_up() {
 moe_status_t launch_ffn_rows_fp8(const moe_layer_desc_t& d, const uint8_t* xq, const uint8_t* xs,
                                  const int32_t* off, const Fp8Weights& w, bf16* a, bf16* h,
                                  uint8_t* hq, uint8_t* hs, bf16* o, int* status, int* dep,
-                                 cudaStream_t st, bool counters_zeroed) {
+                                 cudaStream_t st) {
   const long long N = (long long)d.T * d.k;
   CUtensorMap m[6];
   if (!make_map(&m[0], w.w1q, 2, d.H, 2ll * d.E * d.F, 1, 128, 1) ||
@@ -506,11 +551,11 @@ moe_status_t launch_ffn_rows_fp8(const moe_layer_desc_t& d, const uint8_t* xq, c
       !make_map(&m[3], w.w2q, 2, d.F, (long long)d.E * d.H, 1, 128, 1) ||
       !make_map(&m[4], hq, 2, d.F, N, 1, NT, 1) || !make_map(&m[5], hq, 2, d.F, N, 1, kSmallBox, 1))
     return MOE_ERR_CUDA;
-  const RowsParams p = {d.E, d.H, d.F, N, off, xs, w, a, h, hq, hs, o, status, dep, 0};
+  const RowsParams p = {d.E, d.H, d.F, N, off, xs, w, a, h, hq, hs, o, status, dep,
+                        tile_counter(status), 0};
   cudaError_t e = set_up();
-  if (e == cudaSuccess && !counters_zeroed) e = launch_zero_counters(dep, d.E, st);
-  // one CTA per SM (all resident: second tiles wait for first ones), fewer when
-  // there cannot be as many tiles
+  if (e == cudaSuccess) e = launch_zero_counters(dep, d.E, p.tile, st);
+  // one CTA per SM, fewer when there cannot be as many tiles
   const long long rows = N / NT + std::min<long long>(N, d.E);
   const long long tiles = rows * (fp8_blocks(d.F) + fp8_blocks(d.H));
   const int grid = (int)std::min<long long>(device_sm_count(), tiles);
