@@ -25,10 +25,14 @@
 //               rounding, block maxima, e4m3 -> global; two warps per TMEM lane
 //               quarter, each owning 64 of every 128 columns
 // Tiles are claimed in order from a counter, the first GEMM's before the second's
-// (the odd CTA's warp 1 claims for the pair, two tiles ahead). A tile of the second
-// GEMM starts once every tile of its expert in the first has been stored
+// (the odd CTA's warp 1 claims for the pair, up to two ahead of what the slowest
+// warp works on; the second once the first is under way, or with few tiles half of
+// the pairs would take two each). A tile of the second GEMM starts once every tile of its expert in the first has been stored
 // (per-expert counters): those have been claimed before it by pairs that are
 // running, so the wait ends however many pairs are resident beside other work.
+// (Tiles dealt out by CTA number would need every CTA resident; they are as fast:
+// 163 against 166 us at 4096 tokens of 2048, 128 experts of 768, top 8, with a, h
+// kept; one token of that layer 15.2 against 16.4 us.)
 //
 // TMEM: two 256-column accumulators and four buffers of 12 scale columns do not
 // fit 512 columns, so the accumulators share 64: columns 0..255 and 192..447.
@@ -139,11 +143,12 @@ struct Tile {
 
 struct SmemCtl {
   uint64_t full[kMaxBars], empty[kMaxBars];
-  uint64_t aux_full[2], aux_empty[2];
+  uint64_t aux_full[2], aux_empty[2], aux_done;
   uint64_t paired[4];  // both warps of a quarter have left their block maxima
   uint64_t sf_full[kSf], sf_empty[kSf];
   uint64_t tmem_full[2], tmem_empty[2], ovl, drain;
   uint64_t sched_full[2], sched_empty[2];  // claimed tiles
+  uint64_t claim;                          // odd CTA: time to claim the second tile
   int sched[2];
   uint64_t stored[2], counted[2];  // a first-GEMM tile's stores issued; counted for its expert
   uint32_t tmem_base;
@@ -295,13 +300,14 @@ __device__ __forceinline__ int next_tile(SmemCtl& c, uint32_t n, int* status, bo
   return i;
 }
 // Claims tiles for the pair until none is left (one thread of the odd CTA).
-__device__ __forceinline__ void claim_tiles(SmemCtl& c, const KParams& p, int total) {
+__device__ __forceinline__ void claim_tiles(SmemCtl& c, const KParams& p, int first, int total) {
   for (uint32_t n = 0;; ++n) {
-    if (!mbar_wait_cluster(&c.sched_empty[n & 1], ((n >> 1) & 1) ^ 1, &c.abort)) {
+    if ((n == 1 && !ptx::mbar_wait(&c.claim, 0, &c.abort, kWaitLimitNs)) ||
+        !mbar_wait_cluster(&c.sched_empty[n & 1], ((n >> 1) & 1) ^ 1, &c.abort)) {
       flag_timeout(c, p.status, 15);
       return;
     }
-    const int i = min(atomicAdd(p.tile, 1), total);
+    const int i = min(n > 0 ? atomicAdd(p.tile, 1) : first, total);
     c.sched[n & 1] = i;
     asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(ptx::mapa_shared(&c.sched[n & 1], 0)),
                  "r"(i)
@@ -353,6 +359,7 @@ __device__ __forceinline__ bool producer_tile(SmemCtl& c, int ring, uint8_t* sme
       flag_timeout(c, p.status, 1);
       return false;
     }
+    if (rank == 1 && kt == nk / 4) ptx::mbar_arrive(&c.claim);
     uint8_t* sA = smem + stage * kStageBytes;
     uint8_t* sB = sA + kABytes;
     const int k0 = kt * BK;
@@ -855,6 +862,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int q = 0; q < 4; ++q) ptx::mbar_init(&ctl.paired[q], 2);
     ptx::mbar_init(&ctl.ovl, 8);  // the four warps of each CTA that hold the shared columns
     ptx::mbar_init(&ctl.drain, 1);
+    ptx::mbar_init(&ctl.claim, 1);
+    ptx::mbar_init(&ctl.aux_done, 1);
     ctl.abort = 0;
     ptx::fence_mbar_init();
   }
@@ -869,6 +878,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::tma_prefetch_desc(t);
   }
   pdl_wait();
+  const uint32_t rank = ptx::cluster_ctarank();
+  int first = 0;  // the first tile, claimed while the tables are made
+  if (warp == 1 && lane == 0 && rank == 1) first = atomicAdd(p1.tile, 1);
   // offsets outside 0..N would send stores out of the buffers
   for (int e = threadIdx.x; e <= E; e += blockDim.x)
     ctl.off[e] = (int)min(max((long long)p1.off[e], 0ll), p1.N);
@@ -909,7 +921,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
-  const uint32_t rank = ptx::cluster_ctarank();
   const int total1 = ctl.tstart[0][E], total = total1 + ctl.tstart[1][E];
   int cur1 = 0, cur2 = 0;
   auto tile1 = [&](int i) { return tile_at<M1>(p1, ctl, i, cur1, rank); };
@@ -918,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_dec<kRegsControl>();
     if (warp == 0 && lane == 0) {
       int stage = 0;
-      uint32_t phase = 0, steps = 0;
+      uint32_t phase = 0;
       bool ok = true, second = !C::kAux;
       int ring = 0, ring_stages = C::kStages1;
       for (uint32_t n = 0; ok; ++n) {
@@ -926,20 +937,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = i >= 0;
         if (!ok || i >= total) break;
         if (i < total1) {
-          const Tile t = tile1(i);
-          steps += t.rows > 0 ? 2 * p1.halves : 0;
-          ok = producer_tile<M1, C::kStages1>(ctl, 0, smem, p1, &m.a1, &m.s1, &m.b1, t, rank,
-                                              stage, phase);
+          ok = producer_tile<M1, C::kStages1>(ctl, 0, smem, p1, &m.a1, &m.s1, &m.b1, tile1(i),
+                                              rank, stage, phase);
           continue;
         }
         if (!second) {
           // the second ring takes the first one's memory and the pre-activations':
-          // wait until every stage and both steps have been read
+          // wait until every stage and every step have been read (the aux loader knows:
+          // the epilogue may be more than a tile behind this warp)
           for (int s = 0; ok && s < C::kStages1; ++s)
             ok = ptx::mbar_wait(&ctl.empty[s], s < stage ? phase : phase ^ 1, &ctl.abort,
                                 kWaitLimitNs);
-          for (uint32_t b = steps > 2 ? steps - 2 : 0; ok && b < steps; ++b)
-            ok = ptx::mbar_wait(&ctl.aux_empty[b & 1], (b >> 1) & 1, &ctl.abort, kWaitLimitNs);
+          ok = ok && ptx::mbar_wait(&ctl.aux_done, 0, &ctl.abort, kWaitLimitNs);
           if (!ok) {
             flag_timeout(ctl, p1.status, 13);
             break;
@@ -978,16 +987,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_wait(&ctl.drain, 0, &dummy, kWaitLimitNs);
       }
     } else if (warp == 1 && lane == 0) {
-      claim_tiles(ctl, p1, total);
+      claim_tiles(ctl, p1, first, total);
     } else if (C::kAux && warp == 3 && lane == 0) {
       ptx::tma_prefetch_desc(&m.aux);
       uint32_t tiles = 0, step = 0;
-      bool ok = true;
+      bool ok = true, done = false;
       for (uint32_t n = 0; ok; ++n) {
         const int i = next_tile(ctl, n, p1.status, false);
         ok = i >= 0;
         if (!ok || i >= total) break;
-        if (i < total1) ok = aux_tile(ctl, smem + C::kAuxAt, p1, &m.aux, tile1(i), tiles, step);
+        if (i < total1) {
+          ok = aux_tile(ctl, smem + C::kAuxAt, p1, &m.aux, tile1(i), tiles, step);
+        } else if (!done) {  // the last two steps have been read: the producer may have the room
+          for (uint32_t b = step > 2 ? step - 2 : 0; ok && b < step; ++b)
+            ok = ptx::mbar_wait(&ctl.aux_empty[b & 1], (b >> 1) & 1, &ctl.abort, kWaitLimitNs);
+          if (!ok) flag_timeout(ctl, p1.status, 17);
+          ptx::mbar_arrive(&ctl.aux_done);
+          done = true;
+        }
       }
       // after an abort: the loads of the last two steps have landed
       for (uint32_t n = step > 2 ? step - 2 : 0; !ok && n < step; ++n) {

@@ -66,7 +66,7 @@ struct Tile {
 struct SmemCtl {
   uint64_t full[kStages], empty[kStages];
   uint64_t sf_full[2], sf_empty[2], tmem_full[2], tmem_empty[2], drain;
-  uint64_t sched_full[2], sched_empty[2];  // claimed tiles
+  uint64_t sched_full[2], sched_empty[2], claim;  // claimed tiles
   int sched[2];
   uint32_t tmem_base;
   int abort;
@@ -134,13 +134,14 @@ __device__ __forceinline__ int next_tile(SmemCtl& c, uint32_t n, int* status, bo
   if (!warp || (threadIdx.x & 31) == 0) ptx::mbar_arrive(&c.sched_empty[n & 1]);
   return i;
 }
-__device__ __forceinline__ void claim_tiles(SmemCtl& c, const RowsParams& p, int total) {
+__device__ __forceinline__ void claim_tiles(SmemCtl& c, const RowsParams& p, int first, int total) {
   for (uint32_t n = 0;; ++n) {
-    if (!ptx::mbar_wait(&c.sched_empty[n & 1], ((n >> 1) & 1) ^ 1, &c.abort, kWaitLimitNs)) {
+    if ((n == 1 && !ptx::mbar_wait(&c.claim, 0, &c.abort, kWaitLimitNs)) ||
+        !ptx::mbar_wait(&c.sched_empty[n & 1], ((n >> 1) & 1) ^ 1, &c.abort, kWaitLimitNs)) {
       flag_timeout(c, p.status, 28);
       return;
     }
-    const int i = min(atomicAdd(p.tile, 1), total);
+    const int i = min(n > 0 ? atomicAdd(p.tile, 1) : first, total);
     *(volatile int*)&c.sched[n & 1] = i;
     ptx::mbar_arrive(&c.sched_full[n & 1]);
     if (i == total) return;
@@ -169,6 +170,7 @@ __device__ __forceinline__ bool producer_tile(SmemCtl& c, uint8_t* smem, const R
       flag_timeout(c, p.status, 21);
       return false;
     }
+    if (kt == nk / 4) ptx::mbar_arrive(&c.claim);
     uint8_t* s = smem + stage * kStageBytes;
     uint64_t* bar = &c.full[stage];
     const int k0 = kt * 128;
@@ -416,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&ctl.sched_empty[b], kReaders);
     }
     ptx::mbar_init(&ctl.drain, 1);
+    ptx::mbar_init(&ctl.claim, 1);
     ctl.abort = 0;
     ptx::fence_mbar_init();
     for (const CUtensorMap* m : {&tmW1, &tmX1, &tmS1, &tmW2, &tmX2, &tmS2})
@@ -426,6 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tmem_relinquish();
   }
   pdl_wait();
+  int first = 0;  // the first tile, claimed while the tables are made
+  if (warp == 2 && lane == 0) first = atomicAdd(p.tile, 1);
   // offsets outside 0..N would send stores out of the buffers
   for (int e = threadIdx.x; e <= p.E; e += blockDim.x)
     ctl.off[e] = (uint16_t)min(max((long long)p.off[e], 0ll), p.N);
@@ -491,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 2) {
-    if (lane == 0) claim_tiles(ctl, p, total);
+    if (lane == 0) claim_tiles(ctl, p, first, total);
     __syncwarp();
   } else if (warp >= 8) {
     uint32_t group = 0;

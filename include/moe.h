@@ -449,7 +449,8 @@ moe_status_t moe_layer_steps_host(const moe_layer_desc_t* d, const moe_mb_bufs_t
  *     The same quantised weights serve the forward and the gradient.
  * Products are accumulated in fp32; the scales are applied exactly. Buffer
  * arguments of type moe_e4m3 and moe_e8m0 are device pointers, 16-byte aligned
- * like every other. */
+ * like every other; a, h, hq, o, da, daq and dx_perm of these calls are 32-byte
+ * aligned (the kernels move their rows in whole 32-byte sectors). */
 
 /* Bytes of the scale buffer of `rows` rows of `blocks` blocks (0 if negative). */
 size_t moe_fp8_scale_bytes(int64_t rows, int32_t blocks);

@@ -499,6 +499,56 @@ def test_two_calls_at_once_with_workspaces_of_their_own():
         assert torch.equal(c.o, w)
 
 
+def test_chains_of_every_kind_at_once():
+    # forwards of many and of few rows and a gradient, each with more tiles than CTAs
+    # or sharing the SMs with one that has: none may wait for a CTA that is not there
+    many, few, grad = (Case(T=T, H=512, E=32, k=4, F=512, seed=s)
+                       for T, s in ((2500, 21), (200, 22), (2500, 23)))
+    want = []
+    for c in (many, few, grad):
+        c.quantize()
+        c.permute()
+        c.forward()
+        c.combine_bwd()
+        c.dgrad()
+        want.append([t.clone() for t in (c.o, c.da, c.dx)])
+        c.o.zero_()
+        c.dx.zero_()
+    torch.cuda.synchronize()
+    sts = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(8):
+        many.forward(stream=sts[0])
+        few.forward(stream=sts[1])
+        grad.dgrad(stream=sts[2])
+        few.forward(stream=sts[1])
+    torch.cuda.synchronize()
+    for c in (many, few, grad):
+        c.status()
+    assert torch.equal(many.o, want[0][0]) and torch.equal(few.o, want[1][0])
+    assert torch.equal(grad.da, want[2][1]) and torch.equal(grad.dx, want[2][2])
+
+
+@pytest.mark.parametrize("H", [64, 512])
+def test_short_products_with_long_epilogues_repeat(H):
+    # the gradient's first product is over long before its epilogue: the second one's
+    # operands may not take the pre-activations' memory yet
+    c = Case(T=6000, H=H, E=8, k=2, F=576, seed=24)
+    c.quantize()
+    c.permute()
+    c.forward()
+    c.combine_bwd()
+    want = None
+    for _ in range(20):
+        c.da.zero_()
+        c.dx.zero_()
+        c.dgrad()
+        got = (c.da.clone(), c.q.daq.view(torch.uint8).clone(), c.dx.clone())
+        want = want or got
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    c.status()
+    test_dgrad_stages(c)
+
+
 @pytest.mark.parametrize("T", [1, 200])
 def test_captured_and_replayed(T):
     c = Case(T=T, H=256, E=8, k=4, F=192, seed=15)
