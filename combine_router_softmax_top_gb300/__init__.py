@@ -459,9 +459,18 @@ def moe_expert_ffn_bwd_dgrad_fp8(desc, dq, ds, a, off, w1q, w1s, w2q, w2s, da, d
     _check(lib().moe_expert_ffn_bwd_dgrad_fp8(_d(desc), *p, ws.numel(), _fp8_stream(stream)), what)
 
 
+def _fp8_fits(what, desc, bufs, fp8):
+    """Refuses buffers made for other sizes or for fewer rows than desc's."""
+    for name, of in (("bufs", bufs.desc), ("fp8", fp8.desc)):
+        if (of.H, of.E, of.F) != (desc.H, desc.E, desc.F) or of.T < desc.T or of.k != desc.k:
+            raise MoeError(MOE_ERR_INVALID_ARG, what, f"{name} is of another layer: T={of.T} "
+                           f"H={of.H} E={of.E} k={of.k} F={of.F}")
+
+
 def moe_layer_forward_fp8(desc, bufs: "LayerBuffers", fp8: "Fp8Buffers", save: bool = True,
                           stream=None):
     """Layer forward with 8-bit experts; save=True keeps what the backward reads."""
+    _fp8_fits("moe_layer_forward_fp8", desc, bufs, fp8)
     _check(lib().moe_layer_forward_fp8(_d(desc), ctypes.byref(bufs.struct()),
                                        ctypes.byref(fp8.struct()), int(bool(save)), _s(stream)),
            "moe_layer_forward_fp8")
@@ -470,6 +479,7 @@ def moe_layer_forward_fp8(desc, bufs: "LayerBuffers", fp8: "Fp8Buffers", save: b
 def moe_layer_backward_fp8(desc, bufs: "LayerBuffers", fp8: "Fp8Buffers", run_wgrad: bool = True,
                            stream=None):
     """Layer backward with 8-bit experts, after a forward that saved."""
+    _fp8_fits("moe_layer_backward_fp8", desc, bufs, fp8)
     _check(lib().moe_layer_backward_fp8(_d(desc), ctypes.byref(bufs.struct()),
                                         ctypes.byref(fp8.struct()), int(bool(run_wgrad)),
                                         _s(stream)), "moe_layer_backward_fp8")
@@ -500,7 +510,6 @@ class Fp8Buffers:
         if backward:
             self.dq, self.ds = rows(H), scales(nh)
             self.daq, self.das = rows(2 * F), scales(2 * nf)
-        self._struct = None
 
     def quantize_weights(self, w1, w2, stream=None):
         """Fills w1q, w1s, w2q, w2s from the bf16 expert weights."""
@@ -508,13 +517,8 @@ class Fp8Buffers:
                                  stream)
 
     def struct(self) -> Fp8Bufs:
-        if self._struct is None:
-            s = Fp8Bufs()
-            for n in _FP8_FIELDS:
-                t = getattr(self, n)
-                setattr(s, n, None if t is None else t.data_ptr())
-            self._struct = s
-        return self._struct
+        return Fp8Bufs(*[None if t is None else t.data_ptr()
+                         for t in (getattr(self, n) for n in _FP8_FIELDS)])
 
 
 class LayerBuffers:

@@ -20,7 +20,9 @@ __device__ __forceinline__ uint32_t max8(uint32_t m, const uint4& v) {
 // ------------------------------------------------------------------ weights
 // One CTA per 128 x 128 block. A thread holds 16 columns of 4 rows in registers
 // between the pass that finds the block's maximum and the one that rounds, so
-// each weight is read once: 2 bytes in, 1 byte out.
+// each weight is read once: 2 bytes in, 1 byte out. A row of the block is 256
+// contiguous bytes in and 128 out, whole lines both ways. 128 experts of 2048 x 768:
+// 1812 MB in 254 us, 7.1 TB/s (more than a copy, as reads outweigh writes).
 struct WeightMat {
   const bf16* w;
   uint8_t* q;
@@ -77,7 +79,10 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(WeightMat m1, Wei
 // xq[slot[t,j]] = e4m3(x[t] / scale). A warp takes one token's 512 columns
 // (four blocks, the four bytes of one scale word): it reads and rounds them
 // once and writes them to the token's k rows, so x is read once and only the
-// 8-bit rows are written. Lane j holds the token's j-th slot.
+// 8-bit rows are written. Lane j holds the token's j-th slot. 4096 tokens of 2048,
+// 8 rows each: 84 MB in 14.9 us, 5.7 TB/s; one token 5.6 us, the launch itself. (A
+// token's blocks need no exchange between warps, so a decode batch has a warp for
+// every 512 columns.)
 __global__ void __launch_bounds__(256) permute_fp8_kernel(const bf16* __restrict__ x,
                                                           const int32_t* __restrict__ slot,
                                                           uint8_t* __restrict__ xq,
@@ -131,8 +136,8 @@ __global__ void __launch_bounds__(256) permute_fp8_kernel(const bf16* __restrict
 // not overlap within a block, so many small blocks do better than few large ones:
 // on the 4096-token layer with d_o, 128 threads x 8 blocks an SM with 4 rows in
 // flight 63.5 us, 256 x 3 with 8 rows 65.1 us, 256 x 2 78 us, 64 x 12 68 us; one
-// token's 8 columns a thread over 256 threads 67 us. 353 MB at 5.56 TB/s: 0.82 of
-// the copy rate, as the bf16 gathers of this layer reach.
+// token's 8 columns a thread over 256 threads 67 us. 353 MB in 63.2 us, 5.6 TB/s: 0.82
+// of the copy rate, as the bf16 gathers of this layer reach.
 constexpr int kRowsInFlight = 4;
 constexpr int kCombineThreads = 128;
 constexpr int kCombineBlocks = 8;  // resident blocks an SM, k <= 8

@@ -19,6 +19,11 @@
 //   warps 4..7  epilogue: thread = weight row (column of h or o), registers = rows;
 //               block maxima by warp reductions and shared memory
 //   warps 8..11 scales into TMEM, ahead of the MMAs
+//
+// 64 tokens of the 128-expert layer (H 2048, F 768, top 8, skewed): 85 us, 7.0 TB/s,
+// the rate of a copy. One token: 16 us for 38 MB; its 48 tiles of the first product
+// read 512 KB each at what one SM takes in (about 100 GB/s), 5 us, and the rest is
+// the two launches, their set-up and the hand-over between the products.
 #include <algorithm>
 #include <atomic>
 
@@ -456,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
   // one token of the 128-expert layer has 64 second tiles of 256 columns: half of
-  // the SMs would have none
+  // the SMs would have none (128 columns: 17.3 -> 15.2 us)
   p.w2 = ctl.rtile[p.E] * ((p.H + 255) / 256) < (int)gridDim.x ? 128 : 256;
   const int total1 = ctl.rtile[p.E] * ncols<kFc1>(p);
   const int total = total1 + ctl.rtile[p.E] * ncols<kFc2>(p);

@@ -141,3 +141,21 @@ def test_binding_refuses_strided_and_small_tensors(L):
     with pytest.raises(moe.MoeError, match="aligned"):
         big = torch.zeros(16 * 192 + 1, dtype=torch.bfloat16, device="cuda")
         moe.moe_permute_fp8(D, big[1:].view(16, 192), slot, xq, xs)
+
+
+@pytest.mark.parametrize("call", ["moe_layer_forward_fp8", "moe_layer_backward_fp8"])
+@pytest.mark.parametrize("other", [dict(T=15), dict(H=128), dict(E=4), dict(k=1), dict(F=128)])
+def test_layer_calls_refuse_buffers_of_another_layer(call, other):
+    small = moe.LayerDesc.of(**{**dict(T=16, H=192, E=8, k=2, F=192), **other})
+    mine = moe.LayerBuffers(D, "cpu"), moe.Fp8Buffers(D, "cpu")
+    theirs = moe.LayerBuffers(small, "cpu"), moe.Fp8Buffers(small, "cpu")
+    for b, q, name in ((theirs[0], mine[1], "bufs"), (mine[0], theirs[1], "fp8")):
+        with pytest.raises(moe.MoeError, match=f"{name} is of another layer"):
+            getattr(moe, call)(D, b, q)
+
+
+def test_buffer_struct_follows_the_tensors():
+    q = moe.Fp8Buffers(D, "cpu")
+    before = q.struct().w1q
+    q.w1q = torch.empty_like(q.w1q)
+    assert q.struct().w1q == q.w1q.data_ptr() != before
