@@ -156,19 +156,20 @@ inline bool make_map(CUtensorMap* m, const void* base, int dims, long long d0, l
   return true;
 }
 
-// Map of bf16 rows [rows, cols] in boxes of 32 columns x box_rows, 64-byte swizzle.
+// Map of bf16 (or, in boxes of 64 columns, e4m3) rows [rows, cols] in boxes of 64
+// bytes x box_rows, 64-byte swizzle.
 inline bool make_rows_map(CUtensorMap* m, const void* base, long long rows, long long cols,
-                          int box_rows) {
+                          int box_rows, bool fp8 = false) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) {
     set_error("cuTensorMapEncodeTiled is not available from the driver");
     return false;
   }
   cuuint64_t dim[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-  cuuint32_t box[2] = {32, (cuuint32_t)box_rows};
+  cuuint64_t strides[1] = {(cuuint64_t)cols * (fp8 ? 1 : 2)};
+  cuuint32_t box[2] = {fp8 ? 64u : 32u, (cuuint32_t)box_rows};
   cuuint32_t es[2] = {1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dim, strides,
+  CUresult r = enc(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dim, strides,
                    box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                    CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {

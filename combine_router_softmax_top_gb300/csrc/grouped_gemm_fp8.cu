@@ -27,12 +27,11 @@
 // Tiles are claimed in order from a counter, the first GEMM's before the second's
 // (the odd CTA's warp 1 claims for the pair, up to two ahead of what the slowest
 // warp works on; the second once the first is under way, or with few tiles half of
-// the pairs would take two each). A tile of the second GEMM starts once every tile of its expert in the first has been stored
-// (per-expert counters): those have been claimed before it by pairs that are
-// running, so the wait ends however many pairs are resident beside other work.
-// (Tiles dealt out by CTA number would need every CTA resident; they are as fast:
-// 163 against 166 us at 4096 tokens of 2048, 128 experts of 768, top 8, with a, h
-// kept; one token of that layer 15.2 against 16.4 us.)
+// the pairs would take two each). A tile of the second GEMM starts once every tile
+// of its expert in the first has been stored (per-expert counters): those have been
+// claimed before it by pairs that are running, so the wait ends however many pairs
+// are resident beside other work. (Tiles dealt out by CTA number would need every
+// CTA resident, and are little faster: 163 against 166 us for the forward below.)
 //
 // TMEM: two 256-column accumulators and four buffers of 12 scale columns do not
 // fit 512 columns, so the accumulators share 64: columns 0..255 and 192..447.
@@ -45,9 +44,11 @@
 //
 // What bounds it, 128 experts of H 2048, F 768 at 4096 tokens, top 8, balanced: the
 // forward that keeps a and h moves 956 MB in 157 to 167 us (5.7 to 6.1 TB/s, the copy
-// rate being 6.8), the gradient 1007 MB in 177 to 190 us, held by the first product's
-// epilogue. Skewed loads (95 to 4096 rows an expert) cost the gradient 230 to 245 us:
-// half as many 256-row tiles again, their last rows empty. 64 experts of F 1408 at
+// rate being 6.8), the gradient 1007 MB in 177 us. Its second product lands 64 KB of
+// operands in a pair for each 256 x 256 x 128 step, at the 9 to 10 TB/s that L2 gives all
+// SMs together. Skewed loads (95 to 4096 rows an expert) cost the gradient 230 to 240
+// us: half as many 256-row tiles again, their last rows empty, and a first product at
+// the pace of its epilogue (22000 clocks a tile, the K loop 14000). 64 experts of F 1408 at
 // 8192 tokens, nothing kept: 1134 GFLOP in 405 us alone (2.8 PFLOP/s, tensor pipe 73%
 // active), 480 us again and again, when the power limit lowers the clocks.
 //
@@ -109,7 +110,7 @@ constexpr int kMaxBars = 10;
 
 struct Maps {
   CUtensorMap a1, s1, b1, a2, s2, b2;  // operands: A, A in small boxes, B of both GEMMs
-  CUtensorMap o1, o2, o3;              // a | da, h, o | dx_perm
+  CUtensorMap o1, o2, o3;              // a | da, h | daq, o | dx_perm
   CUtensorMap aux;                     // the saved pre-activation
 };
 
@@ -255,6 +256,11 @@ __device__ __forceinline__ void store_box(const Out& o, const CUtensorMap* map, 
     st_sector(p, w);
     st_sector(p + 16, w + 8);
   }
+}
+// 16 bf16 columns (8 packed words) rounded to e4m3
+__device__ __forceinline__ uint4 fp8x16(const uint32_t* w, uint32_t inv) {
+  return make_uint4(fp8x4_of_bf16(w[0], w[1], inv), fp8x4_of_bf16(w[2], w[3], inv),
+                    fp8x4_of_bf16(w[4], w[5], inv), fp8x4_of_bf16(w[6], w[7], inv));
 }
 // 32 bf16 columns (16 packed words) rounded to e4m3
 __device__ __forceinline__ void store_fp8(uint8_t* p, const uint32_t* w, uint32_t inv) {
@@ -557,6 +563,22 @@ __device__ __forceinline__ uint32_t pair_max(SmemCtl& c, const KParams& p, uint3
   return max(m, c.amax[buf][ew ^ 4][lane]);
 }
 
+// Hands a first-GEMM tile, the n-th of this CTA, to the counting warp, which has
+// counted the one before the last. The gradient's only once the next tile is known
+// (and before anything is waited for that could depend on this one): daq leaves by
+// TMA, and the stores' completion, waited for here, takes 1000 clocks and more.
+template <int MODE>
+__device__ __forceinline__ void hand_over(SmemCtl& c, const KParams& p, uint32_t n, int lane) {
+  __syncwarp();
+  if (lane == 0) {
+    if (MODE == FC2_DGRAD) ptx::bulk_wait_group0();
+    if (!ptx::mbar_wait(&c.counted[n & 1], ((n >> 1) & 1) ^ 1, &c.abort, kWaitLimitNs))
+      flag_timeout(c, p.status, 7);
+    ptx::mbar_arrive(&c.stored[n & 1]);
+  }
+  __syncwarp();
+}
+
 // ================================================================ aux loader
 // FC2 dgrad: the saved pre-activations of a tile, in the epilogue's four steps:
 // for each 128 columns (half) and each 32 of a warp's 64 columns (i), the gate and
@@ -719,8 +741,12 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const uint8_t* aux, ui
         // up boxes): the buffer is free once the stores have read it, at the next step.
         // Through the 2 KB buffer the second box of a step would wait for the first one's
         // store, 700 clocks; unstored, or with rows of another expert, it is free now.
-        const bool inplace = p.out0 && ok && out.rows >= 32;
-        if (lane == 0 && !inplace) ptx::mbar_arrive(&c.aux_empty[b]);
+        const bool whole = ok && out.rows >= 32, inplace = p.out0 && whole;
+        // the half's last step stays for daq's boxes (below)
+        if (lane == 0) {
+          if (whole && (inplace || i == 1)) held = b;
+          else ptx::mbar_arrive(&c.aux_empty[b]);
+        }
         const uint32_t* ag = reinterpret_cast<const uint32_t*>(gc);
         const uint32_t* au = reinterpret_cast<const uint32_t*>(uc);
 #pragma unroll
@@ -754,7 +780,6 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const uint8_t* aux, ui
             ptx::tma_store_2d(&m.o1, slab, f, (int)row0);
             ptx::tma_store_2d(&m.o1, slab + 8192, p.F + f, (int)row0);
             ptx::bulk_commit_group();
-            held = b;
           }
         } else if (p.out0 && ok && rok) {
           bf16* da = p.out0 + row * (size_t)(2 * p.F) + f;
@@ -768,7 +793,28 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const uint8_t* aux, ui
       const uint32_t bu = fp8_scale_byte(pair_max(c, p, absmax_bits(mu), ew, lane, pairs));
       const uint32_t ig = fp8_inv_scale2(bg), iu = fp8_inv_scale2(bu);
       const int f = t.n0 + 128 * half + 64 * hf;
-      if (rok && f < p.F) {
+      if (f < p.F && out.rows >= 32) {
+        // daq's 64-byte rows, in place of the last step's da once that has been read (as
+        // 32-byte sectors from registers every row is a request of its own: 182 -> 177 us
+        // on the balanced layer, 234 -> 229 on the skewed one)
+        uint8_t* slab = const_cast<uint8_t*>(aux) + ((step - 1) & 1) * kAuxBytes + 16384 * hf +
+                        q * 2048;
+        if (lane == 0) ptx::bulk_wait_group_read0();
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int at = lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16);
+          *reinterpret_cast<uint4*>(slab + at) = fp8x16(gw + 8 * j, ig);
+          *reinterpret_cast<uint4*>(slab + 8192 + at) = fp8x16(uw + 8 * j, iu);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::tma_store_2d(&m.o2, slab, f, (int)row0);
+          ptx::tma_store_2d(&m.o2, slab + 8192, p.F + f, (int)row0);
+          ptx::bulk_commit_group();
+        }
+      } else if (rok && f < p.F) {
         uint8_t* qp = p.q + row * (size_t)(2 * p.F) + f;
         store_fp8(qp, gw, ig);
         store_fp8(qp + 32, gw + 16, ig);
@@ -805,16 +851,7 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const uint8_t* aux, ui
       if (t.n0 + col < p.H) store_box(out, &m.o3, w, p.out0, row0, p.H, t.n0 + col);
     }
   }
-  if (Mode<MODE>::kFirst) {
-    // hand the tile to the counting warp, which has counted the one before last
-    __syncwarp();
-    if (lane == 0) {
-      if (!ptx::mbar_wait(&c.counted[acc], ((tiles >> 1) & 1) ^ 1, &c.abort, kWaitLimitNs))
-        flag_timeout(c, p.status, 7);
-      ptx::mbar_arrive(&c.stored[acc]);
-    }
-    __syncwarp();
-  }
+  if (MODE == FC1_FWD) hand_over<MODE>(c, p, tiles, lane);
   ++tiles;
   return true;
 }
@@ -1033,12 +1070,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 12) {
     regs_inc<kRegsEpilogue>();
     uint32_t tiles = 0, step = 0, pairs = 0;
-    bool ok = true;
+    bool ok = true, pending = false;
     const int ew = warp - 4;
     const uint8_t* aux = smem + C::kAuxAt;
     uint4* buf = reinterpret_cast<uint4*>(smem + C::kEpiAt) + ew * 128;
     for (uint32_t n = 0; ok; ++n) {
       const int i = next_tile(ctl, n, p1.status, true);
+      if (pending) hand_over<M1>(ctl, p1, tiles - 1, lane);
+      pending = M1 == FC2_DGRAD && i < total1;
       ok = i >= 0;
       if (!ok || i >= total) break;
       ok = i < total1 ? epilogue_tile<M1>(ctl, aux, buf, p1, m, tile1(i), tmem, rank, tiles, step,
@@ -1192,6 +1231,7 @@ moe_status_t launch_ffn_dgrad_fp8(const moe_layer_desc_t& d, const uint8_t* dq, 
       !make_map(&m.a2, daq, 3, d.F, 2, N, 1, BM) || !make_map(&m.s2, daq, 3, d.F, 2, N, 1, kABoxRows) ||
       !make_map(&m.b2, w.w1q, 3, d.H, d.F, 2ll * d.E, 128, 1) ||
       !make_rows_map(&m.o3, dx_perm, N, d.H, 32) || !make_rows_map(&m.aux, a, N, 2 * d.F, BM) ||
+      !make_rows_map(&m.o2, daq, N, 2 * d.F, 32, true) ||
       (da && !make_rows_map(&m.o1, da, N, 2 * d.F, 32)))
     return MOE_ERR_CUDA;
   KParams p1 = params(d, off, status, dep), p2 = p1;
