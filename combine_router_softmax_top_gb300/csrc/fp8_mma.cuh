@@ -87,7 +87,7 @@ __device__ __forceinline__ int ld_acquire(const int* p) {
 // As ptx::mbar_wait, acquiring what another CTA of the cluster released.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
                                                   volatile int* abort) {
-  const uint64_t t0 = ptx::globaltimer_ns();
+  uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
     uint32_t ok;
     asm volatile(
@@ -98,7 +98,10 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
         : "r"(ptx::smem_u32(bar)), "r"(parity)
         : "memory");
     if (ok) return true;
-    if ((i & 63) == 0 && (*abort || ptx::globaltimer_ns() - t0 > kWaitLimitNs)) return false;
+    if ((i & 63) == 0) {
+      if (t0 == 0) t0 = ptx::globaltimer_ns();
+      if (*abort || ptx::globaltimer_ns() - t0 > kWaitLimitNs) return false;
+    }
   }
 }
 

@@ -59,7 +59,6 @@ struct RowsParams {
   uint8_t *hq, *hs;
   bf16* o;
   int *status, *dep, *tile;
-  int w2;             // FC2 columns of a tile: 256, or 128 when there are few tiles (set on the device)
 };
 
 struct Tile {
@@ -87,19 +86,27 @@ __device__ __forceinline__ int kblocks(const RowsParams& p) {
 }
 template <int G>
 __device__ __forceinline__ int ncols(const RowsParams& p) {  // column blocks of an expert
-  return G == kFc1 ? (p.F + 127) / 128 : (p.H + p.w2 - 1) / p.w2;
+  return G == kFc1 ? (p.F + 127) / 128 : (p.H + 255) / 256;
 }
 
 template <int G>
 __device__ __forceinline__ Tile tile_at(const RowsParams& p, const SmemCtl& c, int i, int& cursor) {
   const int nc = ncols<G>(p);
-  while (c.rtile[cursor + 1] * nc <= i) ++cursor;
+  if (c.rtile[cursor + 1] * nc <= i) {  // (most experts may have no rows)
+    int lo = cursor + 1, hi = p.E - 1;  // the first expert that ends past i
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (c.rtile[mid + 1] * nc <= i) lo = mid + 1;
+      else hi = mid;
+    }
+    cursor = lo;
+  }
   Tile t;
   t.e = cursor;
   const int cnt = c.off[cursor + 1] - c.off[cursor];
   const int local = i - c.rtile[cursor] * nc, nt = (cnt + NT - 1) / NT;
   const int r = (local % nt) * NT;  // row tiles fastest: they share the weights
-  t.n0 = (local / nt) * (G == kFc1 ? 128 : p.w2);
+  t.n0 = (local / nt) * (G == kFc1 ? 128 : 256);
   t.row = (long long)c.off[cursor] + r;
   t.rows = min(NT, cnt - r);
   return t;
@@ -156,7 +163,7 @@ __device__ __forceinline__ void claim_tiles(SmemCtl& c, const RowsParams& p, int
 // M tiles of a tile: the second one is past the edge when 128 columns or fewer are left
 template <int G>
 __device__ __forceinline__ int mtiles(const RowsParams& p, const Tile& t) {
-  return G == kFc1 || (p.w2 == 256 && t.n0 + 128 < p.H) ? 2 : 1;
+  return G == kFc1 || t.n0 + 128 < p.H ? 2 : 1;
 }
 
 template <int G>
@@ -273,20 +280,27 @@ __device__ __forceinline__ bool mma_tile(SmemCtl& c, uint32_t smem, const RowsPa
   if (!wait(&c.tmem_empty[acc], ((m.tiles >> 1) & 1) ^ 1, 23)) return false;
   ptx::tc_fence_after();
   const uint32_t d = tmem + acc * kAccCols;
+  constexpr uint32_t kSel = (1u << 4) | (1u << 29);  // scale byte kb of both operands
   for (int k0 = 0; k0 < nk; k0 += 4) {
     const int buf = m.group & 1;
     if (!wait(&c.sf_full[buf], (m.group >> 1) & 1, 24)) return false;
+    ptx::tc_fence_after();
     const uint32_t sf = tmem + kTmemScales + buf * 12;
+    bool good = true;
+    // one lane waits and issues for all four K blocks: with 32 rows the tensor pipe
+    // takes 300 clocks a block, and a wait of the whole warp for each is as long
+    if (elect_one()) {
+      int stage = m.stage;
+      uint32_t phase = m.phase;
 #pragma unroll
-    for (int kb = 0; kb < 4; ++kb) {
-      if (k0 + kb >= nk) break;
-      if (!wait(&c.full[m.stage], m.phase, 25)) return false;
-      ptx::tc_fence_after();
-      const uint64_t a0 = desc0 | ((smem + m.stage * kStageBytes) >> 4);
-      const uint64_t x = a0 + (2 * kWBytes >> 4);
-      constexpr uint32_t kSel = (1u << 4) | (1u << 29);  // scale byte kb of both operands
-      const uint32_t on = (k0 + kb) != 0;
-      if (elect_one()) {
+      for (int kb = 0; kb < 4; ++kb) {
+        if (k0 + kb >= nk) break;
+        good = ptx::mbar_wait(&c.full[stage], phase, &c.abort, kWaitLimitNs);
+        if (!good) break;
+        ptx::tc_fence_after();
+        const uint64_t a0 = desc0 | ((smem + stage * kStageBytes) >> 4);
+        const uint64_t x = a0 + (2 * kWBytes >> 4);
+        const uint32_t on = (k0 + kb) != 0;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           umma_mxf8(d, a0 + kk * 2, x + kk * 2, idesc | kb * kSel, sf, sf + 8, on | (kk != 0));
@@ -294,15 +308,23 @@ __device__ __forceinline__ bool mma_tile(SmemCtl& c, uint32_t smem, const RowsPa
             umma_mxf8(d + NT, a0 + (kWBytes >> 4) + kk * 2, x + kk * 2, idesc | kb * kSel, sf + 4,
                       sf + 8, on | (kk != 0));
         }
-        ptx::umma_commit(&c.empty[m.stage]);
+        ptx::umma_commit(&c.empty[stage]);
         if (kb == 3 || k0 + kb == nk - 1) ptx::umma_commit(&c.sf_empty[buf]);
         if (k0 + kb == nk - 1) ptx::umma_commit(&c.tmem_full[acc]);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
-      __syncwarp();
-      if (++m.stage == kStages) {
-        m.stage = 0;
-        m.phase ^= 1;
-      }
+    }
+    if (!__all_sync(0xffffffffu, good)) {
+      flag_timeout(c, p.status, 25);
+      return false;
+    }
+    m.stage += min(4, nk - k0);
+    if (m.stage >= kStages) {
+      m.stage -= kStages;
+      m.phase ^= 1;
     }
     ++m.group;
   }
@@ -402,12 +424,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap tmS1,
                         const __grid_constant__ CUtensorMap tmW2,
                         const __grid_constant__ CUtensorMap tmX2,
-                        const __grid_constant__ CUtensorMap tmS2, const RowsParams args) {
+                        const __grid_constant__ CUtensorMap tmS2, const RowsParams p) {
   extern __shared__ uint8_t dyn_smem[];
   __shared__ SmemCtl ctl;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) &
                                              ~uintptr_t(1023));
-  RowsParams p = args;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -440,29 +461,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int e = threadIdx.x; e <= p.E; e += blockDim.x)
     ctl.off[e] = (uint16_t)min(max((long long)p.off[e], 0ll), p.N);
   __syncthreads();
-  if (warp == 0) {  // row tiles of the experts -> exclusive prefix
-    int carry = 0;
-    for (int base = 0; base < p.E; base += 32) {
-      const int e = base + lane;
-      const int n = e < p.E ? max(0, (ctl.off[e + 1] - ctl.off[e] + NT - 1) / NT) : 0;
-      int incl = n;
+  if (warp == 0) {  // row tiles of the experts -> exclusive prefix, 8 experts a lane
+    int n[kMaxE / 32], sum = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      if (e < p.E) ctl.rtile[e] = (uint16_t)(carry + incl - n);
-      carry += __shfl_sync(0xffffffffu, incl, 31);
+    for (int k = 0; k < kMaxE / 32; ++k) {
+      const int e = lane * (kMaxE / 32) + k;
+      n[k] = sum;
+      if (e < p.E) sum += max(0, (ctl.off[e + 1] - ctl.off[e] + NT - 1) / NT);
     }
-    if (lane == 0) ctl.rtile[p.E] = (uint16_t)carry;
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+#pragma unroll
+    for (int k = 0; k < kMaxE / 32; ++k) {
+      const int e = lane * (kMaxE / 32) + k;
+      if (e < p.E) ctl.rtile[e] = (uint16_t)(incl - sum + n[k]);
+    }
+    if (lane == 31) ctl.rtile[p.E] = (uint16_t)incl;
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
-  // one token of the 128-expert layer has 64 second tiles of 256 columns: half of
-  // the SMs would have none (128 columns: 17.3 -> 15.2 us)
-  p.w2 = ctl.rtile[p.E] * ((p.H + 255) / 256) < (int)gridDim.x ? 128 : 256;
   const int total1 = ctl.rtile[p.E] * ncols<kFc1>(p);
   const int total = total1 + ctl.rtile[p.E] * ncols<kFc2>(p);
   int cur1 = 0, cur2 = 0;
@@ -562,7 +585,7 @@ moe_status_t launch_ffn_rows_fp8(const moe_layer_desc_t& d, const uint8_t* xq, c
       !make_map(&m[4], hq, 2, d.F, N, 1, NT, 1) || !make_map(&m[5], hq, 2, d.F, N, 1, kSmallBox, 1))
     return MOE_ERR_CUDA;
   const RowsParams p = {d.E, d.H, d.F, N, off, xs, w, a, h, hq, hs, o, status, dep,
-                        tile_counter(status), 0};
+                        tile_counter(status)};
   cudaError_t e = set_up();
   if (e == cudaSuccess) e = launch_zero_counters(dep, d.E, p.tile, st);
   // one CTA per SM, fewer when there cannot be as many tiles

@@ -151,6 +151,9 @@ CASES = {
     "max_experts": dict(T=200, H=128, E=256, k=8, F=64),
     "max_hidden": dict(T=40, H=16384, E=2, k=2, F=128),
     "max_inner": dict(T=40, H=128, E=2, k=2, F=16384),
+    "one_token_long": dict(T=1, H=4096, E=8, k=2, F=1408),
+    "one_token_short": dict(T=1, H=320, E=4, k=4, F=192),
+    "one_expert_many_rows": dict(T=40, H=704, E=1, k=1, F=1088),
     "few_rows_odd": dict(T=3, H=704, E=12, k=5, F=320),
     "long_expert": dict(T=700, H=256, E=2, k=2, F=384),
     # few rows an expert on average, a hundred at some: several row tiles
