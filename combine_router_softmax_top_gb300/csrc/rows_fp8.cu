@@ -21,9 +21,12 @@
 //   warps 8..11 scales into TMEM, ahead of the MMAs
 //
 // 64 tokens of the 128-expert layer (H 2048, F 768, top 8, skewed): 85 us, 7.0 TB/s,
-// the rate of a copy. One token: 16 us for 38 MB; its 48 tiles of the first product
-// read 512 KB each at what one SM takes in (about 100 GB/s), 5 us, and the rest is
-// the two launches, their set-up and the hand-over between the products.
+// the rate of a copy. One token: 16 us for 38 MB, a chain of latencies (clocks of a
+// CTA, weights in L2): set-up and tables 1900, the first tile's claim and loads 2900,
+// its 16 K blocks 10700, epilogue and count 2200, the second product's wait and
+// scales 3000, its K blocks 3500, epilogue and end 1500. Two CTAs a tile, half of K
+// each, were no faster: what the K loop saves, the cluster's barriers and the exchange
+// of sums cost again (15.0 against 15.1 us).
 #include <algorithm>
 #include <atomic>
 
@@ -43,7 +46,8 @@ constexpr int kStages = 6;
 constexpr int kThreads = 384;
 constexpr int kMaxE = 256;
 constexpr int kAccCols = 2 * NT;              // TMEM columns of one accumulator (two M tiles)
-constexpr int kTmemScales = 2 * kAccCols;     // two buffers of 12: two M tiles, the rows
+constexpr int kTmemScales = 2 * kAccCols;     // buffers of 12: two M tiles, the rows
+constexpr int kSf = 4;                        // (two: a buffer's turn-around is not covered)
 constexpr int kTmemCols = 256;
 constexpr int kSmallBox = 8;                  // rows of the small TMA box
 static_assert(kFp8FewRows * kMaxE < 65536, "16-bit tables");
@@ -69,7 +73,7 @@ struct Tile {
 
 struct SmemCtl {
   uint64_t full[kStages], empty[kStages];
-  uint64_t sf_full[2], sf_empty[2], tmem_full[2], tmem_empty[2], drain;
+  uint64_t sf_full[kSf], sf_empty[kSf], tmem_full[2], tmem_empty[2], drain;
   uint64_t sched_full[2], sched_empty[2], claim;  // claimed tiles
   int sched[2];
   uint32_t tmem_base;
@@ -240,9 +244,9 @@ __device__ __forceinline__ bool scales_tile(SmemCtl& c, const RowsParams& p, con
     uint32_t wb[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i) wb[i >> 2] |= __shfl_sync(0xffffffffu, b, i) << (8 * (i & 3));
-    const int buf = group & 1;
+    const int buf = group % kSf;
     const bool got =
-        ptx::mbar_wait(&c.sf_empty[buf], ((group >> 1) & 1) ^ 1, &c.abort, kWaitLimitNs);
+        ptx::mbar_wait(&c.sf_empty[buf], ((group / kSf) & 1) ^ 1, &c.abort, kWaitLimitNs);
     if (!__all_sync(0xffffffffu, got)) {
       if (lane == 0) flag_timeout(c, p.status, 22);
       return false;
@@ -281,22 +285,24 @@ __device__ __forceinline__ bool mma_tile(SmemCtl& c, uint32_t smem, const RowsPa
   ptx::tc_fence_after();
   const uint32_t d = tmem + acc * kAccCols;
   constexpr uint32_t kSel = (1u << 4) | (1u << 29);  // scale byte kb of both operands
-  for (int k0 = 0; k0 < nk; k0 += 4) {
-    const int buf = m.group & 1;
-    if (!wait(&c.sf_full[buf], (m.group >> 1) & 1, 24)) return false;
-    ptx::tc_fence_after();
-    const uint32_t sf = tmem + kTmemScales + buf * 12;
-    bool good = true;
-    // one lane waits and issues for all four K blocks: with 32 rows the tensor pipe
-    // takes 300 clocks a block, and a wait of the whole warp for each is as long
-    if (elect_one()) {
-      int stage = m.stage;
-      uint32_t phase = m.phase;
+  // One lane waits and issues for the whole tile: the eight MMAs of a K block take the
+  // tensor pipe 400 to 500 clocks, and waits of the whole warp as long again (one token
+  // of the 128-expert layer: 16.9 -> 15.9 us).
+  int where = 0;
+  if (elect_one()) {
+    int stage = m.stage;
+    uint32_t phase = m.phase, group = m.group;
+    for (int k0 = 0; k0 < nk && !where; k0 += 4, ++group) {
+      const int buf = group % kSf;
+      if (!ptx::mbar_wait(&c.sf_full[buf], (group / kSf) & 1, &c.abort, kWaitLimitNs)) where = 24;
+      const uint32_t sf = tmem + kTmemScales + buf * 12;
 #pragma unroll
       for (int kb = 0; kb < 4; ++kb) {
-        if (k0 + kb >= nk) break;
-        good = ptx::mbar_wait(&c.full[stage], phase, &c.abort, kWaitLimitNs);
-        if (!good) break;
+        if (k0 + kb >= nk || where) break;
+        if (!ptx::mbar_wait(&c.full[stage], phase, &c.abort, kWaitLimitNs)) {
+          where = 25;
+          break;
+        }
         ptx::tc_fence_after();
         const uint64_t a0 = desc0 | ((smem + stage * kStageBytes) >> 4);
         const uint64_t x = a0 + (2 * kWBytes >> 4);
@@ -317,17 +323,16 @@ __device__ __forceinline__ bool mma_tile(SmemCtl& c, uint32_t smem, const RowsPa
         }
       }
     }
-    if (!__all_sync(0xffffffffu, good)) {
-      flag_timeout(c, p.status, 25);
-      return false;
-    }
-    m.stage += min(4, nk - k0);
-    if (m.stage >= kStages) {
-      m.stage -= kStages;
-      m.phase ^= 1;
-    }
-    ++m.group;
   }
+  where = __reduce_max_sync(0xffffffffu, where);
+  if (where) {
+    flag_timeout(c, p.status, where);
+    return false;
+  }
+  m.group += (nk + 3) / 4;
+  const int at = m.stage + nk;
+  m.phase ^= (at / kStages) & 1;
+  m.stage = at % kStages;
   ++m.tiles;
   return true;
 }
@@ -435,9 +440,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&ctl.full[s], 1);
       ptx::mbar_init(&ctl.empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kSf; ++b) {
       ptx::mbar_init(&ctl.sf_full[b], 4);
       ptx::mbar_init(&ctl.sf_empty[b], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(&ctl.tmem_full[b], 1);
       ptx::mbar_init(&ctl.tmem_empty[b], 4);
       ptx::mbar_init(&ctl.sched_full[b], 1);
