@@ -342,49 +342,54 @@ _E4M3, _U8, _BF16, _I32T, _F32 = (torch.float8_e4m3fn, torch.uint8, torch.bfloat
                                   torch.float32)
 
 
-def _fp8_refuse(what, name, t, dt, n, dev):
-    if t is None:
-        why = "is None"
-    elif t.dtype is not dt:
-        why = f"is {t.dtype}, not {dt}"
-    elif not t.is_cuda or t.get_device() != dev:
-        why = f"is on {t.device}, not on the current CUDA device"
-    elif not t.is_contiguous():
-        why = "is not contiguous"
-    else:
-        why = f"has {t.numel()} elements, fewer than {abs(n)}"
-    raise MoeError(MOE_ERR_INVALID_ARG, what, f"{name} {why}")
+def _fp8_refuse(what, spec, tensors, sizes):
+    """Raises for the first argument that a call may not have."""
+    dev = _get_device() if torch.cuda.is_available() else -1
+    for (name, dt, may_be_none), t, n in zip(spec, tensors, sizes):
+        if t is None:
+            if may_be_none:
+                continue
+            why = "is None"
+        elif t.dtype is not dt:
+            why = f"is {t.dtype}, not {dt}"
+        elif not t.is_cuda or t.get_device() != dev:
+            why = f"is on {t.device}, not on the current CUDA device"
+        elif not t.is_contiguous():
+            why = "is not contiguous"
+        elif t.numel() < n:
+            why = f"has {t.numel()} elements, fewer than {n}"
+        else:
+            continue
+        raise MoeError(MOE_ERR_INVALID_ARG, what, f"{name} {why}")
+    raise MoeError(MOE_ERR_INVALID_ARG, what, "an argument was refused")
 
 
 _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _fp8_args(what: str, *args):
-    """Checks (name, tensor, dtype, least number of elements) of a call: contiguous
-    tensors of that type on the current device, or None where the size is negative
-    (optional). Returns their addresses."""
-    first = args[0][1]
-    dev = _get_device() if first is not None and first.is_cuda else -2
-    out = []
-    for name, t, dt, n in args:
+def _fp8_call(what, desc, spec, tensors, sizes, stream, *tail):
+    """Checks a call's tensors and makes it: of spec's types, contiguous, on the current
+    device, with at least so many elements, or None where spec allows it. Small calls
+    are bound by this function: no object is built that they do not need."""
+    first = tensors[0]
+    dev = -1 if first is None else first.get_device()
+    if dev < 0 or dev != _get_device():
+        _fp8_refuse(what, spec, tensors, sizes)
+    p = []
+    for t, (_, dt, may_be_none), n in zip(tensors, spec, sizes):
         if t is None:
-            if n >= 0:
-                _fp8_refuse(what, name, t, dt, n, dev)
-            out.append(None)
-        elif (t.dtype is dt and t.get_device() == dev and t.is_contiguous()
-              and t.numel() >= (n if n >= 0 else -n)):
-            out.append(t.data_ptr())
+            if not may_be_none:
+                _fp8_refuse(what, spec, tensors, sizes)
+            p.append(None)
+        elif (t.dtype is dt and t.numel() >= n and t.get_device() == dev and t.is_contiguous()):
+            p.append(t.data_ptr())
         else:
-            _fp8_refuse(what, name, t, dt, n, dev)
-    return out
-
-
-def _fp8_stream(stream):
-    """As _s, without building a Stream object for the current stream (2 us less a call)."""
-    if stream is None and _raw_stream is not None:
-        return _raw_stream(_get_device())
-    return _s(stream)
+            _fp8_refuse(what, spec, tensors, sizes)
+    st = _raw_stream(dev) if stream is None and _raw_stream is not None else _s(stream)
+    status = getattr(_lib or lib(), what)(ctypes.byref(desc), *p, *tail, st)
+    if status != MOE_OK:
+        _check(status, what)
 
 
 def _blocks(n: int) -> int:
@@ -396,67 +401,72 @@ def moe_fp8_scale_bytes(rows: int, blocks: int) -> int:
     return int(lib().moe_fp8_scale_bytes(int(rows), int(blocks)))
 
 
-def _words(rows: int, blocks: int) -> int:
-    return -(-blocks // 4) * 4 * rows
+def _words(rows: int, columns: int) -> int:  # bytes of the rows' scale words
+    return -(-columns // 512) * 4 * rows
+
+
+def _spec(names: str):
+    """(name, type, may be None) of a call's tensors, from "name:type" (type? may be None)."""
+    types = {"bf16": _BF16, "e4m3": _E4M3, "u8": _U8, "i32": _I32T, "f32": _F32}
+    return tuple((n, types[t.rstrip("?")], t.endswith("?"))
+                 for n, t in (w.split(":") for w in names.split()))
+
+
+_W8 = " w1q:e4m3 w1s:u8 w2q:e4m3 w2s:u8 "
+_SPEC_WEIGHTS = _spec("w1:bf16 w2:bf16" + _W8)
+_SPEC_PERMUTE = _spec("x:bf16 slot:i32 xq:e4m3 xs:u8")
+_SPEC_FWD = _spec("xq:e4m3 xs:u8 off:i32" + _W8 + "a:bf16? h:bf16? hq:e4m3 hs:u8 o:bf16 ws:u8")
+_SPEC_COMBINE_BWD = _spec("dy:bf16 o:bf16 slot:i32 gates:f32 d_o:bf16? dq:e4m3 ds:u8 dgates:f32")
+_SPEC_DGRAD = _spec("dq:e4m3 ds:u8 a:bf16 off:i32" + _W8
+                    + "da:bf16? daq:e4m3 das:u8 dx_perm:bf16 ws:u8")
 
 
 def moe_fp8_quantize_weights(desc, w1, w2, w1q, w1s, w2q, w2s, stream=None):
     """Expert weights into e4m3 and one scale for each 128 x 128 block."""
-    n, nb = desc.E * desc.F * desc.H, desc.E * _blocks(desc.F) * _blocks(desc.H)
-    what = "moe_fp8_quantize_weights"
-    p = _fp8_args(what, ("w1", w1, _BF16, 2 * n), ("w2", w2, _BF16, n), ("w1q", w1q, _E4M3, 2 * n),
-                  ("w1s", w1s, _U8, 2 * nb), ("w2q", w2q, _E4M3, n), ("w2s", w2s, _U8, nb))
-    _check(lib().moe_fp8_quantize_weights(_d(desc), *p, _fp8_stream(stream)), what)
+    E, H, F = desc.E, desc.H, desc.F
+    n, nb = E * F * H, E * _blocks(F) * _blocks(H)
+    _fp8_call("moe_fp8_quantize_weights", desc, _SPEC_WEIGHTS, (w1, w2, w1q, w1s, w2q, w2s),
+              (2 * n, n, 2 * n, 2 * nb, n, nb), stream)
 
 
 def moe_permute_fp8(desc, x, slot, xq, xs, stream=None):
     """Permute that quantises: e4m3 rows with one scale for each 128 columns."""
-    T, H, N = desc.T, desc.H, desc.T * desc.k
-    p = _fp8_args("moe_permute_fp8", ("x", x, _BF16, T * H), ("slot", slot, _I32T, N),
-                  ("xq", xq, _E4M3, N * H), ("xs", xs, _U8, _words(N, _blocks(H))))
-    _check(lib().moe_permute_fp8(_d(desc), *p, _fp8_stream(stream)), "moe_permute_fp8")
-
-
-def _fp8_weight_args(desc, w1q, w1s, w2q, w2s):
-    n, nb = desc.E * desc.F * desc.H, desc.E * _blocks(desc.F) * _blocks(desc.H)
-    return (("w1q", w1q, _E4M3, 2 * n), ("w1s", w1s, _U8, 2 * nb), ("w2q", w2q, _E4M3, n),
-            ("w2s", w2s, _U8, nb))
+    T, H = desc.T, desc.H
+    N = T * desc.k
+    _fp8_call("moe_permute_fp8", desc, _SPEC_PERMUTE, (x, slot, xq, xs),
+              (T * H, N, N * H, _words(N, H)), stream)
 
 
 def moe_expert_ffn_fwd_fp8(desc, xq, xs, off, w1q, w1s, w2q, w2s, a, h, hq, hs, o, ws,
                            stream=None):
     """Expert FFN forward on 8-bit operands; a and h may be None (serving)."""
-    H, F, N = desc.H, desc.F, desc.T * desc.k
-    what = "moe_expert_ffn_fwd_fp8"
-    p = _fp8_args(what, ("xq", xq, _E4M3, N * H), ("xs", xs, _U8, _words(N, _blocks(H))),
-                  ("off", off, _I32T, desc.E + 1), *_fp8_weight_args(desc, w1q, w1s, w2q, w2s),
-                  ("a", a, _BF16, -2 * N * F), ("h", h, _BF16, -N * F), ("hq", hq, _E4M3, N * F),
-                  ("hs", hs, _U8, _words(N, _blocks(F))), ("o", o, _BF16, N * H),
-                  ("ws", ws, _U8, 1))
-    _check(lib().moe_expert_ffn_fwd_fp8(_d(desc), *p, ws.numel(), _fp8_stream(stream)), what)
+    H, E, F, N = desc.H, desc.E, desc.F, desc.T * desc.k
+    n, nb = E * F * H, E * _blocks(F) * _blocks(H)
+    _fp8_call("moe_expert_ffn_fwd_fp8", desc, _SPEC_FWD,
+              (xq, xs, off, w1q, w1s, w2q, w2s, a, h, hq, hs, o, ws),
+              (N * H, _words(N, H), E + 1, 2 * n, 2 * nb, n, nb, 2 * N * F, N * F, N * F,
+               _words(N, F), N * H, 1), stream, 0 if ws is None else ws.numel())
 
 
 def moe_combine_bwd_fp8(desc, dy, o, slot, gates, d_o, dq, ds, dgates, stream=None):
     """Combine backward into 8-bit rows; d_o (the same rows in bf16) may be None."""
-    T, H, N = desc.T, desc.H, desc.T * desc.k
-    p = _fp8_args("moe_combine_bwd_fp8", ("dy", dy, _BF16, T * H), ("o", o, _BF16, N * H),
-                  ("slot", slot, _I32T, N), ("gates", gates, _F32, N), ("d_o", d_o, _BF16, -N * H),
-                  ("dq", dq, _E4M3, N * H), ("ds", ds, _U8, _words(N, _blocks(H))),
-                  ("dgates", dgates, _F32, N))
-    _check(lib().moe_combine_bwd_fp8(_d(desc), *p, _fp8_stream(stream)), "moe_combine_bwd_fp8")
+    T, H = desc.T, desc.H
+    N = T * desc.k
+    _fp8_call("moe_combine_bwd_fp8", desc, _SPEC_COMBINE_BWD,
+              (dy, o, slot, gates, d_o, dq, ds, dgates),
+              (T * H, N * H, N, N, N * H, N * H, _words(N, H), N), stream)
 
 
 def moe_expert_ffn_bwd_dgrad_fp8(desc, dq, ds, a, off, w1q, w1s, w2q, w2s, da, daq, das, dx_perm,
                                  ws, stream=None):
     """Expert FFN activation gradient on 8-bit operands; da (bf16) may be None."""
-    H, F, N = desc.H, desc.F, desc.T * desc.k
-    what = "moe_expert_ffn_bwd_dgrad_fp8"
-    p = _fp8_args(what, ("dq", dq, _E4M3, N * H), ("ds", ds, _U8, _words(N, _blocks(H))),
-                  ("a", a, _BF16, 2 * N * F), ("off", off, _I32T, desc.E + 1),
-                  *_fp8_weight_args(desc, w1q, w1s, w2q, w2s), ("da", da, _BF16, -2 * N * F),
-                  ("daq", daq, _E4M3, 2 * N * F), ("das", das, _U8, _words(N, 2 * _blocks(F))),
-                  ("dx_perm", dx_perm, _BF16, N * H), ("ws", ws, _U8, 1))
-    _check(lib().moe_expert_ffn_bwd_dgrad_fp8(_d(desc), *p, ws.numel(), _fp8_stream(stream)), what)
+    H, E, F, N = desc.H, desc.E, desc.F, desc.T * desc.k
+    n, nb = E * F * H, E * _blocks(F) * _blocks(H)
+    _fp8_call("moe_expert_ffn_bwd_dgrad_fp8", desc, _SPEC_DGRAD,
+              (dq, ds, a, off, w1q, w1s, w2q, w2s, da, daq, das, dx_perm, ws),
+              (N * H, _words(N, H), 2 * N * F, E + 1, 2 * n, 2 * nb, n, nb, 2 * N * F, 2 * N * F,
+               -(-2 * _blocks(F) // 4) * 4 * N, N * H, 1), stream,
+              0 if ws is None else ws.numel())
 
 
 def _fp8_fits(what, desc, bufs, fp8):

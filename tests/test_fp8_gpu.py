@@ -460,6 +460,17 @@ def test_no_tokens(T):
     assert float(b.dw1.abs().max()) == 0
 
 
+def test_no_tokens_without_the_saved_buffers():
+    c = Case(T=1, H=192, E=4, k=2, F=128, seed=25)
+    c.d = moe.LayerDesc.of(0, 192, 4, 2, 128)
+    c.off.zero_()
+    c.forward(save=False)
+    c.combine_bwd(save=False)
+    c.dgrad(save=False)
+    c.status()
+    assert float(c.o.min()) == 7 and float(c.dx.min()) == 7
+
+
 # ----------------------------------------------------------------------------- streams, graphs
 def test_side_stream_and_repeat_give_the_same_bits():
     c = Case(T=300, H=320, E=8, k=4, F=192, seed=12)
