@@ -49,8 +49,8 @@
 // SMs together. Skewed loads (95 to 4096 rows an expert) cost the gradient 230 to 240
 // us: half as many 256-row tiles again, their last rows empty, and a first product at
 // the pace of its epilogue (22000 clocks a tile, the K loop 14000). 64 experts of F 1408 at
-// 8192 tokens, nothing kept: 1134 GFLOP in 405 us alone (2.8 PFLOP/s, tensor pipe 73%
-// active), 480 us again and again, when the power limit lowers the clocks.
+// 8192 tokens, nothing kept: 1134 GFLOP in 410 us alone (2.8 PFLOP/s, tensor pipe 73%
+// active), 470 to 490 us again and again, when the power limit lowers the clocks.
 //
 // Ragged groups as in the bf16 GEMMs: expert e owns rows off[e]..off[e+1]-1; a
 // tile's rows past the expert's end are computed on whatever TMA loaded and
@@ -446,6 +446,7 @@ __device__ __forceinline__ bool scales_tile(SmemCtl& c, const KParams& p, const 
     bool ok = true;
     if (lane == 0) ok = wait_expert(c, p, t.e);
     if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+    __syncwarp();  // what lane 0 acquired, for all lanes
   }
   for (int g = 0; g * 4 < nk; ++g, ++group) {
     // row r of the tile: lane r % 32, column r / 32

@@ -237,6 +237,7 @@ __device__ __forceinline__ bool scales_tile(SmemCtl& c, const RowsParams& p, con
     bool ok = true;
     if (lane == 0) ok = wait_expert(c, p, t.e);
     if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+    __syncwarp();  // what lane 0 acquired, for all lanes
   }
   for (int g = 0; g * 4 < nk; ++g, ++group) {
     const uint32_t x = lane < t.rows ? __ldcg(words + (size_t)g * p.N + t.row + lane) : 0;
