@@ -470,11 +470,16 @@ def moe_expert_ffn_bwd_dgrad_fp8(desc, dq, ds, a, off, w1q, w1s, w2q, w2s, da, d
 
 
 def _fp8_fits(what, desc, bufs, fp8):
-    """Refuses buffers made for other sizes or for fewer rows than desc's."""
+    """Refuses buffers made for other sizes, for fewer rows than desc's, or on another
+    device than the current one."""
     for name, of in (("bufs", bufs.desc), ("fp8", fp8.desc)):
         if (of.H, of.E, of.F) != (desc.H, desc.E, desc.F) or of.T < desc.T or of.k != desc.k:
             raise MoeError(MOE_ERR_INVALID_ARG, what, f"{name} is of another layer: T={of.T} "
                            f"H={of.H} E={of.E} k={of.k} F={of.F}")
+    for name, t in (("bufs", bufs.x), ("fp8", fp8.xq), ("fp8's weights", fp8.w1q)):
+        if t.get_device() < 0 or t.get_device() != _get_device():
+            raise MoeError(MOE_ERR_INVALID_ARG, what,
+                           f"{name}: on {t.device}, not on the current CUDA device")
 
 
 def moe_layer_forward_fp8(desc, bufs: "LayerBuffers", fp8: "Fp8Buffers", save: bool = True,
@@ -513,6 +518,10 @@ class Fp8Buffers:
             self.w1q, self.w2q = z(E, 2 * F, H, dt=_E4M3), z(E, H, F, dt=_E4M3)
             self.w1s, self.w2s = z(E, 2, nf, nh, dt=_U8), z(E, nh, nf, dt=_U8)
         else:
+            of = weights.desc
+            if (of.H, of.E, of.F) != (H, E, F):
+                raise MoeError(MOE_ERR_INVALID_ARG, "Fp8Buffers", "weights are of another layer: "
+                               f"H={of.H} E={of.E} F={of.F}")
             self.w1q, self.w1s, self.w2q, self.w2s = (weights.w1q, weights.w1s, weights.w2q,
                                                       weights.w2s)
         self.xq, self.xs, self.hq, self.hs = rows(H), scales(nh), rows(F), scales(nf)

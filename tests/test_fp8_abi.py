@@ -159,3 +159,18 @@ def test_buffer_struct_follows_the_tensors():
     before = q.struct().w1q
     q.w1q = torch.empty_like(q.w1q)
     assert q.struct().w1q == q.w1q.data_ptr() != before
+
+
+@pytest.mark.parametrize("call", ["moe_layer_forward_fp8", "moe_layer_backward_fp8"])
+def test_layer_calls_refuse_buffers_in_host_memory(call):
+    with pytest.raises(moe.MoeError, match="CUDA device"):
+        getattr(moe, call)(D, moe.LayerBuffers(D, "cpu"), moe.Fp8Buffers(D, "cpu"))
+
+
+@pytest.mark.parametrize("other", [dict(H=128), dict(E=4), dict(F=128)])
+def test_shared_weights_are_of_the_same_layer(other):
+    q = moe.Fp8Buffers(D, "cpu")
+    assert moe.Fp8Buffers(moe.LayerDesc.of(T=1, H=192, E=8, k=1, F=192), "cpu", weights=q).w1q is q.w1q
+    theirs = moe.LayerDesc.of(**{**dict(T=16, H=192, E=8, k=2, F=192), **other})
+    with pytest.raises(moe.MoeError, match="another layer"):
+        moe.Fp8Buffers(theirs, "cpu", weights=q)
