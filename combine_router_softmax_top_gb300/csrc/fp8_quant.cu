@@ -80,7 +80,8 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(WeightMat m1, Wei
 // (four blocks, the four bytes of one scale word): it reads and rounds them
 // once and writes them to the token's k rows, so x is read once and only the
 // 8-bit rows are written. Lane j holds the token's j-th slot. 4096 tokens of 2048,
-// 8 rows each: 84 MB in 14.9 us, 5.7 TB/s; one token 5.6 us, the launch itself. (A
+// 8 rows each: 84 MB in 13.9 to 14.5 us, 6 TB/s (plain stores 14.9; with the forward behind
+// it, which reads the rows, 168.6 us either way); one token 5.5 us, the call itself. (A
 // token's blocks need no exchange between warps, so a decode batch has a warp for
 // every 512 columns.)
 __global__ void __launch_bounds__(256) permute_fp8_kernel(const bf16* __restrict__ x,
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(256) permute_fp8_kernel(const bf16* __restrict
     if (sl >= 0) xs[(size_t)seg * N + sl] = word;
     for (int j = 0; j < k; ++j) {
       const int s = __shfl_sync(0xffffffffu, sl, j);
-      if (s >= 0 && ok) *reinterpret_cast<uint4*>(xq + (size_t)s * H + col) = q;
+      if (s >= 0 && ok) __stcs(reinterpret_cast<uint4*>(xq + (size_t)s * H + col), q);
     }
   }
 }

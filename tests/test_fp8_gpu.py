@@ -269,6 +269,25 @@ def test_dgrad_stages(case):
     print(r)
 
 
+@pytest.mark.parametrize("seed", range(10))
+def test_seeded_random_shapes(seed):
+    rng = np.random.default_rng(700 + seed)
+    E = int(rng.choice([1, 3, 8, 40, 128, 256]))
+    c = Case(T=int(rng.choice([1, 2, 17, 64, 200, 900])), H=64 * int(rng.integers(1, 13)), E=E,
+             k=int(rng.integers(1, min(E, 8) + 1)), F=64 * int(rng.integers(1, 10)),
+             kind=("balanced", "skewed")[seed % 2], seed=seed)
+    c.quantize()
+    c.permute()
+    c.forward()
+    c.combine_bwd()
+    c.dgrad()
+    c.status()
+    test_permute_bit_exact(c)
+    test_forward_stages(c)
+    test_combine_bwd_stages(c)
+    test_dgrad_stages(c)
+
+
 def test_serving_gives_the_same_bits(case):
     """Without a, h, d_o and da the results are those of the calls that store them."""
     o, hq, dq, dx = (t.clone().view(torch.uint8) for t in (case.o, case.q.hq, case.q.dq, case.dx))
