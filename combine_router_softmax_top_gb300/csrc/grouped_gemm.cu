@@ -39,17 +39,8 @@
 #include "moe_internal.cuh"
 #include "sm100_ptx.cuh"
 
-#ifndef MOE_ROW_CS
-#define MOE_ROW_CS 1
-#endif
 #ifndef MOE_PAIR
 #define MOE_PAIR 1
-#endif
-#ifndef MOE_WG1_CS
-#define MOE_WG1_CS 2
-#endif
-#ifndef MOE_WG2_CS
-#define MOE_WG2_CS 2
 #endif
 
 namespace moe {
@@ -81,26 +72,24 @@ struct Mode {
   static constexpr bool kRagK = MODE == GEMM_WGRAD_W1 || MODE == GEMM_WGRAD_W2;
   static constexpr int kAMn = kRagK ? 1 : 0;
   static constexpr int kBMn = (MODE == GEMM_FC2_DGRAD || MODE == GEMM_FC1_DGRAD || kRagK) ? 1 : 0;
-  // CTAs per cluster: kCS consecutive M blocks of one (expert, N block) share
-  // the B tile; each CTA loads a slice and multicasts it to all of them.
   // CTA pairs (tcgen05 cta_group::2): M = 256 rows per MMA, each CTA loading
   // its own 128 rows of A and half of B, so a CTA takes in 32 KB per K stage
   // instead of 48 KB and holds 6 stages. Pairs speed up the forward and dgrad
   // GEMMs. The short-K wgrad tiles (4 K stages per expert at 256 rows) stay
-  // unpaired and share B across a cluster by multicast. Measured on the
-  // 256-rows-per-expert layer, clusters of 2 are fastest (W1 201 us against
-  // 208 us unclustered and 220 to 223 us with 3, 4 or 6 CTAs; W2 115 us with
-  // 2 to 4, 129 us with 8). A paired wgrad (each CTA loading its own A and
-  // half of B, 128 KB per 128 x 256 output instead of 192 KB received) stays
-  // slower even with the pair handshakes trimmed (one arrival per stage, the
-  // odd CTA's accumulator release forwarded once per tile): W1 222 us, W2
-  // 130 us. A trace shows each short tile's MMA resuming 1.3 to 1.6 us after
-  // both epilogues released the accumulator, a latency two accumulators do
-  // not hide when a tile's MMAs take 1.2 us.
+  // unpaired, every CTA loading the whole 48 KB of its stages; consecutive
+  // CTAs take consecutive M blocks of one (expert, N block), so B comes out of
+  // L2. On the 256-rows-per-expert layer W1 and W2 in one launch take 311 us so
+  // (W1 alone 208), on the skewed one 406. A paired wgrad
+  // (128 KB per 128 x 256 output instead of 192 KB received) is slower even
+  // with the pair handshakes trimmed (one arrival per stage, the odd CTA's
+  // accumulator release forwarded once per tile): W1 222 us, W2 130 us. A
+  // trace shows each short tile's MMA resuming 1.3 to 1.6 us after both
+  // epilogues released the accumulator, a latency two accumulators do not hide
+  // when a tile's MMAs take 1.2 us. (Loads that land B in both CTAs of a
+  // cluster at once took 305 and 389 us, but this library also runs with one
+  // rank on each of several GPUs, where such loads are not to be used.)
   static constexpr bool kPair = MOE_PAIR && !kRagK;
-  static constexpr int kCS = kPair ? 2
-                            : MODE == GEMM_WGRAD_W1 ? MOE_WG1_CS
-                            : MODE == GEMM_WGRAD_W2 ? MOE_WG2_CS : MOE_ROW_CS;
+  static constexpr int kCS = kPair ? 2 : 1;  // CTAs of a tile
   // The FC2 dgrad epilogue needs the tile's saved pre-activation (gate and up)
   // next to the accumulator: a dedicated warp TMA-loads it into shared memory
   // ahead of the epilogue, one 64-column quarter (gate and up, 32 KB) at a time.
@@ -176,10 +165,8 @@ __device__ __forceinline__ Tile tile_at(const KParams& p, const int* tstart, con
   const int cnt = off[t.e + 1] - t.row0;
   const int local = tile - tstart[cursor];
   if (Mode<MODE>::kRagK) {
-    // one cluster tile = kCS consecutive M blocks of one (expert, N block)
-    constexpr int cs = Mode<MODE>::kCS;
-    const int mg = ((Mode<MODE>::wg_mdim(p) + BM - 1) / BM + cs - 1) / cs;
-    t.m0 = ((local % mg) * cs + (int)rank) * BM;
+    const int mg = (Mode<MODE>::wg_mdim(p) + BM - 1) / BM;
+    t.m0 = (local % mg) * BM;
     t.n0 = (local / mg) * BN;
     t.rows = cnt;
     t.nk = (cnt + BK - 1) / BK;
@@ -398,7 +385,6 @@ struct Role {
   uint8_t* smem;
   SmemCtl* ctl;
   uint32_t crank;
-  uint16_t cmask;
   uint32_t tmem_base;
   int lane;
 };
@@ -422,7 +408,7 @@ __device__ __forceinline__ void tile_prefix(const KParams& p, const int* off, co
     if (pos < p.E) {
       const int cnt = off[e + 1] - off[e];
       if (M::kRagK)
-        n = (((M::wg_mdim(p) + BM - 1) / BM + M::kCS - 1) / M::kCS) * M::ntiles(p);
+        n = ((M::wg_mdim(p) + BM - 1) / BM) * M::ntiles(p);
       else n = (((cnt + BM - 1) / BM + M::kCS - 1) / M::kCS) * M::ntiles(p);
       if (cnt < 0) n = 0;
     }
@@ -485,7 +471,6 @@ __device__ __forceinline__ bool producer_tile(const Role& R, const KParams& p,
   SmemCtl& ctl = *R.ctl;
   const int lane = R.lane;
   const uint32_t crank = R.crank;
-  const uint16_t cmask = R.cmask;
   for (int kt = 0; kt < t.nk; ++kt) {
     if (!ptx::mbar_wait(&ctl.empty[stage], phase ^ 1, &ctl.abort, kWaitLimitNs)) {
       if (lane == 0) flag_timeout(ctl, p.status, 1);
@@ -497,24 +482,15 @@ __device__ __forceinline__ bool producer_tile(const Role& R, const KParams& p,
     uint64_t* bar = &ctl.full[stage];
     if (lane == 0) {
       if (M::kRagK) {
-        // A: this CTA's own M block. B: slice i of the shared tile is loaded
-        // by cluster rank i % kCS and multicast to every CTA of the cluster,
-        // so full[stage] collects all 32 KB of B in every CTA. In the last K
-        // stage of an expert the rows past its end are the next expert's;
-        // the MMA warp zeroes them in A once the stage has landed, so the
-        // producer never waits for a load.
-        ptx::mbar_arrive_expect_tx(&ctl.full[stage], M::kStageBytes);
+        // In the last K stage of an expert the rows past its end are the next
+        // expert's; the MMA warp zeroes them in A once the stage has landed,
+        // so the producer never waits for a load.
+        ptx::mbar_arrive_expect_tx(bar, M::kStageBytes);
         const int r = t.row0 + k0;
         ptx::tma_load_2d(sA, tmA, bar, t.m0, r);
         ptx::tma_load_2d(sA + 8192, tmA, bar, t.m0 + 64, r);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (M::kCS == 1)
-            ptx::tma_load_2d(sB + 8192 * i, tmB, &ctl.full[stage], t.n0 + 64 * i, r);
-          else if (i % M::kCS == (int)crank)
-            ptx::tma_load_2d_multicast(sB + 8192 * i, tmB, &ctl.full[stage], t.n0 + 64 * i, r,
-                                       cmask);
-        }
+        for (int i = 0; i < 4; ++i) ptx::tma_load_2d(sB + 8192 * i, tmB, bar, t.n0 + 64 * i, r);
       } else if (M::kPair) {
         // both CTAs' loads complete on the even CTA's full[stage]
         const uint32_t fb = ptx::mapa_shared(&ctl.full[stage], 0);
@@ -534,24 +510,18 @@ __device__ __forceinline__ bool producer_tile(const Role& R, const KParams& p,
       } else {
         ptx::mbar_arrive_expect_tx(bar, M::kStageBytes);
         ptx::tma_load_2d(sA, tmA, bar, k0, t.row0 + t.m0);
-        // B boxes: box i is loaded by cluster rank i % kCS and multicast
-        auto load_b = [&](int i, void* dst, int c0, int c1) {
-          if (M::kCS == 1)
-            ptx::tma_load_2d(dst, tmB, bar, c0, c1);
-          else if (i % M::kCS == (int)crank)
-            ptx::tma_load_2d_multicast(dst, tmB, bar, c0, c1, cmask);
-        };
+        auto load_b = [&](void* dst, int c0, int c1) { ptx::tma_load_2d(dst, tmB, bar, c0, c1); };
         if (MODE == GEMM_FC1_FWD) {
           const int base = t.e * 2 * p.F;
-          load_b(0, sB, k0, base + t.n0);                // 128 gate rows
-          load_b(1, sB + 16384, k0, base + p.F + t.n0);  // 128 up rows
+          load_b(sB, k0, base + t.n0);                // 128 gate rows
+          load_b(sB + 16384, k0, base + p.F + t.n0);  // 128 up rows
         } else if (MODE == GEMM_FC2_FWD) {
-          load_b(0, sB, k0, t.e * p.H + t.n0);
-          load_b(1, sB + 16384, k0, t.e * p.H + t.n0 + 128);
+          load_b(sB, k0, t.e * p.H + t.n0);
+          load_b(sB + 16384, k0, t.e * p.H + t.n0 + 128);
         } else {
           const int base = MODE == GEMM_FC2_DGRAD ? t.e * p.H : t.e * 2 * p.F;
 #pragma unroll
-          for (int i = 0; i < M::kBN / 64; ++i) load_b(i, sB + 8192 * i, t.n0 + 64 * i, base + k0);
+          for (int i = 0; i < M::kBN / 64; ++i) load_b(sB + 8192 * i, t.n0 + 64 * i, base + k0);
         }
       }
     }
@@ -631,10 +601,8 @@ __device__ __forceinline__ bool mma_tile(const Role& R, const KParams& p, const 
           ptx::umma_bf16(d_tmem, adesc + (uint64_t)(kk * a_adv), bdesc + (uint64_t)(kk * b_adv),
                          idesc, (kt | kk) != 0);
       }
-      // the stage is free once every CTA whose shared memory the MMAs read
-      // (pair) or that received the multicast B slices has consumed it
+      // the stage is free once the MMAs have read it (pair: in both CTAs)
       if (M::kPair) ptx::umma_commit_pair(&ctl.empty[stage], 3);
-      else if (M::kCS > 1) ptx::umma_commit_multicast(&ctl.empty[stage], R.cmask);
       else ptx::umma_commit(&ctl.empty[stage]);
     }
     if (++stage == KSTAGES) {
@@ -868,9 +836,8 @@ __global__ void __launch_bounds__(Fuse<MODE, MODE2>::kWarps * 32, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < KS; ++s) {
       ptx::mbar_init(&ctl.full[s], 1);
-      // multicast B: every CTA of the cluster releases the stage; pair: the
-      // even CTA's MMA releases it in both CTAs
-      ptx::mbar_init(&ctl.empty[s], F::kPair ? 1 : F::kCS);
+      // pair: the even CTA's MMA releases the stage in both CTAs
+      ptx::mbar_init(&ctl.empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(&ctl.tmem_full[b], 1);
@@ -919,9 +886,6 @@ __global__ void __launch_bounds__(Fuse<MODE, MODE2>::kWarps * 32, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  // peers multicast into this CTA's shared memory and barriers: all must be
-  // initialised first
-  if (F::kCS > 1 && !F::kPair) ptx::cluster_sync();
   const int total1 = ctl.tstart[E];
   const int total = total1 + (F::kHas2 ? ctl.tstart2[E] : 0);
   Role R;
@@ -929,7 +893,6 @@ __global__ void __launch_bounds__(Fuse<MODE, MODE2>::kWarps * 32, 1)
   R.ctl = &ctl;
   R.tmem_base = ctl.tmem_base;
   R.crank = F::kCS > 1 ? ptx::cluster_ctarank() : 0;
-  R.cmask = (uint16_t)((1u << F::kCS) - 1u);
   R.lane = lane;
   const int first = F::kCS > 1 ? (int)ptx::cluster_id_x() : (int)blockIdx.x;
   const int stride = F::kCS > 1 ? (int)ptx::cluster_count_x() : (int)gridDim.x;
@@ -1234,13 +1197,11 @@ bool mode_setup(const moe_layer_desc_t& d, const GemmArgs& g, CUtensorMap (&m)[4
       break;
     case GEMM_WGRAD_W1:
       ok = make_map(&m[0], g.A, N, 2 * F, 64) && make_map(&m[1], g.B, N, H, 64);
-      ntile_bound = (long long)E * ceil_div(ceil_div(2 * F, BM), Mode<GEMM_WGRAD_W1>::kCS) *
-                    Mode<GEMM_WGRAD_W1>::kCS * ((H + BN - 1) / BN);
+      ntile_bound = (long long)E * ceil_div(2 * F, BM) * ((H + BN - 1) / BN);
       break;
     case GEMM_WGRAD_W2:
       ok = make_map(&m[0], g.A, N, H, 64) && make_map(&m[1], g.B, N, F, 64);
-      ntile_bound = (long long)E * ceil_div(ceil_div(H, BM), Mode<GEMM_WGRAD_W2>::kCS) *
-                    Mode<GEMM_WGRAD_W2>::kCS * ((F + BN - 1) / BN);
+      ntile_bound = (long long)E * ceil_div(H, BM) * ((F + BN - 1) / BN);
       break;
     default:
       set_error("unknown grouped GEMM mode %d", g.mode);
