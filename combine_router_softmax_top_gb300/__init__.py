@@ -470,12 +470,14 @@ def moe_expert_ffn_bwd_dgrad_fp8(desc, dq, ds, a, off, w1q, w1s, w2q, w2s, da, d
 
 
 def _fp8_fits(what, desc, bufs, fp8):
-    """Refuses buffers made for other sizes, for fewer rows than desc's, or on another
-    device than the current one."""
+    """Refuses buffers made for other sizes, for fewer rows than desc's, for another number
+    of ranks (the 8-bit buffers have no part in that), or on another device than the
+    current one."""
     for name, of in (("bufs", bufs.desc), ("fp8", fp8.desc)):
-        if (of.H, of.E, of.F) != (desc.H, desc.E, desc.F) or of.T < desc.T or of.k != desc.k:
+        if ((of.H, of.E, of.F) != (desc.H, desc.E, desc.F) or of.T < desc.T or of.k != desc.k
+                or (of is bufs.desc and of.R != desc.R)):
             raise MoeError(MOE_ERR_INVALID_ARG, what, f"{name} is of another layer: T={of.T} "
-                           f"H={of.H} E={of.E} k={of.k} F={of.F}")
+                           f"H={of.H} E={of.E} k={of.k} F={of.F} R={of.R}")
     for name, t in (("bufs", bufs.x), ("fp8", fp8.xq), ("fp8's weights", fp8.w1q)):
         if t.get_device() < 0 or t.get_device() != _get_device():
             raise MoeError(MOE_ERR_INVALID_ARG, what,

@@ -174,3 +174,15 @@ def test_shared_weights_are_of_the_same_layer(other):
     theirs = moe.LayerDesc.of(**{**dict(T=16, H=192, E=8, k=2, F=192), **other})
     with pytest.raises(moe.MoeError, match="another layer"):
         moe.Fp8Buffers(theirs, "cpu", weights=q)
+
+
+@pytest.mark.parametrize("call", ["moe_layer_forward_fp8", "moe_layer_backward_fp8"])
+@pytest.mark.parametrize("mine,theirs", [(8, 1), (1, 8), (2, 4)])
+def test_layer_calls_refuse_buffers_of_another_number_of_ranks(call, mine, theirs):
+    """rank_off has R + 1 entries, which the layout writes: R=1's buffers are too small for R=8."""
+    of = lambda r: moe.LayerDesc.of(T=16, H=192, E=8, k=2, F=192, R=r)  # noqa: E731
+    with pytest.raises(moe.MoeError, match=f"bufs is of another layer: .*R={theirs}$"):
+        getattr(moe, call)(of(mine), moe.LayerBuffers(of(theirs), "cpu"), moe.Fp8Buffers(of(mine), "cpu"))
+    # the 8-bit buffers do not depend on it: the call gets as far as their place
+    with pytest.raises(moe.MoeError, match="CUDA device"):
+        getattr(moe, call)(of(mine), moe.LayerBuffers(of(mine), "cpu"), moe.Fp8Buffers(of(theirs), "cpu"))
