@@ -45,6 +45,10 @@ class LayerDesc(ctypes.Structure):
     def as_dict(self):
         return {n: getattr(self, n) for n, _ in self._fields_}
 
+    def copy(self):
+        """What a buffer set keeps of the descriptor that it was made for."""
+        return LayerDesc(**self.as_dict())
+
 
 _MB_FIELDS = ["x", "dy", "w_r", "bias", "w1", "w2", "logits", "idx", "gates", "cnt", "off",
               "slot", "row_src", "cnt_re", "rank_off", "x_perm", "a", "h", "o", "y", "d_o",
@@ -515,7 +519,7 @@ class Fp8Buffers:
         z = lambda *s, dt: torch.zeros(*s, dtype=torch.uint8, device=device).view(dt)  # noqa: E731
         rows = lambda c: z(N, c, dt=_E4M3)  # noqa: E731
         scales = lambda nb: z(-(-nb // 4), N, 4, dt=_U8)  # noqa: E731
-        self.desc = desc
+        self.desc = desc.copy()
         if weights is None:
             self.w1q, self.w2q = z(E, 2 * F, H, dt=_E4M3), z(E, H, F, dt=_E4M3)
             self.w1s, self.w2s = z(E, 2, nf, nh, dt=_U8), z(E, nh, nf, dt=_U8)
@@ -551,7 +555,7 @@ class LayerBuffers:
         T = max(T, 1)  # zero-token layers still get valid (unused) pointers
         bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
         z = lambda *s, dt: torch.zeros(*s, dtype=dt, device=device)  # noqa: E731
-        self.desc = desc
+        self.desc = desc.copy()
         self.x, self.dy = z(T, H, dt=bf), z(T, H, dt=bf)
         if weights is None:
             self.w_r, self.w1, self.w2 = z(E, H, dt=bf), z(E, 2 * F, H, dt=bf), z(E, H, F, dt=bf)

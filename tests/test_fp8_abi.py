@@ -186,3 +186,15 @@ def test_layer_calls_refuse_buffers_of_another_number_of_ranks(call, mine, their
     # the 8-bit buffers do not depend on it: the call gets as far as their place
     with pytest.raises(moe.MoeError, match="CUDA device"):
         getattr(moe, call)(of(mine), moe.LayerBuffers(of(mine), "cpu"), moe.Fp8Buffers(of(theirs), "cpu"))
+
+
+@pytest.mark.parametrize("call", ["moe_layer_forward_fp8", "moe_layer_backward_fp8"])
+def test_buffers_know_the_sizes_that_they_were_made_for(call):
+    """A descriptor changed after its buffers were made does not take them along."""
+    d = moe.LayerDesc.of(T=16, H=192, E=8, k=2, F=192)
+    b, q = moe.LayerBuffers(d, "cpu"), moe.Fp8Buffers(d, "cpu")
+    d.T = 32
+    with pytest.raises(moe.MoeError, match="bufs is of another layer: T=16 "):
+        getattr(moe, call)(d, b, q)
+    with pytest.raises(moe.MoeError, match="fp8 is of another layer: T=16 "):
+        getattr(moe, call)(d, moe.LayerBuffers(d, "cpu"), q)
