@@ -180,8 +180,8 @@ __device__ __forceinline__ bool producer_tile(SmemCtl& c, uint8_t* smem, const R
   const int w1 = w0 + (G == kFc1 ? p.F : 128);
   const bool small = t.rows <= NT / 2;
   const int xrows = small ? (t.rows + kSmallBox - 1) / kSmallBox * kSmallBox : NT;
-  bool ready = G == kFc1;
-  for (int kt = 0; kt < nk; ++kt) {
+  bool ready = G == kFc1, ok = true;
+  for (int kt = 0; kt < nk && ok; ++kt) {
     if (!ptx::mbar_wait(&c.empty[stage], phase ^ 1, &c.abort, kWaitLimitNs)) {
       flag_timeout(c, p.status, 21);
       return false;
@@ -194,7 +194,8 @@ __device__ __forceinline__ bool producer_tile(SmemCtl& c, uint8_t* smem, const R
     ptx::tma_load_2d(s, tmW, bar, k0, w0);
     if (mt == 2) ptx::tma_load_2d(s + kWBytes, tmW, bar, k0, w1);
     if (!ready) {  // the weights do not wait for the first product, its rows do
-      if (!wait_expert(c, p, t.e)) return false;
+      // (after an abort the stage is still loaded whole: drain_loads waits for stages)
+      ok = wait_expert(c, p, t.e);
       asm volatile("fence.proxy.async.global;" ::: "memory");
       ready = true;
     }
@@ -208,7 +209,7 @@ __device__ __forceinline__ bool producer_tile(SmemCtl& c, uint8_t* smem, const R
       phase ^= 1;
     }
   }
-  return true;
+  return ok;
 }
 
 // Scale byte of weight block (K block kb, M tile i).

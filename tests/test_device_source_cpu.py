@@ -17,6 +17,16 @@ def code(path):
     return re.sub(r'"\s*\n?\s*"', "", s)
 
 
+def rest_of_block(text):
+    """Up to the brace that closes the block in which the text begins."""
+    depth = 0
+    for i, c in enumerate(text):
+        depth += (c == "{") - (c == "}")
+        if depth < 0:
+            return text[:i]
+    return text
+
+
 @pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
 def test_no_load_is_multicast(path):
     """The library runs with one rank on each of several GPUs: a TMA load fills its own CTA's
@@ -24,3 +34,20 @@ def test_no_load_is_multicast(path):
     for s in re.findall(r'"(?:[^"\\]|\\.)*"', code(path)):
         for instruction in s.replace("\\n", ";").replace("\\t", " ").split(";"):
             assert not ("cp.async.bulk" in instruction and "multicast" in instruction), instruction
+
+
+def test_an_announced_stage_is_loaded_whole():
+    """A producer that gives up leaves no stage of its operand ring with some of the announced
+    bytes on their way: after an abort the loads in flight are waited for by whole stages
+    (drain_loads), so none may write into shared memory that is no longer the kernel's."""
+    seen = 0
+    for path in SOURCES:
+        text = code(path)
+        if "drain_loads(" not in text:
+            continue
+        for at in re.finditer(r"mbar_arrive_expect_tx\(", text):
+            stage = rest_of_block(text[at.start():])
+            if "tma_load" in stage:
+                seen += 1
+                assert "return" not in stage, (os.path.basename(path), stage)
+    assert seen >= 2
