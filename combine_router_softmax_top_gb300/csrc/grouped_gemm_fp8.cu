@@ -25,7 +25,7 @@
 //               rounding, block maxima, e4m3 -> global; two warps per TMEM lane
 //               quarter, each owning 64 of every 128 columns
 // Tiles are claimed in order from a counter, the first GEMM's before the second's
-// (the odd CTA's warp 1 claims for the pair, up to two ahead of what the slowest
+// (the odd CTA's warp 1 claims for the pair, up to two ahead of what its slowest
 // warp works on; the second once the first is under way, or with few tiles half of
 // the pairs would take two each). A tile of the second GEMM starts once every tile
 // of its expert in the first has been stored (per-expert counters): those have been
@@ -107,6 +107,7 @@ struct Chain {
   static_assert(!kAux || kAuxAt + 2 * kAuxBytes <= kEpiAt, "the pre-activations' room");
 };
 constexpr int kMaxBars = 10;
+constexpr int kHalf = 8;  // slots of half a mailbox (below)
 
 struct Maps {
   CUtensorMap a1, s1, b1, a2, s2, b2;  // operands: A, A in small boxes, B of both GEMMs
@@ -156,9 +157,10 @@ struct SmemCtl {
   uint64_t paired[4];  // both warps of a quarter have left their block maxima
   uint64_t sf_full[kSf], sf_empty[kSf];
   uint64_t tmem_full[2], tmem_empty[2], ovl, drain;
-  uint64_t sched_full[2], sched_empty[2];  // claimed tiles
+  uint64_t mail_full[2 * kHalf], mail_empty[2];  // claimed tiles, from the odd CTA to both producers
+  uint64_t sched_full[2], sched_empty[2];  // and from the producer to the others of its CTA
   uint64_t claim;                          // odd CTA: time to claim the second tile
-  int sched[2];
+  int mail[2 * kHalf], sched[2];
   uint64_t stored[2], counted[2];  // a first-GEMM tile's stores issued; counted for its expert
   uint32_t tmem_base;
   int abort;
@@ -289,45 +291,79 @@ __device__ __forceinline__ bool wait_expert(SmemCtl& c, const KParams& p, int e)
 }
 
 // ================================================================ tiles
-// What reads the claimed tiles: producer, counting warp, scale and epilogue warps
-// in both CTAs, the MMA issuer in one (and the gradient's aux loaders).
-constexpr int kReaders = 2 * (1 + 1 + 4 + 8) + 1;
+// The odd CTA claims for the pair and leaves the tile in a mailbox in each CTA; that
+// CTA's producer, which needs it first, takes it out and hands it to the others of its
+// CTA. So one thread of the even CTA, with no stores in flight, releases what it read
+// to the odd one, and as a release at cluster scope takes some 3000 clocks with stores
+// in flight on the SM, it does so once in kHalf tiles: the mailbox has two halves of as
+// many slots. (Once a tile: the balanced forward 180 us against 160 so, the gradient 191
+// against 180, prefill 515 against 499, in turn on one GPU; by every warp of the pair, as
+// slow.)
+//
+// What reads the tiles of a CTA beside the producer: counting warp, scale and epilogue
+// warps, the MMA issuer in the even one (and the gradient's aux loader).
+__device__ __forceinline__ int readers(uint32_t rank, bool aux) {
+  return 1 + 4 + 8 + (rank == 0) + aux;
+}
+// Relaxed: for accesses to TMEM alone, which the tcgen05 fences on both sides order.
 __device__ __forceinline__ void arrive_remote(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
                : "memory");
 }
-// The n-th tile claimed for this pair (past the last: none is left; -1: gave up).
-// Every lane of a warp that passes warp = true calls it together.
+// The producer: takes the n-th tile claimed for this pair (past the last: none is left; -1:
+// gave up) out of the mailbox and hands it on.
+__device__ __forceinline__ int take_tile(SmemCtl& c, uint32_t n, int* status) {
+  const int slot = n % (2 * kHalf);
+  const uint32_t round = n / (2 * kHalf);
+  if (!mbar_wait_cluster(&c.mail_full[slot], round & 1, &c.abort)) {
+    flag_timeout(c, status, 14);
+    return -1;
+  }
+  const int i = *(volatile int*)&c.mail[slot];
+  if (slot % kHalf == kHalf - 1)  // the half has been read
+    ptx::mbar_arrive_cluster(ptx::mapa_shared(&c.mail_empty[slot / kHalf], 1));
+  if (!ptx::mbar_wait(&c.sched_empty[n & 1], ((n >> 1) & 1) ^ 1, &c.abort, kWaitLimitNs)) {
+    flag_timeout(c, status, 18);
+    return -1;
+  }
+  *(volatile int*)&c.sched[n & 1] = i;
+  ptx::mbar_arrive(&c.sched_full[n & 1]);
+  return i;
+}
+// The others: the n-th tile. Every lane of a warp that passes warp = true calls it together.
 __device__ __forceinline__ int next_tile(SmemCtl& c, uint32_t n, int* status, bool warp) {
-  bool ok = mbar_wait_cluster(&c.sched_full[n & 1], (n >> 1) & 1, &c.abort);
+  bool ok = ptx::mbar_wait(&c.sched_full[n & 1], (n >> 1) & 1, &c.abort, kWaitLimitNs);
   if (warp) ok = __all_sync(0xffffffffu, ok);
   if (!ok) {
-    flag_timeout(c, status, 14);
+    flag_timeout(c, status, 19);
     return -1;
   }
   const int i = *(volatile int*)&c.sched[n & 1];
   if (warp) __syncwarp();
-  // the slot is free once it has been read: the address depends on what was (never
-  // negative), so that the relaxed arrival cannot pass the load
-  if (!warp || (threadIdx.x & 31) == 0)
-    arrive_remote(ptx::mapa_shared(&c.sched_empty[n & 1], 1) + (uint32_t)min(i, 0));
+  if (!warp || (threadIdx.x & 31) == 0) ptx::mbar_arrive(&c.sched_empty[n & 1]);
   return i;
 }
-// Claims tiles for the pair until none is left (one thread of the odd CTA).
+// Claims tiles for the pair until none is left (one thread of the odd CTA): each once
+// this CTA's warps have read the last but one, and both producers, for the first of a
+// half, what that half held.
 __device__ __forceinline__ void claim_tiles(SmemCtl& c, const KParams& p, int first, int total) {
   for (uint32_t n = 0;; ++n) {
+    const int slot = n % (2 * kHalf);
+    const uint32_t round = n / (2 * kHalf);
     if ((n == 1 && !ptx::mbar_wait(&c.claim, 0, &c.abort, kWaitLimitNs)) ||
-        !mbar_wait_cluster(&c.sched_empty[n & 1], ((n >> 1) & 1) ^ 1, &c.abort)) {
+        !ptx::mbar_wait(&c.sched_empty[n & 1], ((n >> 1) & 1) ^ 1, &c.abort, kWaitLimitNs) ||
+        (slot % kHalf == 0 &&
+         !mbar_wait_cluster(&c.mail_empty[slot / kHalf], (round & 1) ^ 1, &c.abort))) {
       flag_timeout(c, p.status, 15);
       return;
     }
     const int i = min(n > 0 ? atomicAdd(p.tile, 1) : first, total);
-    c.sched[n & 1] = i;
-    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(ptx::mapa_shared(&c.sched[n & 1], 0)),
+    c.mail[slot] = i;
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(ptx::mapa_shared(&c.mail[slot], 0)),
                  "r"(i)
                  : "memory");
-    ptx::mbar_arrive_cluster(ptx::mapa_shared(&c.sched_full[n & 1], 0));
-    ptx::mbar_arrive_cluster(ptx::mapa_shared(&c.sched_full[n & 1], 1));
+    ptx::mbar_arrive_cluster(ptx::mapa_shared(&c.mail_full[slot], 0));
+    ptx::mbar_arrive_cluster(ptx::mapa_shared(&c.mail_full[slot], 1));
     if (i == total) return;
   }
 }
@@ -886,6 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = p1.E;
+  const uint32_t rank = ptx::cluster_ctarank();
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kBars; ++s) {
       ptx::mbar_init(&ctl.full[s], 1);
@@ -897,7 +934,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(&ctl.sched_full[a], 1);
-      ptx::mbar_init(&ctl.sched_empty[a], kReaders + (C::kAux ? 2 : 0));
+      ptx::mbar_init(&ctl.sched_empty[a], readers(rank, C::kAux));
+      ptx::mbar_init(&ctl.mail_empty[a], 2);  // (the odd CTA's) both producers
       ptx::mbar_init(&ctl.stored[a], 8);  // this CTA's epilogue warps
       ptx::mbar_init(&ctl.counted[a], 1);
       ptx::mbar_init(&ctl.aux_full[a], 1);
@@ -905,6 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&ctl.tmem_full[a], 1);
       ptx::mbar_init(&ctl.tmem_empty[a], 16);  // both CTAs' epilogue warps
     }
+    for (int i = 0; i < 2 * kHalf; ++i) ptx::mbar_init(&ctl.mail_full[i], 1);
     for (int q = 0; q < 4; ++q) ptx::mbar_init(&ctl.paired[q], 2);
     ptx::mbar_init(&ctl.ovl, 8);  // the four warps of each CTA that hold the shared columns
     ptx::mbar_init(&ctl.drain, 1);
@@ -924,7 +963,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::tma_prefetch_desc(t);
   }
   pdl_wait();
-  const uint32_t rank = ptx::cluster_ctarank();
   int first = 0;  // the first tile, claimed while the tables are made
   if (warp == 1 && lane == 0 && rank == 1) first = atomicAdd(p1.tile, 1);
   // offsets outside 0..N would send stores out of the buffers
@@ -979,7 +1017,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true, second = !C::kAux;
       int ring = 0, ring_stages = C::kStages1;
       for (uint32_t n = 0; ok; ++n) {
-        const int i = next_tile(ctl, n, p1.status, false);
+        const int i = take_tile(ctl, n, p1.status);
         ok = i >= 0;
         if (!ok || i >= total) break;
         if (i < total1) {

@@ -51,3 +51,23 @@ def test_an_announced_stage_is_loaded_whole():
                 seen += 1
                 assert "return" not in stage, (os.path.basename(path), stage)
     assert seen >= 2
+
+
+def test_a_claimed_tiles_slot_is_released_by_its_readers():
+    """The slot that a claimed tile is read from is overwritten once its readers have arrived: a
+    relaxed arrival would not order their loads before that, nor one at the scope of a CTA
+    where the writer is in another one."""
+    seen = []
+    for path in SOURCES:
+        text = code(path)
+        for at in re.finditer(r"int (next_tile|take_tile)\([^;{]*\{", text):
+            for a in re.findall(r"(\w*arrive\w*)\(([^;]*);", rest_of_block(text[at.end():])):
+                seen.append((os.path.basename(path), at[1], a[0], re.search(r"c\.(\w+)", a[1])[1]))
+    local, remote = "mbar_arrive", "mbar_arrive_cluster"
+    assert seen == [("grouped_gemm_fp8.cu", "take_tile", remote, "mail_empty"),
+                    ("grouped_gemm_fp8.cu", "take_tile", local, "sched_full"),
+                    ("grouped_gemm_fp8.cu", "next_tile", local, "sched_empty"),
+                    ("rows_fp8.cu", "next_tile", local, "sched_empty")]
+    ptx = code(os.path.join(ROOT, "combine_router_softmax_top_gb300", "csrc", "sm100_ptx.cuh"))
+    assert "mbarrier.arrive.release.cluster.shared::cluster.b64" in ptx
+    assert "mbarrier.arrive.relaxed" not in ptx
