@@ -64,7 +64,7 @@ extern "C" {
 
 size_t moe_fp8_scale_bytes(int64_t rows, int32_t blocks) {
   if (rows < 0 || blocks < 0) return 0;
-  return (size_t)((blocks + 3) / 4) * 4 * (size_t)rows;
+  return ((size_t)blocks + 3) / 4 * 4 * (size_t)rows;
 }
 
 moe_status_t moe_fp8_quantize_weights(const moe_layer_desc_t* d, const moe_bf16* w1,

@@ -198,3 +198,9 @@ def test_buffers_know_the_sizes_that_they_were_made_for(call):
         getattr(moe, call)(d, b, q)
     with pytest.raises(moe.MoeError, match="fp8 is of another layer: T=16 "):
         getattr(moe, call)(d, moe.LayerBuffers(d, "cpu"), q)
+
+
+def test_scale_bytes_of_the_largest_counts(L):
+    most = (1 << 31) - 1
+    assert moe.moe_fp8_scale_bytes(1, most) == 1 << 31
+    assert moe.moe_fp8_scale_bytes(3, most - 3) == 3 * (most - 3)
