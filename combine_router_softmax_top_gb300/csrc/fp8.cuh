@@ -94,9 +94,18 @@ moe_status_t launch_ffn_fwd_fp8(const moe_layer_desc_t& d, const uint8_t* xq, co
                                 cudaStream_t st);
 // The forward for few rows an expert (rows_fp8.cu), which launch_ffn_fwd_fp8 takes
 // up to kFp8FewRows rows an expert on average. Measured, this kernel against the
-// GEMM chain, us: 128 experts (H 2048, F 768) at 4 rows an expert 90 / 114, 16
-// rows 102 / 131, 32 rows 110 / 136, 48 rows 126 / 140, 64 rows 147 / 146; 16
-// experts (H 1024, F 1024) at 32 rows 18 / 22, 64 rows 25 / 24.
+// GEMM chain, us, nothing kept (a and h kept: 1 to 8 us more on both sides):
+//   rows an expert on average            4         16        32        48        64
+//   128 experts, H 2048, F 768     92 / 127  95 / 133 100 / 141 124 / 151 123 / 158
+//     skewed                       88 / 121  97 / 133 104 / 138 122 / 144 147 / 150
+//     all on 8 of the experts       20 / 29   36 / 25   61 / 32   86 / 36  111 / 42
+//   64 experts, H 2048, F 1408     86 / 106  89 / 110  91 / 120 108 / 128 100 / 137
+//   16 experts, H 1024, F 1024      15 / 26   18 / 23   18 / 24   27 / 25   27 / 26
+//   8 experts, H 4096, F 1408       33 / 41   34 / 41   37 / 43   51 / 45   40 / 49
+//   32 experts, H 512, F 512        12 / 22   14 / 22   16 / 22   24 / 23   25 / 23
+// Where the weights come from HBM it is ahead past 48 rows, balanced or skewed; out of
+// L2 the two meet between 32 and 48. What it loses is routing that leaves most experts
+// without rows: the rule sees the average alone, as the offsets are on the device.
 constexpr long long kFp8FewRows = 48;
 moe_status_t launch_ffn_rows_fp8(const moe_layer_desc_t& d, const uint8_t* xq, const uint8_t* xs,
                                  const int32_t* off, const Fp8Weights& w, bf16* a, bf16* h,

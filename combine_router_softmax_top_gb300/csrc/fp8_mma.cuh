@@ -17,8 +17,10 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&b);
 }
 
-// s(x) = 1 / (1 + e^-x) = 1 / (1 + 2^(-x log2 e)): relative error near 1e-6 down
-// to x = -87, where s leaves the normal numbers and is taken as 0. The flushing
+// s(x) = 1 / (1 + e^-x) = 1 / (1 + 2^(-x log2 e)). Rounding log2 e and the product to
+// fp32 makes e^-x off by up to 7.4e-8 |x| of its value, on top of the two instructions'
+// few 2^-23: a relative error of some 5e-7 for |x| < 2 and up to 7e-6 near x = -87, where s leaves the normal numbers and is taken as 0 (rounding s to
+// bf16 is 2^-8). The flushing
 // forms of the two approximate instructions need no scaling around them, which
 // is a third of the instructions of a SwiGLU element.
 __device__ __forceinline__ float sigmoid_f(float x) {

@@ -43,14 +43,15 @@
 // instead of 512.)
 //
 // What bounds it, 128 experts of H 2048, F 768 at 4096 tokens, top 8, balanced: the
-// forward that keeps a and h moves 956 MB in 157 to 167 us (5.7 to 6.1 TB/s, the copy
-// rate being 6.8), the gradient 1007 MB in 177 us. Its second product lands 64 KB of
+// forward that keeps a and h moves 956 MB in 160 to 169 us (5.7 to 6.0 TB/s, the copy
+// rate being 6.8), the gradient 1007 MB in 180 us. Its second product lands 64 KB of
 // operands in a pair for each 256 x 256 x 128 step, at the 9 to 10 TB/s that L2 gives all
-// SMs together. Skewed loads (95 to 4096 rows an expert) cost the gradient 230 to 240
+// SMs together. Skewed loads (95 to 4096 rows an expert) cost the gradient 234 to 248
 // us: half as many 256-row tiles again, their last rows empty, and a first product at
 // the pace of its epilogue (22000 clocks a tile, the K loop 14000). 64 experts of F 1408 at
-// 8192 tokens, nothing kept: 1134 GFLOP in 410 us alone (2.8 PFLOP/s, tensor pipe 73%
-// active), 470 to 490 us again and again, when the power limit lowers the clocks.
+// 8192 tokens, nothing kept: 1134 GFLOP in 410 us for the first launches at 2070 MHz (2.8
+// PFLOP/s, tensor pipe 73% active); after a second of them 1365 W, the power cap active and
+// 1560 MHz, 477 us (484 to 500 from box to box).
 //
 // Ragged groups as in the bf16 GEMMs: expert e owns rows off[e]..off[e+1]-1; a
 // tile's rows past the expert's end are computed on whatever TMA loaded and
@@ -87,7 +88,9 @@ constexpr int kTmemScales = 448;              // buffers of 4 columns for A, 8 f
 constexpr int kSf = 4;                        // scale buffers
 constexpr int kThreads = 512;
 // registers a thread: 128 at launch; the epilogue's two warpgroups take what the
-// control and scale warpgroups give up (2 * 72 + 2 * 184 = 4 * 128)
+// control and scale warpgroups give up (2 * 72 + 2 * 184 = 4 * 128). At 128 the forward
+// chain is compiled with two words spilled (8 bytes stored, 56 loaded), the gradient's
+// with none.
 constexpr int kRegsControl = 72, kRegsEpilogue = 184;
 constexpr int kMaxE = 256;
 
