@@ -70,6 +70,13 @@ class Fp8Bufs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in _FP8_FIELDS]
 
 
+_FP4_FIELDS = ["w1q", "w1s", "w2q", "w2s", "xq", "xs", "hq", "hs"]
+
+
+class Fp4Bufs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in _FP4_FIELDS]
+
+
 class PhaseTime(ctypes.Structure):
     _fields_ = [("mb", ctypes.c_int32), ("phase", ctypes.c_int32), ("stream", ctypes.c_int32),
                 ("start_ms", ctypes.c_float), ("end_ms", ctypes.c_float)]
@@ -126,6 +133,15 @@ _SIGS = {
                               _I32),
     "moe_layer_backward_fp8": ([_DP, ctypes.POINTER(MbBufs), ctypes.POINTER(Fp8Bufs), _I32, _VP],
                                _I32),
+    "moe_fp4_scale_bytes": ([ctypes.c_int64, _I32], _SZ),
+    "moe_fp4_quantize_weights": ([_DP] + [_VP] * 9, _I32),
+    "moe_permute_fp4": ([_DP] + [_VP] * 5, _I32),
+    "moe_expert_ffn_fwd_fp4": ([_DP] + [_VP] * 13 + [_SZ, _VP], _I32),
+    "moe_layer_forward_fp4": ([_DP, ctypes.POINTER(MbBufs), ctypes.POINTER(Fp4Bufs), _I32, _VP],
+                              _I32),
+    "moe_rms_norm": ([_DP] + [_VP] * 3 + [ctypes.c_float] + [_VP] * 6, _I32),
+    "moe_rms_norm_bwd_workspace_size": ([_DP], _SZ),
+    "moe_rms_norm_bwd": ([_DP] + [_VP] * 8 + [_SZ, _VP], _I32),
     "moe_graph_capture": ([_DP, ctypes.POINTER(MbBufs), _I32, _VP, ctypes.POINTER(_VP)], _I32),
     "moe_graph_launch": ([_VP, _VP], _I32),
     "moe_graph_kernel_count": ([_VP], _I32),
@@ -372,10 +388,11 @@ _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _fp8_call(what, desc, spec, tensors, sizes, stream, *tail):
+def _fp8_call(what, desc, spec, tensors, sizes, stream, *tail, at=None, value=None):
     """Checks a call's tensors and makes it: of spec's types, contiguous, on the current
-    device, with at least so many elements, or None where spec allows it. Small calls
-    are bound by this function: no object is built that they do not need."""
+    device, with at least so many elements, or None where spec allows it. `value` is an
+    argument that is no tensor, ahead of tensors[at]. Small calls are bound by this
+    function: no object is built that they do not need."""
     first = tensors[0]
     dev = -1 if first is None else first.get_device()
     if dev < 0 or dev != _get_device():
@@ -390,6 +407,8 @@ def _fp8_call(what, desc, spec, tensors, sizes, stream, *tail):
             p.append(t.data_ptr())
         else:
             _fp8_refuse(what, spec, tensors, sizes)
+    if at is not None:
+        p.insert(at, value)
     st = _raw_stream(dev) if stream is None and _raw_stream is not None else _s(stream)
     status = getattr(_lib or lib(), what)(ctypes.byref(desc), *p, *tail, st)
     if status != MOE_OK:
@@ -477,12 +496,13 @@ def _fp8_fits(what, desc, bufs, fp8):
     """Refuses buffers made for other sizes, for fewer rows than desc's, for another number
     of ranks (the 8-bit buffers have no part in that), or on another device than the
     current one."""
-    for name, of in (("bufs", bufs.desc), ("fp8", fp8.desc)):
+    name8 = "fp8" if isinstance(fp8, Fp8Buffers) else "fp4"
+    for name, of in (("bufs", bufs.desc), (name8, fp8.desc)):
         if ((of.H, of.E, of.F) != (desc.H, desc.E, desc.F) or of.T < desc.T or of.k != desc.k
                 or (of is bufs.desc and of.R != desc.R)):
             raise MoeError(MOE_ERR_INVALID_ARG, what, f"{name} is of another layer: T={of.T} "
                            f"H={of.H} E={of.E} k={of.k} F={of.F} R={of.R}")
-    for name, t in (("bufs", bufs.x), ("fp8", fp8.xq), ("fp8's weights", fp8.w1q)):
+    for name, t in (("bufs", bufs.x), (name8, fp8.xq), (name8 + "'s weights", fp8.w1q)):
         if t.get_device() < 0 or t.get_device() != _get_device():
             raise MoeError(MOE_ERR_INVALID_ARG, what,
                            f"{name}: on {t.device}, not on the current CUDA device")
@@ -504,6 +524,94 @@ def moe_layer_backward_fp8(desc, bufs: "LayerBuffers", fp8: "Fp8Buffers", run_wg
     _check(lib().moe_layer_backward_fp8(_d(desc), ctypes.byref(bufs.struct()),
                                         ctypes.byref(fp8.struct()), int(bool(run_wgrad)),
                                         _s(stream)), "moe_layer_backward_fp8")
+
+
+# ----------------------------------------------------------------------------- 4-bit experts
+def _groups(n: int) -> int:
+    return -(-n // 256)
+
+
+def moe_fp4_scale_bytes(rows: int, blocks: int) -> int:
+    """Bytes of the scale buffer of `rows` rows of `blocks` blocks (include/moe.h)."""
+    return int(lib().moe_fp4_scale_bytes(int(rows), int(blocks)))
+
+
+def _bytes8(rows: int, columns: int) -> int:  # scale bytes of an activation's rows
+    return _groups(columns) * 8 * (rows + (rows & 1))
+
+
+_W4 = " w1q:u8 w1s:u8 w2q:u8 w2s:u8 "
+_SPEC_WEIGHTS4 = _spec("w1:bf16 w2:bf16" + _W4 + "w1v:bf16? w2v:bf16?")
+_SPEC_PERMUTE4 = _spec("x:bf16 slot:i32 xq:u8 xs:u8")
+_SPEC_FWD4 = _spec("xq:u8 xs:u8 off:i32" + _W4 + "a:bf16? h:bf16? hq:u8 hs:u8 o:bf16 ws:u8")
+
+
+def moe_fp4_quantize_weights(desc, w1, w2, w1q, w1s, w2q, w2s, w1v=None, w2v=None, stream=None):
+    """Expert weights into 4-bit codes with one scale for each 32 along K; w1v, w2v (both or
+    neither): the values that the codes stand for, in bf16."""
+    E, H, F = desc.E, desc.H, desc.F
+    n = E * F * H
+    _fp8_call("moe_fp4_quantize_weights", desc, _SPEC_WEIGHTS4,
+              (w1, w2, w1q, w1s, w2q, w2s, w1v, w2v),
+              (2 * n, n, n, 16 * E * F * _groups(H), n // 2, 8 * E * H * _groups(F), 2 * n, n),
+              stream)
+
+
+def moe_permute_fp4(desc, x, slot, xq, xs, stream=None):
+    """Permute that quantises: 4-bit rows with one scale for each 32 columns."""
+    T, H = desc.T, desc.H
+    N = T * desc.k
+    _fp8_call("moe_permute_fp4", desc, _SPEC_PERMUTE4, (x, slot, xq, xs),
+              (T * H, N, N * H // 2, _bytes8(N, H)), stream)
+
+
+def moe_expert_ffn_fwd_fp4(desc, xq, xs, off, w1q, w1s, w2q, w2s, a, h, hq, hs, o, ws,
+                           stream=None):
+    """Expert FFN forward on 4-bit operands; a and h may be None (serving)."""
+    H, E, F, N = desc.H, desc.E, desc.F, desc.T * desc.k
+    n = E * F * H
+    _fp8_call("moe_expert_ffn_fwd_fp4", desc, _SPEC_FWD4,
+              (xq, xs, off, w1q, w1s, w2q, w2s, a, h, hq, hs, o, ws),
+              (N * H // 2, _bytes8(N, H), E + 1, n, 16 * E * F * _groups(H), n // 2,
+               8 * E * H * _groups(F), 2 * N * F, N * F, N * F // 2, _bytes8(N, F), N * H, 1),
+              stream, 0 if ws is None else ws.numel())
+
+
+def moe_layer_forward_fp4(desc, bufs: "LayerBuffers", fp4: "Fp4Buffers", save: bool = False,
+                          stream=None):
+    """Layer forward with 4-bit experts; save=True keeps what moe_layer_backward reads."""
+    _fp8_fits("moe_layer_forward_fp4", desc, bufs, fp4)
+    _check(lib().moe_layer_forward_fp4(_d(desc), ctypes.byref(bufs.struct()),
+                                       ctypes.byref(fp4.struct()), int(bool(save)), _s(stream)),
+           "moe_layer_forward_fp4")
+
+
+# ----------------------------------------------------------------------------- input norm
+_SPEC_NORM = _spec("x:bf16 res:bf16? w:bf16 r:bf16? y:bf16? yq:e4m3? ys:u8? rstd:f32?")
+_SPEC_NORM_BWD = _spec("dy:bf16 dr:bf16? r:bf16 w:bf16 rstd:f32 dx:bf16 dw:f32 ws:u8")
+
+
+def moe_rms_norm(desc, x, res, w, eps, r, y, yq=None, ys=None, rstd=None, stream=None):
+    """Residual addition and root-mean-square norm; y (bf16), yq with ys (e4m3 rows) or both."""
+    T, H = desc.T, desc.H
+    n = T * H
+    _fp8_call("moe_rms_norm", desc, _SPEC_NORM, (x, res, w, r, y, yq, ys, rstd),
+              (n, n, H, n, n, n, _words(T, H), T), stream, at=3, value=eps)
+
+
+def moe_rms_norm_bwd_workspace_size(desc: LayerDesc) -> int:
+    n = lib().moe_rms_norm_bwd_workspace_size(_d(desc))
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_rms_norm_bwd_workspace_size", _err())
+    return n
+
+
+def moe_rms_norm_bwd(desc, dy, dr, r, w, rstd, dx, dw, ws, stream=None):
+    """Gradient of moe_rms_norm: dx of the sum (dr added, unless None), dw of the weights."""
+    T, H = desc.T, desc.H
+    n = T * H
+    _fp8_call("moe_rms_norm_bwd", desc, _SPEC_NORM_BWD, (dy, dr, r, w, rstd, dx, dw, ws),
+              (n, n, n, H, T, n, H, 1), stream, 0 if ws is None else ws.numel())
 
 
 # ----------------------------------------------------------------------------- buffers
@@ -544,6 +652,38 @@ class Fp8Buffers:
     def struct(self) -> Fp8Bufs:
         return Fp8Bufs(*[None if t is None else t.data_ptr()
                          for t in (getattr(self, n) for n in _FP8_FIELDS)])
+
+
+class Fp4Buffers:
+    """The 4-bit buffers of one micro-batch beside its LayerBuffers. weights: another
+    Fp4Buffers whose quantised weights are shared."""
+
+    def __init__(self, desc: LayerDesc, device="cuda", weights: Optional["Fp4Buffers"] = None):
+        H, E, F, N = desc.H, desc.E, desc.F, max(desc.T * desc.k, 1)
+        gh, gf, even = _groups(H), _groups(F), N + (N & 1)
+        z = lambda *s: torch.zeros(*s, dtype=torch.uint8, device=device)  # noqa: E731
+        self.desc = desc.copy()
+        if weights is None:
+            self.w1q, self.w2q = z(E, 2 * F, H // 2), z(E, H, F // 2)
+            self.w1s, self.w2s = z(E, 2, gh, F, 8), z(E, gf, H, 8)
+        else:
+            of = weights.desc
+            if (of.H, of.E, of.F) != (H, E, F):
+                raise MoeError(MOE_ERR_INVALID_ARG, "Fp4Buffers", "weights are of another layer: "
+                               f"H={of.H} E={of.E} F={of.F}")
+            self.w1q, self.w1s, self.w2q, self.w2s = (weights.w1q, weights.w1s, weights.w2q,
+                                                      weights.w2s)
+        self.xq, self.xs = z(N, H // 2), z(gh, even, 8)
+        self.hq, self.hs = z(N, F // 2), z(gf, even, 8)
+
+    def quantize_weights(self, w1, w2, w1v=None, w2v=None, stream=None):
+        """Fills w1q, w1s, w2q, w2s from the bf16 expert weights, and w1v, w2v (which may be
+        w1, w2) with the values that they stand for."""
+        moe_fp4_quantize_weights(self.desc, w1, w2, self.w1q, self.w1s, self.w2q, self.w2s,
+                                 w1v, w2v, stream)
+
+    def struct(self) -> Fp4Bufs:
+        return Fp4Bufs(*[getattr(self, n).data_ptr() for n in _FP4_FIELDS])
 
 
 class LayerBuffers:

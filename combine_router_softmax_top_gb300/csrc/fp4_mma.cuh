@@ -1,0 +1,62 @@
+// Device helpers shared by the 4-bit expert products (grouped_gemm_fp4.cu, rows_fp4.cu).
+#pragma once
+
+#include "fp4.cuh"
+#include "fp8_mma.cuh"
+
+namespace moe {
+namespace fp4 {
+
+// kind::mxf4 instruction descriptor: e2m1 operands (format 1), both K-major, UE8M0
+// scales (bit 23), fp32 D. Bits 4-5 and 29-30 select the byte pair of the scale cells: the
+// two scales of a row's 64 K values.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N) {
+  return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
+         ((uint32_t)(M >> 4) << 24);
+}
+constexpr uint32_t kUpperPair = (2u << 4) | (2u << 29);  // of both operands' cells
+
+__device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X "
+      "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+// The pair's MMA (see grouped_gemm_fp8.cu: A, its scales and D are each CTA's own, B is
+// half in each, B's scales whole in both).
+__device__ __forceinline__ void umma_mxf4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                               uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X "
+      "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+// Contiguous bytes (a multiple of 16, both addresses on 16-byte boundaries) into this CTA's
+// shared memory, counted on its mbarrier.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          ptx::smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
+      : "memory");
+}
+// This warp's 32 lanes x 8 TMEM columns
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&w)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+                   taddr),
+               "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// Rows of an activation's scale buffer for N rows: even
+inline __host__ __device__ long long scale_rows(long long n) { return (n + 1) & ~1ll; }
+
+}  // namespace fp4
+}  // namespace moe

@@ -22,7 +22,9 @@ constexpr int kFp8Block = 128;  // values (or rows and columns) that share a sca
 
 enum Fp8KernelId {  // kernel ids past those of the bf16 layer
   K_FP8_QUANT_W = K_NUM, K_FP8_PERMUTE, K_FP8_COMBINE_BWD, K_FP8_FFN_FWD, K_FP8_FFN_DGRAD,
-  K_FP8_ZERO, K_FP8_ROWS_FFN, K_ALL
+  K_FP8_ZERO, K_FP8_ROWS_FFN,
+  // the input norm and the 4-bit experts (norm.cu, fp4.cuh)
+  K_NORM, K_NORM_BWD, K_NORM_DW, K_FP4_QUANT_W, K_FP4_PERMUTE, K_FP4_FFN_FWD, K_FP4_ROWS_FFN, K_ALL
 };
 
 // ---------------------------------------------------------------- block scales

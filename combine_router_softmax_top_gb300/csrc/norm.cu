@@ -1,0 +1,380 @@
+// The norm in front of the layer: the residual's addition and root-mean-square
+// norm, its rows in bf16 and, when asked for, as e4m3 with block scales; and its
+// gradient. Everything is bound by HBM, or by latency for a few rows.
+//
+//   r = bf16(x + res),  rstd = (mean(r^2) + eps)^-1/2,  y = bf16(r rstd w)
+//   xh = r rstd,  g = dy w
+//   dx = bf16(rstd (g - xh mean(g xh)) + dr),  dw = sum over rows of dy xh
+//
+// A row lives in the registers of its threads between the pass that sums the
+// squares and the one that scales, so it is read once. Sums are fp32: a thread's
+// columns in order, then the threads in a fixed tree, so results do not change
+// from call to call.
+#include <algorithm>
+#include <math.h>
+
+#include "api_checks.cuh"
+#include "fp8.cuh"
+#include "moe_layer_ops.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxThreads = 1024;
+
+// Threads of a row: a power of two, each with up to `vecs` groups of 8 columns, and at
+// least the 16 that hold a block of 128.
+int row_threads(int H, int vecs) {
+  int tpr = H > 64 ? 16 : 8;
+  while (tpr * vecs * 8 < H) tpr <<= 1;
+  return tpr;
+}
+
+// Sum over the threads of a row; s_part: a word for each warp of the block. Rows of
+// more than a warp meet at a barrier of the whole block (all its rows do); two
+// calls in a row need different s_part.
+__device__ __forceinline__ float row_sum(float v, int tpr, float* s_part) {
+  const int width = tpr < 32 ? tpr : 32;
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+    if (o < width) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (tpr <= 32) return v;
+  if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int first = threadIdx.x / tpr * (tpr / 32);
+  v = s_part[first];
+  for (int w = 1; w < tpr / 32; ++w) v += s_part[first + w];
+  return v;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+struct NormParams {
+  const bf16 *x, *res, *w;
+  float eps;
+  bf16 *r, *y;
+  uint8_t* yq;
+  uint32_t* ys;
+  float* rstd;
+  int T, H, tpr;
+};
+
+template <int V>
+__global__ void __launch_bounds__(V == 2 ? kMaxThreads : kThreads) rms_norm_kernel(const NormParams p) {
+  extern __shared__ uint32_t s_words[];  // scale words of the block's rows
+  __shared__ float s_part[2][kMaxThreads / 32];
+  const int rows = blockDim.x / p.tpr, lr = threadIdx.x / p.tpr, sub = threadIdx.x % p.tpr;
+  const int cpr = p.H / 8, nw = (p.H + 511) / 512;
+  if (p.yq)  // bytes past a row's blocks stay 0
+    for (int i = threadIdx.x; i < rows * nw; i += blockDim.x) s_words[i] = 0;
+  pdl_wait();
+  if (p.yq) __syncthreads();
+  const int groups = (p.T + rows - 1) / rows;
+  int buf = 0;
+  for (int grp = blockIdx.x; grp < groups; grp += gridDim.x, buf ^= 1) {
+    const int t = grp * rows + lr;
+    const size_t at = (size_t)t * p.H;
+    uint4 v[V], q[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = sub + i * p.tpr;
+      const bool ok = t < p.T && c < cpr;
+      v[i] = ok ? reinterpret_cast<const uint4*>(p.x + at)[c] : make_uint4(0, 0, 0, 0);
+      if (p.res)
+        q[i] = ok ? reinterpret_cast<const uint4*>(p.res + at)[c] : make_uint4(0, 0, 0, 0);
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      uint32_t* a = reinterpret_cast<uint32_t*>(&v[i]);
+      if (p.res) {
+        const uint32_t* b = reinterpret_cast<const uint32_t*>(&q[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          a[j] = pack2(bf16_lo(a[j]) + bf16_lo(b[j]), bf16_hi(a[j]) + bf16_hi(b[j]));
+        const int c = sub + i * p.tpr;
+        if (p.r && t < p.T && c < cpr) reinterpret_cast<uint4*>(p.r + at)[c] = v[i];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        ss = fmaf(bf16_lo(a[j]), bf16_lo(a[j]), ss);
+        ss = fmaf(bf16_hi(a[j]), bf16_hi(a[j]), ss);
+      }
+    }
+    ss = row_sum(ss, p.tpr, s_part[buf]);
+    const float rs = 1.f / sqrtf(ss / (float)p.H + p.eps);
+    if (p.rstd && sub == 0 && t < p.T) p.rstd[t] = rs;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = sub + i * p.tpr;
+      const bool ok = t < p.T && c < cpr;
+      const uint4 wv = c < cpr ? __ldg(reinterpret_cast<const uint4*>(p.w) + c) : make_uint4(0, 0, 0, 0);
+      const uint32_t* wp = reinterpret_cast<const uint32_t*>(&wv);
+      uint32_t* a = reinterpret_cast<uint32_t*>(&v[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        a[j] = pack2(bf16_lo(a[j]) * rs * bf16_lo(wp[j]), bf16_hi(a[j]) * rs * bf16_hi(wp[j]));
+      if (ok && p.y) reinterpret_cast<uint4*>(p.y + at)[c] = v[i];
+      if (!p.yq) continue;
+      // a block is 16 threads' columns (8 threads' in a row of 64)
+      uint32_t m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(0, a[0]), a[1]), a[2]), a[3]);
+      m = c < cpr ? absmax_bits(m) : 0;
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1)
+        if (o < p.tpr) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const uint32_t b = fp8_scale_byte(m), inv = fp8_inv_scale2(b);
+      if (ok)
+        reinterpret_cast<uint2*>(p.yq + at)[c] =
+            make_uint2(fp8x4_of_bf16(a[0], a[1], inv), fp8x4_of_bf16(a[2], a[3], inv));
+      if ((c & 15) == 0 && c < cpr)
+        reinterpret_cast<uint8_t*>(s_words)[lr * 4 * nw + (c >> 4)] = (uint8_t)b;
+    }
+    if (p.yq) {  // whole words: their bytes come from several threads
+      if (p.tpr <= 32) __syncwarp();
+      else __syncthreads();
+      for (int i = sub; i < nw; i += p.tpr)
+        if (t < p.T) p.ys[(size_t)i * p.T + t] = s_words[lr * nw + i];
+      if (p.tpr <= 32) __syncwarp();
+      else __syncthreads();
+    }
+  }
+}
+
+struct NormBwdParams {
+  const bf16 *dy, *dr, *r, *w;
+  const float* rstd;
+  bf16* dx;
+  float* part;  // [blocks][H]
+  int T, H, tpr;
+};
+
+template <int V>
+__global__ void __launch_bounds__(V == 2 ? kMaxThreads : kThreads) rms_norm_bwd_kernel(const NormBwdParams p) {
+  extern __shared__ float s_dw[];  // [H]
+  __shared__ float s_part[2][kMaxThreads / 32];
+  const int rows = blockDim.x / p.tpr, lr = threadIdx.x / p.tpr, sub = threadIdx.x % p.tpr;
+  const int cpr = p.H / 8;
+  const float inv_h = 1.f / (float)p.H;
+  pdl_wait();
+  const int groups = (p.T + rows - 1) / rows;
+  float dw[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+  int buf = 0;
+  for (int grp = blockIdx.x; grp < groups; grp += gridDim.x, buf ^= 1) {
+    const int t = grp * rows + lr;
+    const size_t at = (size_t)t * p.H;
+    uint4 rv[V], gv[V], dv[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = sub + i * p.tpr;
+      const bool ok = t < p.T && c < cpr;
+      rv[i] = ok ? reinterpret_cast<const uint4*>(p.r + at)[c] : make_uint4(0, 0, 0, 0);
+      gv[i] = ok ? reinterpret_cast<const uint4*>(p.dy + at)[c] : make_uint4(0, 0, 0, 0);
+      if (p.dr) dv[i] = ok ? reinterpret_cast<const uint4*>(p.dr + at)[c] : make_uint4(0, 0, 0, 0);
+    }
+    const float rs = t < p.T ? p.rstd[t] : 0.f;
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = sub + i * p.tpr;
+      const uint4 wv = c < cpr ? __ldg(reinterpret_cast<const uint4*>(p.w) + c) : make_uint4(0, 0, 0, 0);
+      const uint32_t* wp = reinterpret_cast<const uint32_t*>(&wv);
+      const uint32_t *a = reinterpret_cast<const uint32_t*>(&rv[i]), *g = reinterpret_cast<const uint32_t*>(&gv[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p0 = bf16_lo(g[j]) * (bf16_lo(a[j]) * rs), p1 = bf16_hi(g[j]) * (bf16_hi(a[j]) * rs);
+        dw[i][2 * j] += p0;
+        dw[i][2 * j + 1] += p1;
+        dot = fmaf(p0, bf16_lo(wp[j]), dot);
+        dot = fmaf(p1, bf16_hi(wp[j]), dot);
+      }
+    }
+    const float mean = row_sum(dot, p.tpr, s_part[buf]) * inv_h;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = sub + i * p.tpr;
+      if (t >= p.T || c >= cpr) continue;
+      const uint4 wv = __ldg(reinterpret_cast<const uint4*>(p.w) + c);
+      const uint32_t* wp = reinterpret_cast<const uint32_t*>(&wv);
+      const uint32_t *a = reinterpret_cast<const uint32_t*>(&rv[i]), *g = reinterpret_cast<const uint32_t*>(&gv[i]);
+      const uint32_t* d = reinterpret_cast<const uint32_t*>(&dv[i]);
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float d0 = rs * fmaf(-bf16_lo(a[j]) * rs, mean, bf16_lo(g[j]) * bf16_lo(wp[j]));
+        float d1 = rs * fmaf(-bf16_hi(a[j]) * rs, mean, bf16_hi(g[j]) * bf16_hi(wp[j]));
+        if (p.dr) {
+          d0 += bf16_lo(d[j]);
+          d1 += bf16_hi(d[j]);
+        }
+        o[j] = pack2(d0, d1);
+      }
+      reinterpret_cast<uint4*>(p.dx + at)[c] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+  // the block's rows, one after another, into one row of partial sums
+  for (int k = 0; k < rows; ++k) {
+    if (lr == k) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = sub + i * p.tpr;
+        if (c >= cpr) continue;
+        float4* s = reinterpret_cast<float4*>(s_dw) + 2 * c;
+        float4 lo = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+        float4 hi = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+        if (k > 0) {
+          const float4 a = s[0], b = s[1];
+          lo = make_float4(a.x + lo.x, a.y + lo.y, a.z + lo.z, a.w + lo.w);
+          hi = make_float4(b.x + hi.x, b.y + hi.y, b.z + hi.z, b.w + hi.w);
+        }
+        if (k == rows - 1) {
+          float4* o = reinterpret_cast<float4*>(p.part + (size_t)blockIdx.x * p.H) + 2 * c;
+          o[0] = lo;
+          o[1] = hi;
+        } else {
+          s[0] = lo;
+          s[1] = hi;
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// dw[h] = sum over the partial rows, in a fixed order: 16 columns a block, 16 threads
+// of four columns... each of 64 groups takes every 64th row, then a tree.
+constexpr int kDwCols = 16, kDwGroups = 64;
+__global__ void __launch_bounds__(kDwCols / 4 * kDwGroups)
+    rms_norm_dw_kernel(const float* __restrict__ part, float* __restrict__ dw, int parts, int H) {
+  __shared__ float4 s[kDwGroups][kDwCols / 4];
+  const int c = threadIdx.x % (kDwCols / 4), g = threadIdx.x / (kDwCols / 4);
+  pdl_wait();
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = g; i < parts; i += kDwGroups) {
+    const float4 v = reinterpret_cast<const float4*>(part + (size_t)i * H + blockIdx.x * kDwCols)[c];
+    a = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w);
+  }
+  s[g][c] = a;
+#pragma unroll
+  for (int o = kDwGroups / 2; o; o >>= 1) {
+    __syncthreads();
+    if (g < o) {
+      const float4 v = s[g + o][c];
+      a = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w);
+      s[g][c] = a;
+    }
+  }
+  if (g == 0) reinterpret_cast<float4*>(dw + blockIdx.x * kDwCols)[c] = a;
+}
+
+constexpr int kMaxParts = 608;  // rows of partial sums, and blocks of the gradient
+
+moe_status_t launched(cudaError_t e, const char* what) {
+  if (e != cudaSuccess) {
+    set_error("%s launch: %s", what, cudaGetErrorString(e));
+    return MOE_ERR_CUDA;
+  }
+  return check_launch(what);
+}
+
+}  // namespace
+
+moe_status_t launch_rms_norm(const moe_layer_desc_t& d, const bf16* x, const bf16* res, const bf16* w,
+                             float eps, bf16* r, bf16* y, uint8_t* yq, uint8_t* ys, float* rstd,
+                             cudaStream_t st) {
+  if (d.T == 0) return MOE_OK;
+  const bool few = d.T <= device_sm_count() * 4;
+  const int vecs = few ? 2 : 8;
+  NormParams p = {x, res, w, eps, r, y, yq, reinterpret_cast<uint32_t*>(ys), rstd, d.T, d.H,
+                  row_threads(d.H, vecs)};
+  const int threads = std::max(p.tpr, few ? 32 : kThreads);
+  const int rows = threads / p.tpr;
+  const int grid = std::min(ceil_div(d.T, rows), device_sm_count() * 8);
+  const size_t smem = yq ? (size_t)rows * ceil_div(d.H, 512) * 4 : 0;
+  cudaError_t e;
+  {
+    LaunchScope _ls(K_NORM, st);
+    e = vecs == 2 ? launch_k(rms_norm_kernel<2>, grid, threads, smem, st, p)
+                  : launch_k(rms_norm_kernel<8>, grid, threads, smem, st, p);
+  }
+  return launched(e, "rms_norm_kernel");
+}
+
+size_t rms_norm_bwd_ws_bytes(const moe_layer_desc_t& d) {
+  return (size_t)std::min(std::max(d.T, 1), kMaxParts) * d.H * sizeof(float);
+}
+
+moe_status_t launch_rms_norm_bwd(const moe_layer_desc_t& d, const bf16* dy, const bf16* dr, const bf16* r,
+                                 const bf16* w, const float* rstd, bf16* dx, float* dw, float* part,
+                                 cudaStream_t st) {
+  int grid = 0;
+  cudaError_t e = cudaSuccess;
+  if (d.T > 0) {
+    const int vecs = d.H > 8192 ? 2 : 4;
+    NormBwdParams p = {dy, dr, r, w, rstd, dx, part, d.T, d.H, row_threads(d.H, vecs)};
+    const int threads = std::max(p.tpr, kThreads), rows = threads / p.tpr;
+    grid = std::min({ceil_div(d.T, rows), device_sm_count() * 2, kMaxParts});
+    const size_t smem = rows > 1 ? (size_t)d.H * sizeof(float) : 0;
+    LaunchScope _ls(K_NORM_BWD, st);
+    e = vecs == 2 ? launch_k(rms_norm_bwd_kernel<2>, grid, threads, smem, st, p)
+                  : launch_k(rms_norm_bwd_kernel<4>, grid, threads, smem, st, p);
+  }
+  if (e == cudaSuccess) {
+    LaunchScope _ls(K_NORM_DW, st);
+    e = launch_k(rms_norm_dw_kernel, d.H / kDwCols, kDwCols / 4 * kDwGroups, 0, st,
+                 (const float*)part, dw, grid, d.H);
+  }
+  return launched(e, "rms_norm_bwd_kernel");
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+#define S(st) static_cast<cudaStream_t>(st)
+#define BF(p) reinterpret_cast<const bf16*>(p)
+#define BFW(p) reinterpret_cast<bf16*>(p)
+
+extern "C" {
+
+moe_status_t moe_rms_norm(const moe_layer_desc_t* d, const moe_bf16* x, const moe_bf16* res,
+                          const moe_bf16* w, float eps, moe_bf16* r, moe_bf16* y, moe_e4m3* yq,
+                          moe_e8m0* ys, float* rstd, void* stream) {
+  MOE_CHECK(validate(d));
+  MOE_PTR(x); MOE_PTR_OPT(res); MOE_PTR(w); MOE_PTR_OPT(r); MOE_PTR_OPT(y); MOE_PTR_OPT(yq);
+  MOE_PTR_OPT(ys); MOE_PTR_OPT(rstd);
+  if (!(eps >= 0.f) || isinf(eps)) { set_error("eps must be finite and not negative"); return MOE_ERR_INVALID_ARG; }
+  if (r && !res) { set_error("r is the sum with res, which is NULL"); return MOE_ERR_INVALID_ARG; }
+  if (!y && !yq) { set_error("y and yq are both NULL"); return MOE_ERR_INVALID_ARG; }
+  if (!yq != !ys) { set_error("yq and ys are given together or not at all"); return MOE_ERR_INVALID_ARG; }
+  return launch_rms_norm(*d, BF(x), BF(res), BF(w), eps, BFW(r), BFW(y), yq, ys, rstd, S(stream));
+}
+
+size_t moe_rms_norm_bwd_workspace_size(const moe_layer_desc_t* d) {
+  return validate(d) == MOE_OK ? rms_norm_bwd_ws_bytes(*d) : 0;
+}
+
+moe_status_t moe_rms_norm_bwd(const moe_layer_desc_t* d, const moe_bf16* dy, const moe_bf16* dr,
+                              const moe_bf16* r, const moe_bf16* w, const float* rstd, moe_bf16* dx,
+                              float* dw, void* ws, size_t ws_bytes, void* stream) {
+  MOE_CHECK(validate(d));
+  MOE_PTR(dy); MOE_PTR_OPT(dr); MOE_PTR(r); MOE_PTR(w); MOE_PTR(rstd); MOE_PTR(dx); MOE_PTR(dw);
+  MOE_PTR(ws);
+  if (ws_bytes < rms_norm_bwd_ws_bytes(*d)) {
+    set_error("workspace of %zu bytes is smaller than moe_rms_norm_bwd_workspace_size() = %zu",
+              ws_bytes, rms_norm_bwd_ws_bytes(*d));
+    return MOE_ERR_INVALID_ARG;
+  }
+  return launch_rms_norm_bwd(*d, BF(dy), BF(dr), BF(r), BF(w), rstd, BFW(dx), dw,
+                             static_cast<float*>(ws), S(stream));
+}
+
+}  // extern "C"

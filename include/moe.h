@@ -52,6 +52,7 @@ extern "C" {
 
 typedef uint16_t moe_bf16; /* bfloat16 bit pattern */
 typedef uint8_t moe_e4m3;  /* 8-bit float: 4 exponent bits, 3 mantissa bits, no infinity */
+typedef uint8_t moe_e2m1x2; /* two 4-bit floats (2 exponent bits, 1 mantissa bit), first in the low bits */
 typedef uint8_t moe_e8m0;  /* power-of-two block scale: byte b stands for 2^(b - 127), 255 for NaN */
 
 typedef enum {
@@ -533,6 +534,117 @@ moe_status_t moe_layer_forward_fp8(const moe_layer_desc_t* d, const moe_mb_bufs_
  * may be NULL. Gradients pass through the roundings to 8 bits unchanged. */
 moe_status_t moe_layer_backward_fp8(const moe_layer_desc_t* d, const moe_mb_bufs_t* b,
                                     const moe_fp8_bufs_t* q, int32_t run_wgrad, void* stream);
+
+/* ------------------------------------------------------------------ 4-bit experts */
+
+/* The experts' forward on microscaled 4-bit floating point: weights of 4.25 bits a value,
+ * for serving, where the weights' bytes are the time of a batch of single tokens and
+ * the tensor cores' rate that of a prompt. The pages describe no such path; the
+ * arithmetic is stated here.
+ *
+ * 32 consecutive values along the products' K (columns of a row) share a scale byte b.
+ * A value v is held as q = e2m1(v / 2^(b-127)): 0, 0.5, 1, 1.5, 2, 3, 4, 6 or their
+ * negatives, rounded to nearest, ties to the even code; b is the smallest byte with
+ * max|v| <= 6 * 2^(b-127), so nothing is clamped. A block of zeros has b = 0. A block
+ * that holds a NaN or an infinity has b = 255 and unspecified codes: it comes out of the
+ * products as NaN, in its own rows (activations) or output columns (weights).
+ *
+ * Codes of a [R, C] matrix are [R, C/2] bytes, the lower column of a byte in its low four
+ * bits. Its scale bytes are [ceil(C / 256)][R][8]: block b of row r at
+ * ((b / 8) * R + r) * 8 + b % 8. Activations of N rows have R = N rounded up to even
+ * (moe_fp4_scale_bytes() gives the size); weights one such matrix for each expert's gate
+ * rows, up rows and w2: w1s [E, 2, ceil(H / 256), F, 8], w2s [E, ceil(F / 256), H, 8]. Bytes
+ * past a row's blocks are 0 in the weights' and xs, unspecified in hs.
+ * Products are accumulated in fp32; the scales are applied exactly. hq, a, h and o of these
+ * calls are 32-byte aligned.
+ *
+ * There is no 4-bit gradient: a block's scale belongs to K of the forward, and the
+ * gradient's K runs across it. A layer is trained through its 4-bit forward by
+ * moe_layer_forward_fp4 with save != 0 and moe_layer_backward with b->w1, b->w2 = the values
+ * of the 4-bit weights (w1v, w2v below): gradients pass through the roundings unchanged. */
+
+/* Bytes of the scale buffer of `rows` rows of `blocks` blocks (0 if negative). */
+size_t moe_fp4_scale_bytes(int64_t rows, int32_t blocks);
+
+/* Expert weights into 4-bit codes and scales, once per change of the weights: w1 [E,2F,H],
+ * w2 [E,H,F] bf16 -> w1q [E,2F,H/2], w1s, w2q [E,H,F/2], w2s, and, unless both are NULL,
+ * the values that these stand for, in bf16 (exact; 2^128, to which the largest bf16 values
+ * round, is an infinity there): w1v [E,2F,H], w2v [E,H,F] (which may be w1 and w2
+ * themselves). */
+moe_status_t moe_fp4_quantize_weights(const moe_layer_desc_t* d, const moe_bf16* w1,
+                                      const moe_bf16* w2, moe_e2m1x2* w1q, moe_e8m0* w1s,
+                                      moe_e2m1x2* w2q, moe_e8m0* w2s, moe_bf16* w1v,
+                                      moe_bf16* w2v, void* stream);
+
+/* Permute into the 4-bit send buffer: row slot[t,j] of (xq, xs) = quantised x[t,:], for
+ * every j. Slots outside 0..N-1 are skipped, rows that no slot names are left as they were.
+ * x [T,H] bf16, slot [T,k] int32 (of the dispatch layout) -> xq [N,H/2], xs. */
+moe_status_t moe_permute_fp4(const moe_layer_desc_t* d, const moe_bf16* x, const int32_t* slot,
+                             moe_e2m1x2* xq, moe_e8m0* xs, void* stream);
+
+/* Expert FFN forward on 4-bit operands, per expert e on its rows:
+ *   A  = xq_e @ w1q[e]^T with scales                 (fp32, not rounded)
+ *   h  = silu(A[:, :F]) * A[:, F:]                   (fp32)
+ *   hq, hs = quantised h
+ *   o  = bf16(hq_e @ w2q[e]^T with scales)           [rows, H]
+ *   a  = bf16(A) [rows, 2F] and h = bf16(h) [rows, F], each unless NULL, for a backward.
+ * The results do not depend on which of a and h are kept. off [E+1] int32 on the device;
+ * values outside 0..N are taken as the nearest bound; rows at or past off[E] are left as
+ * they were. hq [N,F/2] and hs are scratch that holds quantised h afterwards. */
+moe_status_t moe_expert_ffn_fwd_fp4(const moe_layer_desc_t* d, const moe_e2m1x2* xq,
+                                    const moe_e8m0* xs, const int32_t* off, const moe_e2m1x2* w1q,
+                                    const moe_e8m0* w1s, const moe_e2m1x2* w2q,
+                                    const moe_e8m0* w2s, moe_bf16* a, moe_bf16* h, moe_e2m1x2* hq,
+                                    moe_e8m0* hs, moe_bf16* o, void* ws, size_t ws_bytes,
+                                    void* stream);
+
+/* The 4-bit buffers of one micro-batch beside its moe_mb_bufs_t (device pointers,
+ * caller-owned; the weights may be shared). */
+typedef struct moe_fp4_bufs {
+  const moe_e2m1x2* w1q; const moe_e8m0* w1s; const moe_e2m1x2* w2q; const moe_e8m0* w2s;
+  moe_e2m1x2* xq; moe_e8m0* xs; moe_e2m1x2* hq; moe_e8m0* hs;
+} moe_fp4_bufs_t;
+
+/* Layer forward with 4-bit experts: route, dispatch layout, 4-bit permute, expert FFN,
+ * combine. save != 0 also stores what moe_layer_backward reads (b->x_perm, b->a, b->h);
+ * with save = 0 (serving) those three may be NULL. b->w1, b->w2 and the gradient buffers
+ * are not used. */
+moe_status_t moe_layer_forward_fp4(const moe_layer_desc_t* d, const moe_mb_bufs_t* b,
+                                   const moe_fp4_bufs_t* q, int32_t save, void* stream);
+
+/* ------------------------------------------------------------------ the layer's input norm */
+
+/* Root-mean-square norm of the residual stream, ahead of the layer (the pages begin behind
+ * it; the arithmetic is stated here). Per token t, of d only T and H are used:
+ *   r = bf16(x + res)   (r = x without res)
+ *   rstd = (sum_h r[h]^2 / H + eps)^-1/2                      (fp32)
+ *   y[h] = bf16(r[h] * rstd * w[h])
+ *   yq, ys = y in e4m3, one scale for each 128 columns        (see "8-bit experts")
+ * x [T,H], w [H] bf16; res [T,H] bf16 or NULL; r [T,H] bf16 or NULL (the new residual
+ * stream; only with res; may be x or res themselves); y [T,H] bf16 or NULL; yq [T,H], ys
+ * [ceil(nb / 4), T, 4] with nb = ceil(H / 128), both or neither, exactly what
+ * moe_permute_fp8 makes of y: the rows of an expert that every token visits
+ * (moe_expert_ffn_fwd_fp8 with E = 1, k = 1, off = {0, T}); y or yq must be given; rstd [T]
+ * fp32 or NULL. y, yq, ys and rstd overlap nothing. eps >= 0 and finite. A NaN makes
+ * its whole row NaN; a row with an infinity is NaN there and 0 elsewhere. */
+moe_status_t moe_rms_norm(const moe_layer_desc_t* d, const moe_bf16* x, const moe_bf16* res,
+                          const moe_bf16* w, float eps, moe_bf16* r, moe_bf16* y, moe_e4m3* yq,
+                          moe_e8m0* ys, float* rstd, void* stream);
+
+/* Bytes of workspace that moe_rms_norm_bwd needs (0 on an invalid descriptor). Its contents
+ * need no set-up; calls that can overlap on the GPU need workspaces of their own. */
+size_t moe_rms_norm_bwd_workspace_size(const moe_layer_desc_t* d);
+
+/* Gradient of moe_rms_norm, with xh = r rstd, g = dy w (fp32):
+ *   dx[t,:] = bf16(rstd[t] * (g - xh * (sum_h g xh / H)) + dr[t,:])
+ *   dw[h]   = sum_t dy[t,h] xh[t,h]                           (fp32, overwritten)
+ * dy [T,H] bf16 (of y), dr [T,H] bf16 (of r, what else reads the residual stream) or NULL,
+ * r [T,H] (x without a residual), w [H], rstd [T] as the forward had them -> dx [T,H]
+ * bf16, the gradient of both x and res (may be dy or dr themselves), dw [H] fp32. Sums
+ * run in a fixed order: the same call gives the same bits. */
+moe_status_t moe_rms_norm_bwd(const moe_layer_desc_t* d, const moe_bf16* dy, const moe_bf16* dr,
+                              const moe_bf16* r, const moe_bf16* w, const float* rstd, moe_bf16* dx,
+                              float* dw, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------ CUDA graphs */
 
