@@ -14,14 +14,17 @@ __device__ __forceinline__ uint32_t max8(uint32_t m, const uint4& v) {
   m = absmax_bf16x2(m, v.z);
   return absmax_bf16x2(m, v.w);
 }
-// eight bf16 over their scale -> eight codes
-__device__ __forceinline__ uint32_t codes(const uint4& v, float inv) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// eight bf16 times 1 / scale (two packed bf16) -> eight codes. The bf16 products are exact: a
+// power of two moves exponents alone, and what falls below bf16's normal range is far
+// below e2m1's smallest step.
+__device__ __forceinline__ uint32_t codes(const uint4& v, uint32_t inv2) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
   float f[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    f[2 * j] = bf16_lo(w[j]) * inv;
-    f[2 * j + 1] = bf16_hi(w[j]) * inv;
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(w[j]) : "r"(inv2));
+    f[2 * j] = bf16_lo(w[j]);
+    f[2 * j + 1] = bf16_hi(w[j]);
   }
   return fp4x8(f);
 }
@@ -40,23 +43,26 @@ struct Fp4Mat {
 };
 constexpr int kRows = 8;
 
-// The values of eight codes as bf16, exact: two significant bits, and the smallest one is
-// 2^-128, on bf16's grid of 2^-133 there.
-__device__ __forceinline__ uint4 values(uint32_t c, float scale) {
+// The values of the eight codes c of v's elements as bf16, exact: two significant bits, and
+// the smallest one is 2^-128, on bf16's grid of 2^-133 there. Byte tables give the two
+// halves of each magnitude's bf16 pattern, four codes at a time; the signs are the elements'.
+// (Twelve instructions for four values; with the arithmetic spelled out the kernel was bound
+// by issuing it: 527 us for the 128-expert layer's weights.)
+__device__ __forceinline__ uint4 values(const uint4& v, uint32_t c, uint32_t scale2) {
+  const uint32_t x[4] = {v.x, v.y, v.z, v.w};
   uint32_t w[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float f[2];
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t sel = (c >> (16 * j)) & 0x7777u;
+    const uint32_t lo = __byte_perm(0xC0800000u, 0xC0804000u, sel);  // 0 .5 1 1.5 | 2 3 4 6
+    const uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, sel);
+    w[2 * j] = __byte_perm(lo, hi, 0x5140u);
+    w[2 * j + 1] = __byte_perm(lo, hi, 0x7362u);
+  }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t n = (c >> (8 * j + 4 * i)) & 15u, e = (n >> 1) & 3u, m = n & 1u;
-      // 2 |value| is 0, 1 (subnormals), then (2 + m) 2^(e - 1): 2, 3, 4, 6, 8, 12
-      const int twice = e ? (int)(2 + m) << (e - 1) : (int)m;
-      const float a = 0.5f * (float)twice * scale;
-      f[i] = n & 8u ? -a : a;
-    }
-    const __nv_bfloat162 p = __floats2bfloat162_rn(f[0], f[1]);
-    w[j] = *reinterpret_cast<const uint32_t*>(&p);
+  for (int j = 0; j < 4; ++j) {
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(w[j]) : "r"(scale2));
+    w[j] |= x[j] & 0x80008000u;
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -89,13 +95,13 @@ __global__ void __launch_bounds__(256) quantize_weights_fp4_kernel(const Fp4Mat 
     const uint32_t b = fp4_scale_byte(mx);
     if ((lane & 3) == (i & 3)) mine[i >> 2] = b;
     if (!ok) continue;
-    const uint32_t c = codes(v[i], fp4_inv_scale(b));
+    const uint32_t c = codes(v[i], fp8_inv_scale2(b));
     const size_t e = at + (size_t)i * m.C;
     *reinterpret_cast<uint32_t*>(m.q + e / 2) = c;
     if (m.v) {
       // b = 255: NaN; byte 0 is 2^-127, a subnormal
-      const float scale = __uint_as_float(b == 255u ? 0x7FFFFFFFu : b ? b << 23 : 0x00400000u);
-      __stcs(reinterpret_cast<uint4*>(m.v + e), values(c, scale));
+      const uint32_t scale2 = b == 255u ? 0x7FFF7FFFu : b ? b * 0x00800080u : 0x00400040u;
+      __stcs(reinterpret_cast<uint4*>(m.v + e), values(v[i], c, scale2));
     }
   }
   uint8_t* s = m.s + (((size_t)mat * m.groups + g) * m.R + r0 + (lane & 3)) * 8 + (lane >> 2);
@@ -132,7 +138,7 @@ __global__ void __launch_bounds__(256) permute_fp4_kernel(const bf16* __restrict
     uint32_t m = absmax_bits(max8(max8(0, a), c));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     const uint32_t b = fp4_scale_byte(m);
-    const float inv = fp4_inv_scale(b);
+    const uint32_t inv = fp8_inv_scale2(b);
     const uint2 q = make_uint2(codes(a, inv), codes(c, inv));
     // the eight bytes of 256 columns, in every lane of their sixteen
     uint32_t word = b << (8 * ((lane >> 1) & 3));
