@@ -21,8 +21,8 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxThreads = 1024;
+constexpr int kThreads = 256;       // of a block at most, one row being one block's at the most
+constexpr int kMaxThreads = 1024;   // (rows of a latency-bound call are spread wider)
 
 // Threads of a row: a power of two, each with up to `vecs` groups of 8 columns, and at
 // least the 16 that hold a block of 128.
@@ -67,81 +67,84 @@ struct NormParams {
 template <int V>
 __global__ void __launch_bounds__(V == 2 ? kMaxThreads : kThreads) rms_norm_kernel(const NormParams p) {
   extern __shared__ uint32_t s_words[];  // scale words of the block's rows
-  __shared__ float s_part[2][kMaxThreads / 32];
+  __shared__ float s_part[kMaxThreads / 32];
   const int rows = blockDim.x / p.tpr, lr = threadIdx.x / p.tpr, sub = threadIdx.x % p.tpr;
   const int cpr = p.H / 8, nw = (p.H + 511) / 512;
   if (p.yq)  // bytes past a row's blocks stay 0
     for (int i = threadIdx.x; i < rows * nw; i += blockDim.x) s_words[i] = 0;
   pdl_wait();
   if (p.yq) __syncthreads();
-  const int groups = (p.T + rows - 1) / rows;
-  int buf = 0;
-  for (int grp = blockIdx.x; grp < groups; grp += gridDim.x, buf ^= 1) {
-    const int t = grp * rows + lr;
-    const size_t at = (size_t)t * p.H;
-    uint4 v[V], q[V];
+  const int t = blockIdx.x * rows + lr;
+  const size_t at = (size_t)t * p.H;
+  uint4 v[V], q[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = sub + i * p.tpr;
-      const bool ok = t < p.T && c < cpr;
-      v[i] = ok ? reinterpret_cast<const uint4*>(p.x + at)[c] : make_uint4(0, 0, 0, 0);
-      if (p.res)
-        q[i] = ok ? reinterpret_cast<const uint4*>(p.res + at)[c] : make_uint4(0, 0, 0, 0);
-    }
-    float ss = 0.f;
+  for (int i = 0; i < V; ++i) {
+    const int c = sub + i * p.tpr;
+    const bool ok = t < p.T && c < cpr;
+    v[i] = ok ? reinterpret_cast<const uint4*>(p.x + at)[c] : make_uint4(0, 0, 0, 0);
+    if (p.res)
+      q[i] = ok ? reinterpret_cast<const uint4*>(p.res + at)[c] : make_uint4(0, 0, 0, 0);
+  }
+  uint4 wv[V];  // ahead of the sum where latency counts (registers are short with V = 8)
+  auto weight = [&](int i) {
+    const int c = sub + i * p.tpr;
+    return c < cpr ? __ldg(reinterpret_cast<const uint4*>(p.w) + c) : make_uint4(0, 0, 0, 0);
+  };
+  if (V == 2) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      uint32_t* a = reinterpret_cast<uint32_t*>(&v[i]);
-      if (p.res) {
-        const uint32_t* b = reinterpret_cast<const uint32_t*>(&q[i]);
+    for (int i = 0; i < V; ++i) wv[i] = weight(i);
+  }
+  float ss = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          a[j] = pack2(bf16_lo(a[j]) + bf16_lo(b[j]), bf16_hi(a[j]) + bf16_hi(b[j]));
-        const int c = sub + i * p.tpr;
-        if (p.r && t < p.T && c < cpr) reinterpret_cast<uint4*>(p.r + at)[c] = v[i];
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        ss = fmaf(bf16_lo(a[j]), bf16_lo(a[j]), ss);
-        ss = fmaf(bf16_hi(a[j]), bf16_hi(a[j]), ss);
-      }
-    }
-    ss = row_sum(ss, p.tpr, s_part[buf]);
-    const float rs = 1.f / sqrtf(ss / (float)p.H + p.eps);
-    if (p.rstd && sub == 0 && t < p.T) p.rstd[t] = rs;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = sub + i * p.tpr;
-      const bool ok = t < p.T && c < cpr;
-      const uint4 wv = c < cpr ? __ldg(reinterpret_cast<const uint4*>(p.w) + c) : make_uint4(0, 0, 0, 0);
-      const uint32_t* wp = reinterpret_cast<const uint32_t*>(&wv);
-      uint32_t* a = reinterpret_cast<uint32_t*>(&v[i]);
+  for (int i = 0; i < V; ++i) {
+    uint32_t* a = reinterpret_cast<uint32_t*>(&v[i]);
+    if (p.res) {
+      const uint32_t* b = reinterpret_cast<const uint32_t*>(&q[i]);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        a[j] = pack2(bf16_lo(a[j]) * rs * bf16_lo(wp[j]), bf16_hi(a[j]) * rs * bf16_hi(wp[j]));
-      if (ok && p.y) reinterpret_cast<uint4*>(p.y + at)[c] = v[i];
-      if (!p.yq) continue;
-      // a block is 16 threads' columns (8 threads' in a row of 64)
-      uint32_t m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(0, a[0]), a[1]), a[2]), a[3]);
-      m = c < cpr ? absmax_bits(m) : 0;
+        a[j] = pack2(bf16_lo(a[j]) + bf16_lo(b[j]), bf16_hi(a[j]) + bf16_hi(b[j]));
+      const int c = sub + i * p.tpr;
+      if (p.r && t < p.T && c < cpr) reinterpret_cast<uint4*>(p.r + at)[c] = v[i];
+    }
 #pragma unroll
-      for (int o = 1; o < 16; o <<= 1)
-        if (o < p.tpr) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const uint32_t b = fp8_scale_byte(m), inv = fp8_inv_scale2(b);
-      if (ok)
-        reinterpret_cast<uint2*>(p.yq + at)[c] =
-            make_uint2(fp8x4_of_bf16(a[0], a[1], inv), fp8x4_of_bf16(a[2], a[3], inv));
-      if ((c & 15) == 0 && c < cpr)
-        reinterpret_cast<uint8_t*>(s_words)[lr * 4 * nw + (c >> 4)] = (uint8_t)b;
+    for (int j = 0; j < 4; ++j) {
+      ss = fmaf(bf16_lo(a[j]), bf16_lo(a[j]), ss);
+      ss = fmaf(bf16_hi(a[j]), bf16_hi(a[j]), ss);
     }
-    if (p.yq) {  // whole words: their bytes come from several threads
-      if (p.tpr <= 32) __syncwarp();
-      else __syncthreads();
-      for (int i = sub; i < nw; i += p.tpr)
-        if (t < p.T) p.ys[(size_t)i * p.T + t] = s_words[lr * nw + i];
-      if (p.tpr <= 32) __syncwarp();
-      else __syncthreads();
-    }
+  }
+  ss = row_sum(ss, p.tpr, s_part);
+  const float rs = 1.f / sqrtf(ss / (float)p.H + p.eps);
+  if (p.rstd && sub == 0 && t < p.T) p.rstd[t] = rs;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = sub + i * p.tpr;
+    const bool ok = t < p.T && c < cpr;
+    if (V != 2) wv[i] = weight(i);
+    const uint32_t* wp = reinterpret_cast<const uint32_t*>(&wv[i]);
+    uint32_t* a = reinterpret_cast<uint32_t*>(&v[i]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      a[j] = pack2(bf16_lo(a[j]) * rs * bf16_lo(wp[j]), bf16_hi(a[j]) * rs * bf16_hi(wp[j]));
+    if (ok && p.y) reinterpret_cast<uint4*>(p.y + at)[c] = v[i];
+    if (!p.yq) continue;
+    // a block is 16 threads' columns (8 threads' in a row of 64)
+    uint32_t m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(0, a[0]), a[1]), a[2]), a[3]);
+    m = c < cpr ? absmax_bits(m) : 0;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1)
+      if (o < p.tpr) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const uint32_t b = fp8_scale_byte(m), inv = fp8_inv_scale2(b);
+    if (ok)
+      reinterpret_cast<uint2*>(p.yq + at)[c] =
+          make_uint2(fp8x4_of_bf16(a[0], a[1], inv), fp8x4_of_bf16(a[2], a[3], inv));
+    if ((c & 15) == 0 && c < cpr)
+      reinterpret_cast<uint8_t*>(s_words)[lr * 4 * nw + (c >> 4)] = (uint8_t)b;
+  }
+  if (p.yq) {  // whole words: their bytes come from several threads
+    if (p.tpr <= 32) __syncwarp();
+    else __syncthreads();
+    for (int i = sub; i < nw; i += p.tpr)
+      if (t < p.T) p.ys[(size_t)i * p.T + t] = s_words[lr * nw + i];
   }
 }
 
@@ -153,10 +156,11 @@ struct NormBwdParams {
   int T, H, tpr;
 };
 
-template <int V>
-__global__ void __launch_bounds__(V == 2 ? kMaxThreads : kThreads) rms_norm_bwd_kernel(const NormBwdParams p) {
+// BLOCKS resident on an SM, each with a row's partial sums of dw in registers
+template <int V, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) rms_norm_bwd_kernel(const NormBwdParams p) {
   extern __shared__ float s_dw[];  // [H]
-  __shared__ float s_part[2][kMaxThreads / 32];
+  __shared__ float s_part[2][THREADS / 32];
   const int rows = blockDim.x / p.tpr, lr = threadIdx.x / p.tpr, sub = threadIdx.x % p.tpr;
   const int cpr = p.H / 8;
   const float inv_h = 1.f / (float)p.H;
@@ -249,8 +253,8 @@ __global__ void __launch_bounds__(V == 2 ? kMaxThreads : kThreads) rms_norm_bwd_
   }
 }
 
-// dw[h] = sum over the partial rows, in a fixed order: 16 columns a block, 16 threads
-// of four columns... each of 64 groups takes every 64th row, then a tree.
+// dw[h] = sum over the partial rows, in a fixed order: 16 columns a block, four threads
+// across them; each of 64 groups of four takes every 64th row, then a tree.
 constexpr int kDwCols = 16, kDwGroups = 64;
 __global__ void __launch_bounds__(kDwCols / 4 * kDwGroups)
     rms_norm_dw_kernel(const float* __restrict__ part, float* __restrict__ dw, int parts, int H) {
@@ -295,9 +299,10 @@ moe_status_t launch_rms_norm(const moe_layer_desc_t& d, const bf16* x, const bf1
   const int vecs = few ? 2 : 8;
   NormParams p = {x, res, w, eps, r, y, yq, reinterpret_cast<uint32_t*>(ys), rstd, d.T, d.H,
                   row_threads(d.H, vecs)};
-  const int threads = std::max(p.tpr, few ? 32 : kThreads);
-  const int rows = threads / p.tpr;
-  const int grid = std::min(ceil_div(d.T, rows), device_sm_count() * 8);
+  // many rows: small blocks of a few rows each, dealt by the hardware (prompts of 32768 x
+  // 2048: 94 us; 256 threads a block 97, a resident wave of blocks that loop 97)
+  const int threads = std::max(p.tpr, few ? 32 : 64);
+  const int rows = threads / p.tpr, grid = ceil_div(d.T, rows);
   const size_t smem = yq ? (size_t)rows * ceil_div(d.H, 512) * 4 : 0;
   cudaError_t e;
   {
@@ -318,14 +323,17 @@ moe_status_t launch_rms_norm_bwd(const moe_layer_desc_t& d, const bf16* dy, cons
   int grid = 0;
   cudaError_t e = cudaSuccess;
   if (d.T > 0) {
-    const int vecs = d.H > 8192 ? 2 : 4;
-    NormBwdParams p = {dy, dr, r, w, rstd, dx, part, d.T, d.H, row_threads(d.H, vecs)};
-    const int threads = std::max(p.tpr, kThreads), rows = threads / p.tpr;
-    grid = std::min({ceil_div(d.T, rows), device_sm_count() * 2, kMaxParts});
+    // Rows of up to 4096: three blocks of 256 threads with two groups of 8 columns each (4096 x
+    // 2048: 17.3 us with the sum over blocks; four groups and two blocks 18.4, one group and
+    // four blocks 18.7, four groups in one block, which is what fits unasked, 24.3)
+    const bool wide = d.H > 4096;
+    NormBwdParams p = {dy, dr, r, w, rstd, dx, part, d.T, d.H, row_threads(d.H, wide ? 4 : 2)};
+    const int threads = wide ? 512 : 256, rows = threads / p.tpr;
+    grid = std::min({ceil_div(d.T, rows), device_sm_count() * (wide ? 1 : 3), kMaxParts});
     const size_t smem = rows > 1 ? (size_t)d.H * sizeof(float) : 0;
     LaunchScope _ls(K_NORM_BWD, st);
-    e = vecs == 2 ? launch_k(rms_norm_bwd_kernel<2>, grid, threads, smem, st, p)
-                  : launch_k(rms_norm_bwd_kernel<4>, grid, threads, smem, st, p);
+    e = wide ? launch_k(rms_norm_bwd_kernel<4, 512, 1>, grid, threads, smem, st, p)
+             : launch_k(rms_norm_bwd_kernel<2, 256, 3>, grid, threads, smem, st, p);
   }
   if (e == cudaSuccess) {
     LaunchScope _ls(K_NORM_DW, st);
