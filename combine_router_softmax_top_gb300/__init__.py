@@ -388,30 +388,32 @@ _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _fp8_call(what, desc, spec, tensors, sizes, stream, *tail, at=None, value=None):
+_specs = {}  # call -> what _py_call knows of it
+
+
+def _call_spec(what, spec):
+    lib()
+    from . import _py_call
+    _specs[what] = s = (_py_call.call, _py_call.spec(what, tuple((dt, opt) for _, dt, opt in spec)))
+    return s
+
+
+def _fp8_call(what, desc, spec, tensors, sizes, stream, tail=0, value=0.0):
     """Checks a call's tensors and makes it: of spec's types, contiguous, on the current
-    device, with at least so many elements, or None where spec allows it. `value` is an
-    argument that is no tensor, ahead of tensors[at]. Small calls are bound by this
-    function: no object is built that they do not need."""
+    device, with at least so many elements, or None where spec allows it. tail, value: its
+    workspace's size and its number that is no tensor, for calls that have them. Small calls
+    are bound by their way here, so the checks are csrc/py_call.cpp's."""
     first = tensors[0]
     dev = -1 if first is None else first.get_device()
     if dev < 0 or dev != _get_device():
         _fp8_refuse(what, spec, tensors, sizes)
-    p = []
-    for t, (_, dt, may_be_none), n in zip(tensors, spec, sizes):
-        if t is None:
-            if not may_be_none:
-                _fp8_refuse(what, spec, tensors, sizes)
-            p.append(None)
-        elif (t.dtype is dt and t.numel() >= n and t.get_device() == dev and t.is_contiguous()):
-            p.append(t.data_ptr())
-        else:
-            _fp8_refuse(what, spec, tensors, sizes)
-    if at is not None:
-        p.insert(at, value)
-    st = _raw_stream(dev) if stream is None and _raw_stream is not None else _s(stream)
-    status = getattr(_lib or lib(), what)(ctypes.byref(desc), *p, *tail, st)
+    st = (_raw_stream(dev) if stream is None and _raw_stream is not None
+          else _s(stream).value or 0)
+    call, known = _specs.get(what) or _call_spec(what, spec)
+    status = call(known, ctypes.addressof(desc), dev, st, sizes, value, tail, tensors)
     if status != MOE_OK:
+        if status is None:
+            _fp8_refuse(what, spec, tensors, sizes)
         _check(status, what)
 
 
@@ -596,7 +598,7 @@ def moe_rms_norm(desc, x, res, w, eps, r, y, yq=None, ys=None, rstd=None, stream
     T, H = desc.T, desc.H
     n = T * H
     _fp8_call("moe_rms_norm", desc, _SPEC_NORM, (x, res, w, r, y, yq, ys, rstd),
-              (n, n, H, n, n, n, _words(T, H), T), stream, at=3, value=eps)
+              (n, n, H, n, n, n, _words(T, H), T), stream, value=eps)
 
 
 def moe_rms_norm_bwd_workspace_size(desc: LayerDesc) -> int:

@@ -1,7 +1,8 @@
-"""Builds libmoe.so (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Builds libmoe.so (the C-ABI library) in-tree with nvcc for sm_103a, and _py_call.so
+(the binding's call path, csrc/py_call.cpp) with g++ against it.
 
-Each .cu file compiles in parallel to an object under _build/, then nvcc links
-the shared library next to this file. A rebuild happens only when a source or
+Each source compiles in parallel to an object under _build/, then the shared
+libraries are linked next to this file. A rebuild happens only when a source or
 header is newer than the library. No CMake; works the same on x86_64 (where
 it cross-compiles without a GPU) and on aarch64.
 """
@@ -12,12 +13,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
+PY_CALL = os.path.join(HERE, "_py_call.so")
+PY_CALL_SOURCE = os.path.join(CSRC, "py_call.cpp")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -44,9 +48,9 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(PY_CALL)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(PY_CALL))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -61,21 +65,51 @@ def _compile(src: str, extra, verbose: bool) -> str:
     return obj
 
 
+def _torch_dir() -> str:
+    import torch  # (its headers and libraries, not a device)
+    return os.path.dirname(torch.__file__)
+
+
+def _compile_py_call() -> str:
+    inc, obj = os.path.join(_torch_dir(), "include"), os.path.join(BUILD, "py_call.o")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
+           "-I", INCLUDE, "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-c", PY_CALL_SOURCE, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on py_call.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_py_call(obj: str):
+    tmp = PY_CALL + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", HERE, "-l:libmoe.so",
+           "-Wl,-rpath,$ORIGIN", "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, PY_CALL)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compiles and links libmoe.so if needed; returns its path."""
+    """Compiles and links libmoe.so and _py_call.so if needed; returns the former's path."""
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-Xptxas", "-v"] if ptxas_verbose else []
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        py_call = ex.submit(_compile_py_call)
         objs = list(ex.map(lambda s: _compile(s, extra, verbose or ptxas_verbose), srcs))
+        py_obj = py_call.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_py_call(py_obj)
     return LIB
 
 
