@@ -49,15 +49,6 @@ __device__ __forceinline__ uint32_t fp4x8(const float* v) {
       : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return w;
 }
-__device__ __forceinline__ uint32_t fp4x2(float lo, float hi) {
-  uint32_t w;
-  asm("{\n\t.reg .b8 b0;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
-      "cvt.u32.u8 %0, b0;\n\t}"
-      : "=r"(w)
-      : "f"(lo), "f"(hi));
-  return w;
-}
 // Larger magnitude; NaN if either is
 __device__ __forceinline__ float absmax_nan(float m, float v) {
   asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v)));

@@ -14,8 +14,8 @@
 //               contiguous copies, on the same barrier
 //   warp 1      TMEM allocator + MMA issuer
 //   warp 2      claims tiles
-//   warps 4..7  epilogue: thread = weight row (column of h or o), registers = rows; a
-//               warp's 32 columns of h are one block
+//   warps 4..7  epilogue: thread = weight row (column of h or o), registers = rows; then, by
+//               way of shared memory, thread = a block (32 columns) of a row of h
 //   warps 8..11 a stage's scales from shared memory into TMEM, ahead of its MMAs
 #include <algorithm>
 #include <atomic>
@@ -50,6 +50,11 @@ static_assert(kTmemScales + kSf * kSfCols <= kTmemCols, "TMEM columns");
 static_assert(kFp4FewRows * kMaxE < 65536, "16-bit tables");
 constexpr size_t kDynSmem = (size_t)kStages * kStageBytes + 1024;
 
+// The tile's h between the epilogue's two views: a thread writes its column of every row,
+// then takes a block (32 columns) of one row. Blocks 36 floats apart and rows 144: neither
+// the writes nor the 16-byte reads of 8 lanes (two rows' four blocks) meet in a bank.
+constexpr int kHBlock = 36, kHRow = 4 * kHBlock;
+
 struct RowsParams {
   int E, H, F;
   long long N;
@@ -77,7 +82,9 @@ struct SmemCtl {
   int abort;
   uint16_t rtile[kMaxE + 1];      // first row tile of each expert
   uint16_t off[kMaxE + 1];
+  alignas(16) float h[NT * kHRow];  // read 16 bytes at a time
 };
+static_assert(kHBlock % 4 == 0 && kHRow % 4 == 0, "16-byte reads of a row's blocks");
 
 template <int G>
 __device__ __forceinline__ int kvalues(const RowsParams& p) { return G == kFc1 ? p.H : p.F; }
@@ -351,11 +358,8 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const RowsParams& p, c
   ptx::tc_fence_after();
   const uint32_t tbase = tmem + acc * kAccCols + ((uint32_t)(q * 32) << 16);
   if (G == kFc1) {
-    const int f = t.n0 + col, blk = (t.n0 >> 5) + q;
+    const int f = t.n0 + col;
     const bool ok = f < p.F;  // uniform in the warp: F is a multiple of 64
-    const long long np = scale_rows(p.N);
-    uint8_t* hs = p.hs + ((size_t)(blk >> 3) * np + t.row) * 8 + (blk & 7);
-    uint8_t* hq = p.hq + ((size_t)t.row * p.F + f) / 2;
     for (int r0 = 0; r0 < t.rows && ok; r0 += 8) {
       uint32_t g[8], u[8];
       tmem_ld_x8(tbase + r0, g);
@@ -374,20 +378,36 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const RowsParams& p, c
           a[p.F] = __float2bfloat16_rn(uf);
         }
         if (p.h) p.h[row * p.F + f] = __float2bfloat16_rn(hf);
-        const uint32_t b =
-            fp4_scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(hf) & 0x7FFFFFFFu));
-        const float v = hf * fp4_inv_scale(b);
-        // lane 8 i collects the codes of the lanes up to 8 i + 7
-        uint32_t w = fp4x2(v, __shfl_down_sync(0xffffffffu, v, 1));
-        w |= __shfl_down_sync(0xffffffffu, w, 2) << 8;
-        w |= __shfl_down_sync(0xffffffffu, w, 4) << 16;
-        if ((lane & 7) == 0)
-          *reinterpret_cast<uint32_t*>(hq + (size_t)(r0 + j) * (p.F / 2)) = w;
-        if (lane == 0) hs[(r0 + j) * 8] = (uint8_t)b;
+        c.h[(r0 + j) * kHRow + q * kHBlock + lane] = hf;
       }
     }
     arrive(&c.tmem_empty[acc], lane);
-    epilogue_sync();  // every store issued
+    epilogue_sync();  // the tile's h is in shared memory
+    const int r = col >> 2, fb = t.n0 + 32 * (col & 3);  // this thread's row and block
+    if (r < t.rows && fb < p.F) {
+      const float4* hp = reinterpret_cast<const float4*>(&c.h[r * kHRow + (col & 3) * kHBlock]);
+      float v[32], mx = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 x = hp[i];
+        v[4 * i] = x.x;
+        v[4 * i + 1] = x.y;
+        v[4 * i + 2] = x.z;
+        v[4 * i + 3] = x.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) mx = absmax_nan(mx, v[i]);
+      const uint32_t b = fp4_scale_byte(__float_as_uint(mx));
+      const float inv = fp4_inv_scale(b);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] *= inv;
+      const size_t row = (size_t)(t.row + r);
+      const int blk = fb >> 5;
+      *reinterpret_cast<uint4*>(p.hq + (row * p.F + fb) / 2) =
+          make_uint4(fp4x8(v), fp4x8(v + 8), fp4x8(v + 16), fp4x8(v + 24));
+      p.hs[((size_t)(blk >> 3) * scale_rows(p.N) + row) * 8 + (blk & 7)] = (uint8_t)b;
+    }
+    epilogue_sync();  // every store issued, and c.h free again
     if (col == 0) {
       __threadfence();
       atomicAdd(p.dep + t.e, 1);
