@@ -71,8 +71,18 @@ moe_status_t launch_ffn_fwd_fp4(const moe_layer_desc_t& d, const uint8_t* xq, co
                                 uint8_t* hq, uint8_t* hs, bf16* o, int* status, int* dep,
                                 cudaStream_t st);
 // The forward for few rows an expert (rows_fp4.cu), which launch_ffn_fwd_fp4 takes up to
-// kFp4FewRows rows an expert on average.
-constexpr long long kFp4FewRows = 48;
+// kFp4FewRows rows an expert on average. Measured, this kernel against the GEMMs, us,
+// nothing kept:
+//   rows an expert on average            4         16        32        64        96
+//   128 experts, H 2048, F 768      54 / 92   57 / 93   59 / 96  83 / 106  119 / 95
+//     skewed                        51 / 86   60 / 93   69 / 97 106 / 105 139 / 111
+//   64 experts, H 2048, F 1408      50 / 71   52 / 73   53 / 77   71 / 88  102 / 74
+//   16 experts, H 1024, F 1024      12 / 20   14 / 20   14 / 21   20 / 22   20 / 21
+//   8 experts, H 4096, F 1408       22 / 28   23 / 28   24 / 30   27 / 33   33 / 29
+//   32 experts, H 512, F 512        11 / 19   11 / 19   12 / 19   17 / 19   18 / 20
+//   16 experts, H 320, F 448, skewed 10 / 14  11 / 14   11 / 15   13 / 15   15 / 15
+// The rule sees the average alone, as the offsets are on the device.
+constexpr long long kFp4FewRows = 64;
 moe_status_t launch_ffn_rows_fp4(const moe_layer_desc_t& d, const uint8_t* xq, const uint8_t* xs,
                                  const int32_t* off, const Fp4Weights& w, bf16* a, bf16* h,
                                  uint8_t* hq, uint8_t* hs, bf16* o, int* status, int* dep,

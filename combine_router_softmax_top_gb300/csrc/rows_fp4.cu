@@ -54,6 +54,8 @@ constexpr size_t kDynSmem = (size_t)kStages * kStageBytes + 1024;
 // then takes a block (32 columns) of one row. Blocks 36 floats apart and rows 144: neither
 // the writes nor the 16-byte reads of 8 lanes (two rows' four blocks) meet in a bank.
 constexpr int kHBlock = 36, kHRow = 4 * kHBlock;
+constexpr int kORow = 264;  // and of a tile of o, bf16
+static_assert(kORow % 8 == 0 && NT * kORow * 2 <= NT * kHRow * 4, "o's rows in h's room");
 
 struct RowsParams {
   int E, H, F;
@@ -413,20 +415,29 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, const RowsParams& p, c
       atomicAdd(p.dep + t.e, 1);
     }
   } else {
+    // by way of shared memory too, so that rows leave 16 bytes a thread
     const int mt = mtiles<G>(p, t);
+    bf16* buf = reinterpret_cast<bf16*>(c.h);
     for (int m = 0; m < mt; ++m) {
-      const int h = t.n0 + 128 * m + col;
       for (int r0 = 0; r0 < t.rows; r0 += 8) {
         uint32_t v[8];
         tmem_ld_x8(tbase + NT * m + r0, v);
         tmem_ld_wait_x8(v);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (r0 + j < t.rows && h < p.H)
-            p.o[(size_t)(t.row + r0 + j) * p.H + h] = __float2bfloat16_rn(__uint_as_float(v[j]));
+          if (r0 + j < t.rows)
+            buf[(r0 + j) * kORow + 128 * m + col] = __float2bfloat16_rn(__uint_as_float(v[j]));
       }
     }
     arrive(&c.tmem_empty[acc], lane);
+    epilogue_sync();
+    for (int i = col; i < t.rows * 32; i += 128) {
+      const int r = i >> 5, x = (i & 31) * 8;
+      if (t.n0 + x < p.H)
+        *reinterpret_cast<uint4*>(p.o + (size_t)(t.row + r) * p.H + t.n0 + x) =
+            *reinterpret_cast<const uint4*>(buf + r * kORow + x);
+    }
+    epilogue_sync();  // c.h is free again
   }
   ++tiles;
   return *(volatile int*)&c.abort == 0;

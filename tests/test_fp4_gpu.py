@@ -201,6 +201,7 @@ SHAPES = [  # T, H, E, k, F, skew
     (49, 64, 1, 1, 64, 0), (100, 320, 2, 1, 448, 0), (129, 192, 2, 2, 64, 0), (257, 256, 2, 2, 320, 1),
     (400, 512, 8, 4, 192, 1), (600, 64, 3, 2, 576, 1), (500, 576, 6, 3, 256, 2), (1000, 320, 16, 4, 448, 1),
     (255, 1344, 4, 2, 128, 1), (3000, 128, 4, 2, 128, 1), (64, 2048, 1, 1, 768, 0),
+    (65, 64, 1, 1, 64, 0), (70, 2048, 1, 1, 768, 0), (140, 320, 2, 1, 448, 0), (128, 64, 2, 2, 192, 2),
 ]
 
 
