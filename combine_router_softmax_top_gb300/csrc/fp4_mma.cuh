@@ -55,6 +55,16 @@ __device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&w)[8
                : "memory");
 }
 
+// This warp's 32 lanes x 16 TMEM columns
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&w)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]),
+      "r"(w[8]), "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
+      : "memory");
+}
+
 // Rows of an activation's scale buffer for N rows: even
 inline __host__ __device__ long long scale_rows(long long n) { return (n + 1) & ~1ll; }
 

@@ -50,9 +50,9 @@ enum Fp4Mode {
 
 constexpr int BM = 128, BN = 256, BK = kFp4Group;  // BM: rows of one CTA of the pair
 constexpr int kRowBytes = BK / 2;                  // of a stage
-constexpr int kABytes = BM * kRowBytes, kBBytes = BN / 2 * kRowBytes;
-constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kStages = 6;
+constexpr int kSlotBytes = 128 * kRowBytes;        // a stage of A's rows, or of half of B's
+constexpr int kSlots = 12;                         // shared by A and B (below)
+constexpr int kMaxA = 8, kMaxB = 8;
 constexpr int kEpiBytes = 8 * 2048;           // a 32 x 32 bf16 box for each epilogue warp
 constexpr int kScA = 1152;                    // scales of a stage: 128 rows of A from an even one on ...
 constexpr int kScBytes = kScA + BN * 8;       // ... and all of B's
@@ -61,17 +61,20 @@ static_assert((BM + 2) * 8 <= kScA && kScA % 16 == 0, "room for A's scales");
 constexpr int kABoxRows = 16;                 // tiles of 64 rows or fewer load boxes of 16
 constexpr int kTmemCols = 512;
 constexpr int kAccStep = 128;                 // second accumulator's first column
-constexpr int kTmemScales = 384;              // buffers of 24: for each half of a stage 4 for A, 8 for B
-constexpr int kSf = 5, kSfCols = 24;
-static_assert(kTmemScales + kSf * kSfCols <= kTmemCols, "TMEM columns");
+// scale columns: 8 for each slot of A (4 for each half of a stage), buffers of 16 for B
+constexpr int kTmemA = 384, kTmemB = kTmemA + 8 * kMaxA;
+constexpr int kSf = 4;
+static_assert(kTmemB + 16 * kSf <= kTmemCols, "TMEM columns");
 constexpr int kThreads = 512;
 // registers a thread: 128 at launch; the epilogue's two warpgroups take what the
 // control and scale warpgroups give up (2 * 72 + 2 * 184 = 4 * 128)
 constexpr int kRegsControl = 72, kRegsEpilogue = 184;
 constexpr int kMaxE = 256;
-constexpr int kEpiAt = kStages * kStageBytes, kScAt = kEpiAt + kEpiBytes;
+constexpr int kEpiAt = kSlots * kSlotBytes, kScAt = kEpiAt + kEpiBytes;
 constexpr size_t kDynSmem = kScAt + kSc * kScBytes + 1024;
 constexpr int kHalf = 8;  // slots of half a mailbox (below)
+// strips (below) that a pair should get of each product, if they can be as many
+constexpr int kStripsAPair = 6;
 
 struct Maps {
   CUtensorMap a1, s1, b1, a2, s2, b2;  // operands: A, A in small boxes, B of both GEMMs
@@ -87,7 +90,9 @@ struct KParams {
   uint8_t *hq, *hs;
   int* status;
   int* dep;           // per-expert count of FC1 tiles stored, by CTA
-  int* tile;          // tiles claimed
+  int* tile;          // strips claimed
+  int na, nb;         // slots of A and of B
+  int strip[2];       // tiles of a strip, in both products
 };
 
 template <int MODE>
@@ -99,13 +104,15 @@ __device__ __forceinline__ int ntiles(const KParams& p) {
   return MODE == FC1 ? (p.F + 127) / 128 : (p.H + BN - 1) / BN;
 }
 
-struct Tile {
-  int e, m0, n0, rows, row0;  // m0: first row of this CTA's 128 in the expert; rows <= 0: none
-  int rows_odd;               // even CTA: rows left for the odd one
+// A strip: up to p.strip tiles side by side, over the same rows.
+struct Strip {
+  int e, m0, rows, row0;  // m0: first row of this CTA's 128 in the expert; rows <= 0: none
+  int rows_odd;           // even CTA: rows left for the odd one
+  int n0, n1;             // tiles
 };
 
 struct SmemCtl {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t a_empty[kMaxA], full[kMaxB], empty[kMaxB];
   uint64_t sc_full[kSc], sc_empty[kSc];    // scales in shared memory (each CTA its own)
   uint64_t sf_full[kSf], sf_empty[kSf];    // scales in TMEM
   uint64_t tmem_full[2], tmem_empty[2], ovl, drain;
@@ -116,28 +123,36 @@ struct SmemCtl {
   uint64_t stored[2], counted[2];  // an FC1 tile's stores issued; counted for its expert
   uint32_t tmem_base;
   int abort;
-  int tstart[2][kMaxE + 1];  // tile prefixes of the two GEMMs
+  int tstart[2][kMaxE + 1];  // strip prefixes of the two GEMMs
   int off[kMaxE + 1];
 };
 static_assert(kDynSmem + sizeof(SmemCtl) <= 232448, "shared memory of a CTA");
 
 template <int MODE>
-__device__ __forceinline__ Tile tile_at(const KParams& p, const SmemCtl& c, int tile, int& cursor,
-                                        uint32_t rank) {
+__device__ __forceinline__ int strips(const KParams& p) {  // across an expert
+  return (ntiles<MODE>(p) + p.strip[MODE] - 1) / p.strip[MODE];
+}
+template <int MODE>
+__device__ __forceinline__ Strip strip_at(const KParams& p, const SmemCtl& c, int i, int& cursor,
+                                          uint32_t rank) {
   const int* tstart = c.tstart[MODE];
-  while (tstart[cursor + 1] <= tile) ++cursor;
-  Tile t;
+  while (tstart[cursor + 1] <= i) ++cursor;
+  Strip t;
   t.e = cursor;
   t.row0 = c.off[cursor];
   const int cnt = c.off[cursor + 1] - t.row0;
-  const int local = tile - tstart[cursor];
+  const int local = i - tstart[cursor];
   const int mt = (cnt + 2 * BM - 1) / (2 * BM);
-  t.m0 = (local % mt) * 2 * BM + (int)rank * BM;
-  t.n0 = (local / mt) * (MODE == FC1 ? 128 : BN);
+  t.m0 = (local % mt) * 2 * BM + (int)rank * BM;  // row tiles fastest: they share the weights
+  t.n0 = (local / mt) * p.strip[MODE];
+  t.n1 = min(t.n0 + p.strip[MODE], ntiles<MODE>(p));
   t.rows = min(BM, cnt - t.m0);
   t.rows_odd = rank == 0 ? cnt - t.m0 - BM : 0;
   return t;
 }
+// First column of h or o of a tile
+template <int MODE>
+__device__ __forceinline__ int column(int n) { return n * (MODE == FC1 ? 128 : BN); }
 
 __device__ __forceinline__ void give_up(SmemCtl& c, int* status, int where) {
   c.abort = 1;
@@ -190,7 +205,8 @@ __device__ __forceinline__ void store_box(const Out& o, const CUtensorMap* map, 
 // An FC2 tile of expert e: wait (bounded) until the expert's FC1 tiles have all stored
 // their output.
 __device__ __forceinline__ bool wait_expert(SmemCtl& c, const KParams& p, int e) {
-  const int target = 2 * (c.tstart[0][e + 1] - c.tstart[0][e]);  // both CTAs of the pair
+  // tiles of the first product, by both CTAs of the pair
+  const int target = 2 * ((c.off[e + 1] - c.off[e] + 2 * BM - 1) / (2 * BM)) * ntiles<FC1>(p);
   if (ld_acquire(p.dep + e) < target) {
     const uint64_t t0 = ptx::globaltimer_ns();
     while (ld_acquire(p.dep + e) < target) {
@@ -274,87 +290,109 @@ __device__ __forceinline__ void claim_tiles(SmemCtl& c, const KParams& p, int fi
 }
 
 // ================================================================ producer
+// The rows of a strip stay in shared memory while its tiles pass: A is loaded, a slot a
+// stage, with the first tile's B, and its slots are released by the last tile's MMAs.
+// (Rows of more than kMaxA stages stream: a strip is then one tile.) A pair lands 64 KB of
+// operands in 512 clocks of MMAs otherwise, and every byte of it takes shared memory's time
+// from the tensor cores' own reads.
+//
 // Bytes of A loaded for a CTA's `rows` valid rows: rows that no expert has are not
 // fetched (what the buffer held stays in the unused rows of the product).
 __device__ __forceinline__ int a_bytes(int rows) {
   return rows <= 0 ? 0
-         : rows > 64 ? kABytes
+         : rows > 64 ? kSlotBytes
                      : (rows + kABoxRows - 1) / kABoxRows * kABoxRows * kRowBytes;
 }
 
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++at == n) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 template <int MODE>
-__device__ __forceinline__ bool producer_tile(SmemCtl& c, uint8_t* smem, const KParams& p,
-                                              const CUtensorMap* tmA, const CUtensorMap* tmS,
-                                              const CUtensorMap* tmB, const Tile& t, uint32_t rank,
-                                              int& stage, uint32_t& phase) {
+__device__ __forceinline__ bool producer_strip(SmemCtl& c, uint8_t* smem, const KParams& p,
+                                               const CUtensorMap* tmA, const CUtensorMap* tmS,
+                                               const CUtensorMap* tmB, const Strip& t, uint32_t rank,
+                                               Ring& ra, Ring& rb) {
   // (the even CTA announces both CTAs' bytes)
-  const uint32_t bytes = 2 * kBBytes + a_bytes(t.rows) + a_bytes(min(BM, t.rows_odd));
+  const uint32_t bytes = a_bytes(t.rows) + a_bytes(min(BM, t.rows_odd));
   const int row = t.row0 + t.m0, nk = kstages<MODE>(p);
   // FC1: even CTA 128 gate rows of W1, odd CTA 128 up rows
-  const int brow = MODE == FC1 ? (2 * t.e + (int)rank) * p.F + t.n0 : t.e * p.H + t.n0 + 128 * (int)rank;
+  const int brow = MODE == FC1 ? (2 * t.e + (int)rank) * p.F : t.e * p.H + 128 * (int)rank;
   if (MODE == FC2) {
     if (!wait_expert(c, p, t.e)) return false;
     // the generic writes it waited for, before the TMA (async-proxy) reads
     asm volatile("fence.proxy.async.global;" ::: "memory");
   }
-  for (int kt = 0; kt < nk; ++kt) {
-    if (!ptx::mbar_wait(&c.empty[stage], phase ^ 1, &c.abort, kWaitLimitNs)) {
-      give_up(c, p.status, 65);
-      return false;
-    }
-    if (rank == 1 && kt == nk / 4) ptx::mbar_arrive(&c.claim);
-    uint8_t* sA = smem + stage * kStageBytes;
-    const int k0 = kt * kRowBytes;
-    // both CTAs' loads complete on the even CTA's full[stage]
-    uint64_t* bar = &c.full[stage];
-    const uint32_t fb = ptx::mapa_shared(bar, 0);
-    if (rank == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
-    if (t.rows > 64) ptx::tma_load_2d_pair(sA, tmA, fb, k0, row);
-    else
-      for (int r = 0; r < t.rows; r += kABoxRows)
-        ptx::tma_load_2d_pair(sA + r * kRowBytes, tmS, fb, k0, row + r);
-    ptx::tma_load_2d_pair(sA + kABytes, tmB, fb, k0, brow);
-    if (++stage == kStages) {
-      stage = 0;
-      phase ^= 1;
+  for (int n = t.n0; n < t.n1; ++n) {
+    for (int kt = 0; kt < nk; ++kt) {
+      const int k0 = kt * kRowBytes;
+      const bool first = n == t.n0;
+      if (!ptx::mbar_wait(&c.empty[rb.at], rb.phase ^ 1, &c.abort, kWaitLimitNs) ||
+          (first && !ptx::mbar_wait(&c.a_empty[ra.at], ra.phase ^ 1, &c.abort, kWaitLimitNs))) {
+        give_up(c, p.status, 65);
+        return false;
+      }
+      if (rank == 1 && first && kt == nk / 4) ptx::mbar_arrive(&c.claim);
+      // both CTAs' loads complete on the even CTA's barrier
+      uint64_t* bar = &c.full[rb.at];
+      const uint32_t fb = ptx::mapa_shared(bar, 0);
+      if (rank == 0) ptx::mbar_arrive_expect_tx(bar, 2 * kSlotBytes + (first ? bytes : 0));
+      if (first) {
+        uint8_t* sA = smem + ra.at * kSlotBytes;
+        if (t.rows > 64) ptx::tma_load_2d_pair(sA, tmA, fb, k0, row);
+        else
+          for (int r = 0; r < t.rows; r += kABoxRows)
+            ptx::tma_load_2d_pair(sA + r * kRowBytes, tmS, fb, k0, row + r);
+        ra.next(p.na);
+      }
+      ptx::tma_load_2d_pair(smem + (p.na + rb.at) * kSlotBytes, tmB, fb, k0, brow + column<MODE>(n));
+      rb.next(p.nb);
     }
   }
   return true;
 }
 
 // ================================================================ scales
-// Into shared memory: the scales of this CTA's rows of A and of all 256 rows of B, which
-// the pair's MMA wants whole in both CTAs.
+// Into shared memory: the scales of this CTA's rows of A, beside the first tile's, and of
+// all 256 rows of B, which the pair's MMA wants whole in both CTAs.
 template <int MODE>
 __device__ __forceinline__ bool scale_loads(SmemCtl& c, uint8_t* smem, const KParams& p,
-                                            const Tile& t, int& slot, uint32_t& phase) {
+                                            const Strip& t, Ring& slot) {
   const int nk = kstages<MODE>(p), R = MODE == FC1 ? p.F : p.H;
   const long long row = (long long)t.row0 + t.m0, np = scale_rows(p.N), r0 = row & ~1ll;
-  const uint32_t ba = t.rows <= 0 ? 0 : (((int)(row & 1) + t.rows + 1) & ~1) * 8;
+  const uint32_t rows = t.rows <= 0 ? 0 : (((int)(row & 1) + t.rows + 1) & ~1) * 8;
   const uint8_t* sa = (MODE == FC1 ? p.xs : p.hs) + r0 * 8;
-  // the edge of a matrix may cut its 128 (FC1: of both halves) or 256 rows short
-  const uint32_t bb = min(MODE == FC1 ? 128 : 256, R - t.n0) * 8;
-  const uint8_t* sb = (MODE == FC1 ? p.w1s : p.w2s) +
-                      ((size_t)(MODE == FC1 ? 2 * t.e : t.e) * nk * R + t.n0) * 8;
+  const uint8_t* sb = (MODE == FC1 ? p.w1s : p.w2s) + (size_t)(MODE == FC1 ? 2 * t.e : t.e) * nk * R * 8;
   const size_t up = (size_t)nk * R * 8;
   if (MODE == FC2) {
     if (!wait_expert(c, p, t.e)) return false;
     asm volatile("fence.proxy.async.global;" ::: "memory");
   }
-  for (int kt = 0; kt < nk; ++kt) {
-    if (!ptx::mbar_wait(&c.sc_empty[slot], phase ^ 1, &c.abort, kWaitLimitNs)) {
-      give_up(c, p.status, 66);
-      return false;
-    }
-    uint8_t* s = smem + kScAt + slot * kScBytes;
-    uint64_t* bar = &c.sc_full[slot];
-    ptx::mbar_arrive_expect_tx(bar, ba + (MODE == FC1 ? 2 : 1) * bb);
-    if (ba) bulk_load(s, sa + (size_t)kt * np * 8, ba, bar);
-    bulk_load(s + kScA, sb + (size_t)kt * R * 8, bb, bar);
-    if (MODE == FC1) bulk_load(s + kScA + 128 * 8, sb + up + (size_t)kt * R * 8, bb, bar);
-    if (++slot == kSc) {
-      slot = 0;
-      phase ^= 1;
+  for (int n = t.n0; n < t.n1; ++n) {
+    const int n0 = column<MODE>(n);
+    const uint32_t ba = n == t.n0 ? rows : 0;
+    // the edge of a matrix may cut its 128 (FC1: of both halves) or 256 rows short
+    const uint32_t bb = min(MODE == FC1 ? 128 : 256, R - n0) * 8;
+    for (int kt = 0; kt < nk; ++kt) {
+      if (!ptx::mbar_wait(&c.sc_empty[slot.at], slot.phase ^ 1, &c.abort, kWaitLimitNs)) {
+        give_up(c, p.status, 66);
+        return false;
+      }
+      uint8_t* s = smem + kScAt + slot.at * kScBytes;
+      uint64_t* bar = &c.sc_full[slot.at];
+      const uint8_t* b = sb + ((size_t)kt * R + n0) * 8;
+      ptx::mbar_arrive_expect_tx(bar, ba + (MODE == FC1 ? 2 : 1) * bb);
+      if (ba) bulk_load(s, sa + (size_t)kt * np * 8, ba, bar);
+      bulk_load(s + kScA, b, bb, bar);
+      if (MODE == FC1) bulk_load(s + kScA + 128 * 8, b + up, bb, bar);
+      slot.next(kSc);
     }
   }
   return true;
@@ -373,52 +411,56 @@ __device__ __forceinline__ void release(uint64_t* bar, uint32_t rank, int lane) 
 }
 
 struct ScaleState {
-  int slot = 0;
-  uint32_t phase = 0, group = 0;
+  Ring slot, a;
+  uint32_t group = 0;
 };
 // Into TMEM: row r of an operand is lane r % 32, column r / 32; a cell holds four scales,
-// half a stage's.
+// half a stage's. A's stay for the strip, as its rows do.
 template <int MODE>
-__device__ __forceinline__ bool scales_tile(SmemCtl& c, const uint8_t* smem, const KParams& p,
-                                            const Tile& t, uint32_t tmem, uint32_t rank,
-                                            ScaleState& m, int quarter, int lane) {
+__device__ __forceinline__ bool scales_strip(SmemCtl& c, const uint8_t* smem, const KParams& p,
+                                             const Strip& t, uint32_t tmem, uint32_t rank,
+                                             ScaleState& m, int quarter, int lane) {
   const int nk = kstages<MODE>(p);
   const int odd = (t.row0 + t.m0) & 1;
-  for (int kt = 0; kt < nk; ++kt, ++m.group) {
-    const int buf = m.group % kSf;
-    bool got = ptx::mbar_wait(&c.sc_full[m.slot], m.phase, &c.abort, kWaitLimitNs);
-    const uint8_t* s = smem + kScAt + m.slot * kScBytes;
-    uint32_t a0[4], a1[4], b0[8], b1[8];
+  const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+  for (int n = t.n0; n < t.n1; ++n) {
+    for (int kt = 0; kt < nk; ++kt, ++m.group) {
+      const int buf = m.group % kSf;
+      bool got = ptx::mbar_wait(&c.sc_full[m.slot.at], m.slot.phase, &c.abort, kWaitLimitNs);
+      const uint8_t* s = smem + kScAt + m.slot.at * kScBytes;
+      uint32_t a[8], b[16];  // the first half's cells, the second's
+      if (n == t.n0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint2 v = *reinterpret_cast<const uint2*>(s + (odd + 32 * i + lane) * 8);
-      a0[i] = v.x;
-      a1[i] = v.y;
-    }
+        for (int i = 0; i < 4; ++i) {
+          const uint2 v = *reinterpret_cast<const uint2*>(s + (odd + 32 * i + lane) * 8);
+          a[i] = v.x;
+          a[4 + i] = v.y;
+        }
+      }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint2 v = *reinterpret_cast<const uint2*>(s + kScA + (32 * i + lane) * 8);
-      b0[i] = v.x;
-      b1[i] = v.y;
-    }
-    got = got && ptx::mbar_wait(&c.sf_empty[buf], ((m.group / kSf) & 1) ^ 1, &c.abort, kWaitLimitNs);
-    if (!__all_sync(0xffffffffu, got)) {
-      if (lane == 0) give_up(c, p.status, 67);
-      return false;
-    }
-    __syncwarp();  // every lane has read the slot
-    if (lane == 0) ptx::mbar_arrive(&c.sc_empty[m.slot]);
-    ptx::tc_fence_after();  // the MMAs that read this buffer are done
-    const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + kTmemScales + buf * kSfCols;
-    tmem_st_x4(at, a0);
-    tmem_st_x8(at + 4, b0);
-    tmem_st_x4(at + 12, a1);
-    tmem_st_x8(at + 16, b1);
-    tmem_st_wait();
-    release(&c.sf_full[buf], rank, lane);
-    if (++m.slot == kSc) {
-      m.slot = 0;
-      m.phase ^= 1;
+      for (int i = 0; i < 8; ++i) {
+        const uint2 v = *reinterpret_cast<const uint2*>(s + kScA + (32 * i + lane) * 8);
+        b[i] = v.x;
+        b[8 + i] = v.y;
+      }
+      got = got && ptx::mbar_wait(&c.sf_empty[buf], ((m.group / kSf) & 1) ^ 1, &c.abort, kWaitLimitNs);
+      if (n == t.n0)
+        got = got && ptx::mbar_wait(&c.a_empty[m.a.at], m.a.phase ^ 1, &c.abort, kWaitLimitNs);
+      if (!__all_sync(0xffffffffu, got)) {
+        if (lane == 0) give_up(c, p.status, 67);
+        return false;
+      }
+      __syncwarp();  // every lane has read the slot
+      if (lane == 0) ptx::mbar_arrive(&c.sc_empty[m.slot.at]);
+      ptx::tc_fence_after();  // the MMAs that read these columns are done
+      if (n == t.n0) {
+        tmem_st_x8(lanes + kTmemA + 8 * m.a.at, a);
+        m.a.next(p.na);
+      }
+      tmem_st_x16(lanes + kTmemB + 16 * buf, b);
+      tmem_st_wait();
+      release(&c.sf_full[buf], rank, lane);
+      m.slot.next(kSc);
     }
   }
   return true;
@@ -426,49 +468,49 @@ __device__ __forceinline__ bool scales_tile(SmemCtl& c, const uint8_t* smem, con
 
 // ================================================================ MMA issuer
 struct MmaState {
-  int stage = 0;
-  uint32_t phase = 0, group = 0, tiles = 0;
+  Ring a, b;
+  uint32_t group = 0, tiles = 0;
 };
 template <int MODE>
-__device__ __forceinline__ bool mma_tile(SmemCtl& c, uint32_t smem, const KParams& p, uint32_t tmem,
-                                         MmaState& m) {
+__device__ __forceinline__ bool mma_strip(SmemCtl& c, uint32_t smem, const KParams& p, const Strip& t,
+                                          uint32_t tmem, MmaState& m) {
   constexpr uint32_t idesc = idesc_mxf4(2 * BM, BN);
   const uint64_t desc0 = ptx::sdesc_sw128(0, 16, 1024);
   const int K = kvalues<MODE>(p), nk = kstages<MODE>(p);
-  const int acc = m.tiles & 1;
   int where = 0;
-  // One lane waits and issues for the whole tile. Last it waits for the columns that this
+  // One lane waits and issues for the whole strip. Last it waits for the columns that an
   // accumulator shares with the previous tile's, which come free last.
   if (elect_one()) {
-    const uint32_t d = tmem + acc * kAccStep;
-    int stage = m.stage;
-    uint32_t phase = m.phase, group = m.group;
-    for (int kt = 0; kt < nk; ++kt, ++group) {
-      const int buf = group % kSf;
-      if (!ptx::mbar_wait(&c.sf_full[buf], (group / kSf) & 1, &c.abort, kWaitLimitNs)) where = 68;
-      else if (!ptx::mbar_wait(&c.full[stage], phase, &c.abort, kWaitLimitNs)) where = 69;
-      else if (kt == 0 &&
-               (!ptx::mbar_wait(&c.tmem_empty[acc], ((m.tiles >> 1) & 1) ^ 1, &c.abort, kWaitLimitNs) ||
-                (m.tiles > 0 && !ptx::mbar_wait(&c.ovl, (m.tiles - 1) & 1, &c.abort, kWaitLimitNs))))
-        where = 70;
-      if (where) break;
-      ptx::tc_fence_after();
-      const uint32_t sf = tmem + kTmemScales + buf * kSfCols;
-      const uint64_t ad = desc0 | ((smem + stage * kStageBytes) >> 4);
-      const uint64_t bd = ad + (kABytes >> 4);
+    MmaState s = m;
+    for (int n = t.n0; n < t.n1 && !where; ++n, ++s.tiles) {
+      const int acc = s.tiles & 1;
+      const uint32_t d = tmem + acc * kAccStep;
+      Ring a = m.a;  // the strip's rows, for every tile from the first stage on
+      for (int kt = 0; kt < nk; ++kt, ++s.group) {
+        const int buf = s.group % kSf;
+        if (!ptx::mbar_wait(&c.sf_full[buf], (s.group / kSf) & 1, &c.abort, kWaitLimitNs)) where = 68;
+        else if (!ptx::mbar_wait(&c.full[s.b.at], s.b.phase, &c.abort, kWaitLimitNs)) where = 69;
+        else if (kt == 0 &&
+                 (!ptx::mbar_wait(&c.tmem_empty[acc], ((s.tiles >> 1) & 1) ^ 1, &c.abort, kWaitLimitNs) ||
+                  (s.tiles > 0 && !ptx::mbar_wait(&c.ovl, (s.tiles - 1) & 1, &c.abort, kWaitLimitNs))))
+          where = 70;
+        if (where) break;
+        ptx::tc_fence_after();
+        const uint32_t sa = tmem + kTmemA + 8 * a.at, sb = tmem + kTmemB + 16 * buf;
+        const uint64_t ad = desc0 | ((smem + a.at * kSlotBytes) >> 4);
+        const uint64_t bd = desc0 | ((smem + (p.na + s.b.at) * kSlotBytes) >> 4);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {  // 64 K values each; past the edge there are none
-        if (kt * BK + kk * 64 >= K) break;
-        const uint32_t sa = sf + 12 * (kk >> 1);
-        umma_mxf4_pair(d, ad + kk * 2, bd + kk * 2, idesc | (kk & 1 ? kUpperPair : 0), sa, sa + 4,
-                       (kt | kk) != 0);
-      }
-      ptx::umma_commit_pair(&c.empty[stage], 3);
-      ptx::umma_commit_pair(&c.sf_empty[buf], 3);
-      if (kt == nk - 1) ptx::umma_commit_pair(&c.tmem_full[acc], 3);
-      if (++stage == kStages) {
-        stage = 0;
-        phase ^= 1;
+        for (int kk = 0; kk < 4; ++kk) {  // 64 K values each; past the edge there are none
+          if (kt * BK + kk * 64 >= K) break;
+          umma_mxf4_pair(d, ad + kk * 2, bd + kk * 2, idesc | (kk & 1 ? kUpperPair : 0),
+                         sa + 4 * (kk >> 1), sb + 8 * (kk >> 1), (kt | kk) != 0);
+        }
+        ptx::umma_commit_pair(&c.empty[s.b.at], 3);
+        ptx::umma_commit_pair(&c.sf_empty[buf], 3);
+        if (n == t.n1 - 1) ptx::umma_commit_pair(&c.a_empty[a.at], 3);
+        if (kt == nk - 1) ptx::umma_commit_pair(&c.tmem_full[acc], 3);
+        a.next(p.na);
+        s.b.next(p.nb);
       }
     }
   }
@@ -477,11 +519,15 @@ __device__ __forceinline__ bool mma_tile(SmemCtl& c, uint32_t smem, const KParam
     give_up(c, p.status, where);
     return false;
   }
-  m.group += nk;
-  const int at = m.stage + nk;
-  m.phase ^= (at / kStages) & 1;
-  m.stage = at % kStages;
-  ++m.tiles;
+  // where the issuing lane stands, for all
+  const int tiles = t.n1 - t.n0, steps = tiles * nk;
+  m.group += steps;
+  m.tiles += tiles;
+  const int b = m.b.at + steps, a = m.a.at + nk;
+  m.b.phase ^= (b / p.nb) & 1;
+  m.b.at = b % p.nb;
+  m.a.phase ^= (a / p.na) & 1;
+  m.a.at = a % p.na;
   return true;
 }
 
@@ -546,7 +592,7 @@ __device__ __forceinline__ void hand_over(SmemCtl& c, const KParams& p, uint32_t
 // soon as they are in registers.
 template <int MODE>
 __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, uint4* buf, const KParams& p,
-                                              const Maps& m, const Tile& t, uint32_t tmem,
+                                              const Maps& m, const Strip& t, int n0, uint32_t tmem,
                                               uint32_t rank, uint32_t& tiles, int ew, int lane) {
   const int q = ew & 3, hf = ew >> 2;
   const int acc = tiles & 1, rev = acc ^ 1;
@@ -567,7 +613,7 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, uint4* buf, const KPar
     // columns 0..127 gate, 128..255 up of one 128-wide block of h; this warp's 64 of each,
     // the shared ones (up on the first accumulator, gate on the second) first
     uint32_t s0[32], s1[32], o[32], codes[8], b[2];
-    const int f = t.n0 + 64 * hf;
+    const int f = n0 + 64 * hf;
     const bool ok = f < p.F;  // F is a multiple of 64
     const HOut ho = {out, m, p, row0};
     ptx::tmem_ld_32x32b_x32(tbase + 128 * rev, s0);
@@ -610,7 +656,7 @@ __device__ __forceinline__ bool epilogue_tile(SmemCtl& c, uint4* buf, const KPar
       for (int j = 0; j < 16; ++j)
         w[j] = pack_bf16x2(__uint_as_float(v[i & 1][2 * j]), __uint_as_float(v[i & 1][2 * j + 1]));
       if (i < 2) ptx::tmem_ld_32x32b_x32(tbase + 128 * (rev ^ 1) + 32 * i, v[i]);
-      if (t.n0 + col < p.H) store_box(out, &m.o3, w, p.o, row0, p.H, t.n0 + col);
+      if (n0 + col < p.H) store_box(out, &m.o3, w, p.o, row0, p.H, n0 + col);
     }
   }
   if (MODE == FC1) hand_over(c, p, tiles, lane);
@@ -644,33 +690,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = p.E;
   const uint32_t rank = ptx::cluster_ctarank();
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(&ctl.full[s], 1);
-      ptx::mbar_init(&ctl.empty[s], 1);
-    }
-    for (int s = 0; s < kSc; ++s) {
-      ptx::mbar_init(&ctl.sc_full[s], 1);
-      ptx::mbar_init(&ctl.sc_empty[s], 4);  // this CTA's scale warps
-    }
-    for (int b = 0; b < kSf; ++b) {
-      ptx::mbar_init(&ctl.sf_full[b], 8);  // both CTAs' scale warps
-      ptx::mbar_init(&ctl.sf_empty[b], 1);
-    }
-    for (int a = 0; a < 2; ++a) {
-      ptx::mbar_init(&ctl.hand_full[a], 1);
-      ptx::mbar_init(&ctl.hand_empty[a], readers(rank));
-      ptx::mbar_init(&ctl.mail_empty[a], 2);  // (the odd CTA's) both producers
-      ptx::mbar_init(&ctl.stored[a], 8);  // this CTA's epilogue warps
-      ptx::mbar_init(&ctl.counted[a], 1);
-      ptx::mbar_init(&ctl.tmem_full[a], 1);
-      ptx::mbar_init(&ctl.tmem_empty[a], 16);  // both CTAs' epilogue warps
-    }
-    for (int i = 0; i < 2 * kHalf; ++i) ptx::mbar_init(&ctl.mail_full[i], 1);
-    ptx::mbar_init(&ctl.ovl, 16);
-    ptx::mbar_init(&ctl.drain, 1);
-    ptx::mbar_init(&ctl.claim, 1);
-    ctl.abort = 0;
+  if (warp == 0) {  // a lane inits the barriers of its number
+    auto init = [&](uint64_t* b, int n, uint32_t count) {
+      if (lane < n) ptx::mbar_init(b + lane, count);
+    };
+    init(ctl.a_empty, kMaxA, 1);
+    init(ctl.full, kMaxB, 1);
+    init(ctl.empty, kMaxB, 1);
+    init(ctl.sc_full, kSc, 1);
+    init(ctl.sc_empty, kSc, 4);   // this CTA's scale warps
+    init(ctl.sf_full, kSf, 8);    // both CTAs' scale warps
+    init(ctl.sf_empty, kSf, 1);
+    init(ctl.tmem_full, 2, 1);
+    init(ctl.tmem_empty, 2, 16);  // both CTAs' epilogue warps
+    init(&ctl.ovl, 1, 16);
+    init(&ctl.drain, 1, 1);
+    init(ctl.mail_full, 2 * kHalf, 1);
+    init(ctl.mail_empty, 2, 2);   // (the odd CTA's) both producers
+    init(ctl.hand_full, 2, 1);
+    init(ctl.hand_empty, 2, readers(rank));
+    init(&ctl.claim, 1, 1);
+    init(ctl.stored, 2, 8);       // this CTA's epilogue warps
+    init(ctl.counted, 2, 1);
+    if (lane == 0) ctl.abort = 0;
     ptx::fence_mbar_init();
   }
   __syncthreads();
@@ -690,8 +732,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int e = threadIdx.x; e <= E; e += blockDim.x)
     ctl.off[e] = (int)min(max((long long)p.off[e], 0ll), p.N);
   __syncthreads();
-  if (warp < 2) {  // pair tiles per expert -> exclusive prefix, one warp for each GEMM
-    const int nt = warp == 0 ? ntiles<FC1>(p) : ntiles<FC2>(p);
+  if (warp < 2) {  // strips per expert -> exclusive prefix, one warp for each GEMM
+    const int nt = warp == 0 ? strips<FC1>(p) : strips<FC2>(p);
     int carry = 0;
     for (int base = 0; base < E; base += 32) {
       const int e = base + lane;
@@ -717,31 +759,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctl.tmem_base;
   const int total1 = ctl.tstart[0][E], total = total1 + ctl.tstart[1][E];
   int cur1 = 0, cur2 = 0;
-  auto tile1 = [&](int i) { return tile_at<FC1>(p, ctl, i, cur1, rank); };
-  auto tile2 = [&](int i) { return tile_at<FC2>(p, ctl, i - total1, cur2, rank); };
+  auto strip1 = [&](int i) { return strip_at<FC1>(p, ctl, i, cur1, rank); };
+  auto strip2 = [&](int i) { return strip_at<FC2>(p, ctl, i - total1, cur2, rank); };
   bool ok = true;
   if (warp < 4) {
     regs_dec<kRegsControl>();
     if (warp == 0 && lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
+      Ring ra, rb;
       for (uint32_t n = 0; ok; ++n) {
         const int i = mailed_tile(ctl, n, p.status);
         ok = i >= 0;
         if (!ok || i >= total) break;
         ok = i < total1
-                 ? producer_tile<FC1>(ctl, smem, p, &m.a1, &m.s1, &m.b1, tile1(i), rank, stage, phase)
-                 : producer_tile<FC2>(ctl, smem, p, &m.a2, &m.s2, &m.b2, tile2(i), rank, stage, phase);
+                 ? producer_strip<FC1>(ctl, smem, p, &m.a1, &m.s1, &m.b1, strip1(i), rank, ra, rb)
+                 : producer_strip<FC2>(ctl, smem, p, &m.a2, &m.s2, &m.b2, strip2(i), rank, ra, rb);
       }
-      if (!ok && rank == 0) drain_loads(ctl.full, kStages, stage, phase);  // both CTAs'
+      if (!ok && rank == 0) drain_loads(ctl.full, p.nb, rb.at, rb.phase);  // both CTAs'
     } else if (warp == 1 && rank == 0) {
       MmaState st;
       for (uint32_t n = 0; ok; ++n) {
         const int i = handed_tile(ctl, n, p.status, true);
         ok = i >= 0;
         if (!ok || i >= total) break;
-        ok = i < total1 ? mma_tile<FC1>(ctl, ptx::smem_u32(smem), p, tmem, st)
-                        : mma_tile<FC2>(ctl, ptx::smem_u32(smem), p, tmem, st);
+        ok = i < total1 ? mma_strip<FC1>(ctl, ptx::smem_u32(smem), p, strip1(i), tmem, st)
+                        : mma_strip<FC2>(ctl, ptx::smem_u32(smem), p, strip2(i), tmem, st);
       }
       // no MMA may still run when TMEM is released (the same lane is elected as above)
       __syncwarp();
@@ -758,19 +799,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int i = handed_tile(ctl, n, p.status, false);
         ok = i >= 0;
         if (!ok || i >= total) break;
-        if (i < total1) ok = count_tile(ctl, p, tile1(i).e, tiles);
+        if (i >= total1) continue;
+        const Strip t = strip1(i);
+        for (int j = t.n0; j < t.n1 && ok; ++j) ok = count_tile(ctl, p, t.e, tiles);
       }
     } else if (warp == 3 && lane == 0) {
-      int slot = 0;
-      uint32_t phase = 0;
+      Ring slot;
       for (uint32_t n = 0; ok; ++n) {
         const int i = handed_tile(ctl, n, p.status, false);
         ok = i >= 0;
         if (!ok || i >= total) break;
-        ok = i < total1 ? scale_loads<FC1>(ctl, smem, p, tile1(i), slot, phase)
-                        : scale_loads<FC2>(ctl, smem, p, tile2(i), slot, phase);
+        ok = i < total1 ? scale_loads<FC1>(ctl, smem, p, strip1(i), slot)
+                        : scale_loads<FC2>(ctl, smem, p, strip2(i), slot);
       }
-      if (!ok) drain_loads(ctl.sc_full, kSc, slot, phase);
+      if (!ok) drain_loads(ctl.sc_full, kSc, slot.at, slot.phase);
     }
     __syncwarp();
   } else if (warp < 12) {
@@ -782,8 +824,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int i = handed_tile(ctl, n, p.status, true);
       ok = i >= 0;
       if (!ok || i >= total) break;
-      ok = i < total1 ? epilogue_tile<FC1>(ctl, buf, p, m, tile1(i), tmem, rank, tiles, ew, lane)
-                      : epilogue_tile<FC2>(ctl, buf, p, m, tile2(i), tmem, rank, tiles, ew, lane);
+      const Strip t = i < total1 ? strip1(i) : strip2(i);
+      for (int j = t.n0; j < t.n1 && ok; ++j)
+        ok = i < total1
+                 ? epilogue_tile<FC1>(ctl, buf, p, m, t, column<FC1>(j), tmem, rank, tiles, ew, lane)
+                 : epilogue_tile<FC2>(ctl, buf, p, m, t, column<FC2>(j), tmem, rank, tiles, ew, lane);
     }
     // the buffers and the outputs must outlive the TMA stores
     if (lane == 0) ptx::bulk_wait_group0();
@@ -795,8 +840,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int i = handed_tile(ctl, n, p.status, true);
       ok = i >= 0;
       if (!ok || i >= total) break;
-      ok = i < total1 ? scales_tile<FC1>(ctl, smem, p, tile1(i), tmem, rank, st, warp - 12, lane)
-                      : scales_tile<FC2>(ctl, smem, p, tile2(i), tmem, rank, st, warp - 12, lane);
+      ok = i < total1 ? scales_strip<FC1>(ctl, smem, p, strip1(i), tmem, rank, st, warp - 12, lane)
+                      : scales_strip<FC2>(ctl, smem, p, strip2(i), tmem, rank, st, warp - 12, lane);
     }
   }
   ptx::tc_fence_before();
@@ -862,8 +907,14 @@ moe_status_t launch_ffn_fwd_fp4(const moe_layer_desc_t& d, const uint8_t* xq, co
       !make_rows_map(&m.o3, o, N, d.H, 32) || (a && !make_rows_map(&m.o1, a, N, 2 * d.F, 32)) ||
       (h && !make_rows_map(&m.o2, h, N, d.F, 32)))
     return MOE_ERR_CUDA;
-  const KParams p = {d.E, d.H, d.F, N, off, xs, w.w1s, w.w2s, a, h, o, hq, hs,
-                     status, dep, tile_counter(status)};
+  KParams p = {d.E, d.H, d.F, N, off, xs, w.w1s, w.w2s, a, h, o, hq, hs,
+               status, dep, tile_counter(status)};
+  // A's slots hold the longer product's rows where they can, half of all where not
+  const int stages = std::max(fp4_groups(d.H), fp4_groups(d.F));
+  p.na = stages <= kMaxA ? std::max(stages, kSlots - kMaxB) : kSlots / 2;
+  p.nb = kSlots - p.na;
+  // row tiles, if half of the experts end inside one
+  const long long rt = std::max<long long>(1, N / (2 * BM) + std::min<long long>(N, d.E) / 2);
   int pairs = 0;
   cudaError_t e = resident_pairs(&pairs);
   if (e == cudaSuccess) e = launch_zero_counters(dep, d.E, p.tile, st);
@@ -871,6 +922,9 @@ moe_status_t launch_ffn_fwd_fp4(const moe_layer_desc_t& d, const uint8_t* xq, co
     set_error("grouped_gemm_fp4_kernel set-up: %s", cudaGetErrorString(e));
     return MOE_ERR_CUDA;
   }
+  const int parts = (int)std::min<long long>(1 << 20, (kStripsAPair * pairs + rt - 1) / rt);
+  const int nt[2] = {ceil_div(d.F, 128), ceil_div(d.H, BN)}, nk[2] = {fp4_groups(d.H), fp4_groups(d.F)};
+  for (int g = 0; g < 2; ++g) p.strip[g] = nk[g] > p.na ? 1 : ceil_div(nt[g], parts);
   // one pair for every two SMs, and no more than there can be tiles
   const long long rows = N / (2 * BM) + std::min<long long>(N, d.E);
   pairs = (int)std::min<long long>(pairs, rows * (ceil_div(d.F, 128) + ceil_div(d.H, BN)));
