@@ -136,7 +136,15 @@ template <int MODE>
 __device__ __forceinline__ Strip strip_at(const KParams& p, const SmemCtl& c, int i, int& cursor,
                                           uint32_t rank) {
   const int* tstart = c.tstart[MODE];
-  while (tstart[cursor + 1] <= i) ++cursor;
+  if (tstart[cursor + 1] <= i) {
+    int lo = cursor + 1, hi = p.E - 1;  // the first expert that ends past i
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (tstart[mid + 1] <= i) lo = mid + 1;
+      else hi = mid;
+    }
+    cursor = lo;
+  }
   Strip t;
   t.e = cursor;
   t.row0 = c.off[cursor];
@@ -210,7 +218,6 @@ __device__ __forceinline__ bool wait_expert(SmemCtl& c, const KParams& p, int e)
   if (ld_acquire(p.dep + e) < target) {
     const uint64_t t0 = ptx::globaltimer_ns();
     while (ld_acquire(p.dep + e) < target) {
-      __nanosleep(64);
       if (*(volatile int*)&c.abort || ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
         give_up(c, p.status, 60);
         return false;
