@@ -101,6 +101,20 @@ cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sme
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// ---------------------------------------------------------------- tensor maps
+// Calls the driver's cuTensorMapEncodeTiled, `enc`. A host thread that has made no CUDA call yet
+// has no context, which that entry point needs and, unlike the runtime's, does not make:
+// the runtime then makes the device's primary one current.
+template <class Encode, class... Args>
+CUresult encode_map(Encode enc, Args... args) {
+  CUresult r = enc(args...);
+  int dev = 0;
+  if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess &&
+      cudaSetDevice(dev) == cudaSuccess)
+    r = enc(args...);
+  return r;
+}
+
 // ---------------------------------------------------------------- launchers
 moe_status_t launch_route(const moe_layer_desc_t& d, const bf16* x, const bf16* w_r,
                           const float* bias, float* logits, int32_t* idx, float* gates,

@@ -6,6 +6,8 @@ product differs from the oracle's by the fp32 summation alone, in any order: K 2
 (twice that where the order's partial sums are rounded by truncation: the bounds use 2 K 2^-24),
 plus half a bf16 step where it is stored as bf16. h = silu(g) u is fp32 with a sigmoid of
 relative error 7e-6 at most, and |silu'| <= 1.1."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -201,6 +203,7 @@ SHAPES = [  # T, H, E, k, F, skew
     (49, 64, 1, 1, 64, 0), (100, 320, 2, 1, 448, 0), (129, 192, 2, 2, 64, 0), (257, 256, 2, 2, 320, 1),
     (400, 512, 8, 4, 192, 1), (600, 64, 3, 2, 576, 1), (500, 576, 6, 3, 256, 2), (1000, 320, 16, 4, 448, 1),
     (255, 1344, 4, 2, 128, 1), (3000, 128, 4, 2, 128, 1), (64, 2048, 1, 1, 768, 0),
+    (300, 2304, 2, 1, 64, 0), (300, 64, 2, 1, 2304, 0), (290, 2624, 1, 1, 2112, 0), (70, 64, 1, 1, 2048, 0),
     (65, 64, 1, 1, 64, 0), (70, 2048, 1, 1, 768, 0), (140, 320, 2, 1, 448, 0), (128, 64, 2, 2, 192, 2),
 ]
 
@@ -308,9 +311,10 @@ def test_streams_and_captures(T, E, k, F):
     assert torch.equal(o, alone[0]) and moe.moe_device_status(d, ws) == moe.MOE_OK
 
 
-def test_many_tiles_a_pair():
-    """Fifty tiles and more for each CTA pair, experts of every size in turn."""
-    T, H, E, k, F = 24000, 128, 7, 3, 128
+@pytest.mark.parametrize("T,H,E,k,F", [(24000, 128, 7, 3, 128), (30000, 1088, 5, 2, 704)])
+def test_many_tiles_a_pair(T, H, E, k, F):
+    """Many tiles for each CTA pair (in strips of one, in strips of three), experts of every
+    size in turn."""
     d, f, off, off_np, a, h, o, ws = experts(T, H, E, k, F, 1, False)
     run(d, f, off, a, h, o, ws)
     assert moe.moe_device_status(d, ws) == moe.MOE_OK
@@ -437,3 +441,101 @@ def test_refuses_wrong_tensors():
                         (10, None, "None"), (11, o.float(), "float32")):
         with pytest.raises(moe.MoeError, match=why):
             moe.moe_expert_ffn_fwd_fp4(d, *[bad if j == i else t for j, t in enumerate(args)])
+
+
+@pytest.mark.parametrize("T,E,k", [(9, 16, 4), (700, 4, 2)])
+def test_layer_forward_captured(T, E, k):
+    """A captured serving forward, replayed on new inputs, with bf16 work of the same
+    workspace between the replays."""
+    H, F = 256, 192
+    d = moe.LayerDesc.of(T, H, E, k, F)
+    b = moe.LayerBuffers(d)
+    b.w_r.copy_(rnd(E, H, std=0.1, seed=2))
+    b.w1.copy_(rnd(E, 2 * F, H, std=0.1, seed=3))
+    b.w2.copy_(rnd(E, H, F, std=0.1, seed=4))
+    f = moe.Fp4Buffers(d)
+    f.quantize_weights(b.w1, b.w2)
+    want = []
+    for seed in (1, 2, 3):
+        b.x.copy_(rnd(T, H, seed=seed))
+        moe.moe_layer_forward_fp4(d, b, f)
+        want.append(b.y.clone())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.moe_layer_forward_fp4(d, b, f)
+    for seed, y in zip((1, 2, 3), want):
+        b.x.copy_(rnd(T, H, seed=seed))
+        moe.moe_layer_forward(d, b)
+        b.y.zero_()
+        g.replay()
+        assert torch.equal(b.y, y)
+    assert moe.moe_device_status(d, b.ws) == moe.MOE_OK
+
+
+def test_two_host_threads():
+    """Calls from two threads, each on its stream with its workspace, and each the first CUDA
+    call of its thread (the driver's map encoder wants a context, which the thread lacks)."""
+    sets = [experts(T, 256, 8, 2, 320, 1, False, seed=T) for T in (12, 900)]
+    want = []
+    for d, f, off, _, a, h, o, ws in sets:
+        run(d, f, off, a, h, o, ws)
+        want.append(o.clone())
+        o.fill_(3)
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(s, w):
+        try:
+            st = torch.cuda.Stream()
+            d, f, off, _, a, h, o, ws = s
+            for _ in range(50):
+                run(d, f, off, a, h, o, ws, st)
+            st.synchronize()
+            assert torch.equal(o, w) and moe.moe_device_status(d, ws, st) == moe.MOE_OK
+        except BaseException as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=p) for p in zip(sets, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+
+
+def test_first_call_of_a_thread_in_bf16():
+    """The same for the bf16 experts."""
+    T, E, k, H, F = 40, 4, 2, 128, 64
+    d = moe.LayerDesc.of(T, H, E, k, F)
+    b = moe.LayerBuffers(d)
+    b.x.copy_(rnd(T, H, seed=1)), b.w1.copy_(rnd(E, 2 * F, H, seed=2)), b.w2.copy_(rnd(E, H, F, seed=3))
+    moe.moe_layer_forward(d, b)
+    want, errors = b.o.clone(), []
+    b.o.zero_()
+    torch.cuda.synchronize()
+    raw = torch.cuda.current_stream().cuda_stream
+
+    def work():
+        try:
+            moe.moe_expert_ffn_fwd(d, b.x_perm, b.off, b.w1, b.w2, b.a, b.h, b.o, b.ws, raw)
+        except BaseException as e:  # noqa: BLE001
+            errors.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not errors and torch.equal(b.o, want), errors
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_seeded_shapes(seed):
+    """Random shapes over the whole range, on both sides of the few-rows rule."""
+    rng = np.random.default_rng(1000 + seed)
+    H, F = (64 * int(rng.integers(1, 20)) for _ in range(2))
+    E = int(rng.integers(1, 40))
+    k = int(rng.integers(1, min(E, 8) + 1))
+    T = int(np.exp(rng.uniform(0, np.log(1200))))
+    d, f, off, off_np, a, h, o, ws = experts(T, H, E, k, F, int(rng.integers(0, 3)), bool(seed & 1), seed=seed)
+    run(d, f, off, a, h, o, ws)
+    check(d, f, off_np, a, h, o, ws)
