@@ -63,13 +63,17 @@ struct Fp4Weights {
 moe_status_t launch_fp4_quantize_weights(const moe_layer_desc_t& d, const bf16* w1, const bf16* w2,
                                          uint8_t* w1q, uint8_t* w1s, uint8_t* w2q, uint8_t* w2s,
                                          bf16* w1v, bf16* w2v, cudaStream_t st);
+// dep, status: counters of the expert products that follow on the stream, which the launch
+// clears for them (the layer path: one launch less).
 moe_status_t launch_permute_fp4(const moe_layer_desc_t& d, const bf16* x, const int32_t* slot,
-                                uint8_t* xq, uint8_t* xs, cudaStream_t st);
-// Expert FFN forward: a and h (bf16) are written when given.
+                                uint8_t* xq, uint8_t* xs, cudaStream_t st, int* dep = nullptr,
+                                int* status = nullptr);
+// Expert FFN forward: a and h (bf16) are written when given. counters_zeroed: the launch
+// before it on the stream has cleared its counters.
 moe_status_t launch_ffn_fwd_fp4(const moe_layer_desc_t& d, const uint8_t* xq, const uint8_t* xs,
                                 const int32_t* off, const Fp4Weights& w, bf16* a, bf16* h,
                                 uint8_t* hq, uint8_t* hs, bf16* o, int* status, int* dep,
-                                cudaStream_t st);
+                                cudaStream_t st, bool counters_zeroed = false);
 // The forward for few rows an expert (rows_fp4.cu), which launch_ffn_fwd_fp4 takes up to
 // kFp4FewRows rows an expert on average. Measured, this kernel against the GEMMs, us,
 // nothing kept:
@@ -86,6 +90,6 @@ constexpr long long kFp4FewRows = 64;
 moe_status_t launch_ffn_rows_fp4(const moe_layer_desc_t& d, const uint8_t* xq, const uint8_t* xs,
                                  const int32_t* off, const Fp4Weights& w, bf16* a, bf16* h,
                                  uint8_t* hq, uint8_t* hs, bf16* o, int* status, int* dep,
-                                 cudaStream_t st);
+                                 cudaStream_t st, bool counters_zeroed);
 
 }  // namespace moe

@@ -94,10 +94,12 @@ moe_status_t moe_layer_forward_fp4(const moe_layer_desc_t* d, const moe_mb_bufs_
                             b->rank_off, reinterpret_cast<int*>(ws + w.hist), status_of(b->ws),
                             st));
   }
-  MOE_CHECK(launch_permute_fp4(*d, BF(b->x), b->slot, q->xq, q->xs, st));
+  MOE_CHECK(launch_permute_fp4(*d, BF(b->x), b->slot, q->xq, q->xs, st, dep_of(*d, b->ws),
+                               status_of(b->ws)));
   MOE_CHECK(launch_ffn_fwd_fp4(*d, q->xq, q->xs, b->off, Fp4Weights{q->w1q, q->w1s, q->w2q, q->w2s},
                                save ? BFW(b->a) : nullptr, save ? BFW(b->h) : nullptr, q->hq, q->hs,
-                               BFW(b->o), status_of(b->ws), dep_of(*d, b->ws), st));
+                               BFW(b->o), status_of(b->ws), dep_of(*d, b->ws), st,
+                               /*counters_zeroed=*/true));
   return op_combine_mb(*d, b, st);
 }
 

@@ -118,8 +118,13 @@ __global__ void __launch_bounds__(256) permute_fp4_kernel(const bf16* __restrict
                                                           const int32_t* __restrict__ slot,
                                                           uint8_t* __restrict__ xq,
                                                           uint8_t* __restrict__ xs, int T, int H,
-                                                          int k, long long N, int nseg) {
+                                                          int k, long long N, int nseg, int* dep,
+                                                          int ndep, int* tile) {
   pdl_wait();
+  if (dep && blockIdx.x == 0) {
+    if ((int)threadIdx.x < ndep) dep[threadIdx.x] = 0;
+    if (threadIdx.x == 0) *tile = 0;
+  }
   const int lane = threadIdx.x & 31;
   const long long warps = (long long)gridDim.x * (blockDim.x >> 5);
   const long long tasks = (long long)T * nseg, np = fp4::scale_rows(N);
@@ -180,7 +185,7 @@ moe_status_t launch_fp4_quantize_weights(const moe_layer_desc_t& d, const bf16* 
 }
 
 moe_status_t launch_permute_fp4(const moe_layer_desc_t& d, const bf16* x, const int32_t* slot,
-                                uint8_t* xq, uint8_t* xs, cudaStream_t st) {
+                                uint8_t* xq, uint8_t* xs, cudaStream_t st, int* dep, int* status) {
   const long long N = (long long)d.T * d.k;
   if (N == 0) return MOE_OK;
   const int nseg = ceil_div(d.H, 1024);
@@ -189,7 +194,8 @@ moe_status_t launch_permute_fp4(const moe_layer_desc_t& d, const bf16* x, const 
   cudaError_t e;
   {
     LaunchScope _ls(K_FP4_PERMUTE, st);
-    e = launch_k(permute_fp4_kernel, grid, 256, 0, st, x, slot, xq, xs, d.T, d.H, d.k, N, nseg);
+    e = launch_k(permute_fp4_kernel, grid, 256, 0, st, x, slot, xq, xs, d.T, d.H, d.k, N, nseg, dep,
+                 dep ? d.E : 0, dep ? fp8::tile_counter(status) : nullptr);
   }
   return launched(e, "permute_fp4_kernel");
 }

@@ -899,11 +899,12 @@ cudaError_t resident_pairs(int* pairs) {
 moe_status_t launch_ffn_fwd_fp4(const moe_layer_desc_t& d, const uint8_t* xq, const uint8_t* xs,
                                 const int32_t* off, const Fp4Weights& w, bf16* a, bf16* h,
                                 uint8_t* hq, uint8_t* hs, bf16* o, int* status, int* dep,
-                                cudaStream_t st) {
+                                cudaStream_t st, bool counters_zeroed) {
   const long long N = (long long)d.T * d.k;
   if (N == 0) return MOE_OK;
   if (N <= kFp4FewRows * d.E)
-    return launch_ffn_rows_fp4(d, xq, xs, off, w, a, h, hq, hs, o, status, dep, st);
+    return launch_ffn_rows_fp4(d, xq, xs, off, w, a, h, hq, hs, o, status, dep, st,
+                               counters_zeroed);
   Maps m = {};
   if (!make_map(&m.a1, xq, 2, d.H / 2, N, 1, BM, 1) ||
       !make_map(&m.s1, xq, 2, d.H / 2, N, 1, kABoxRows, 1) ||
@@ -924,7 +925,7 @@ moe_status_t launch_ffn_fwd_fp4(const moe_layer_desc_t& d, const uint8_t* xq, co
   const long long rt = std::max<long long>(1, N / (2 * BM) + std::min<long long>(N, d.E) / 2);
   int pairs = 0;
   cudaError_t e = resident_pairs(&pairs);
-  if (e == cudaSuccess) e = launch_zero_counters(dep, d.E, p.tile, st);
+  if (e == cudaSuccess && !counters_zeroed) e = launch_zero_counters(dep, d.E, p.tile, st);
   if (e != cudaSuccess) {
     set_error("grouped_gemm_fp4_kernel set-up: %s", cudaGetErrorString(e));
     return MOE_ERR_CUDA;

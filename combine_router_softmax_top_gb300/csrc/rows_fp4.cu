@@ -47,7 +47,7 @@ constexpr int kSf = 4, kSfCols = 24;
 constexpr int kTmemCols = 256;
 constexpr int kSmallBox = 8;                  // rows of the small TMA box
 static_assert(kTmemScales + kSf * kSfCols <= kTmemCols, "TMEM columns");
-static_assert(kFp4FewRows * kMaxE < 65536, "16-bit tables");
+static_assert(kFp4FewRows * kMaxE < 65536, "16-bit offsets");
 constexpr size_t kDynSmem = (size_t)kStages * kStageBytes + 1024;
 
 // The tile's h between the epilogue's two views: a thread writes its column of every row,
@@ -82,7 +82,7 @@ struct SmemCtl {
   int claimed[2];
   uint32_t tmem_base;
   int abort;
-  uint16_t rtile[kMaxE + 1];      // first row tile of each expert
+  int rtile[kMaxE + 1];           // first row tile of each expert
   uint16_t off[kMaxE + 1];
   alignas(16) float h[NT * kHRow];  // read 16 bytes at a time
 };
@@ -505,9 +505,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int k = 0; k < kMaxE / 32; ++k) {
       const int e = lane * (kMaxE / 32) + k;
-      if (e < p.E) ctl.rtile[e] = (uint16_t)(incl - sum + n[k]);
+      if (e < p.E) ctl.rtile[e] = incl - sum + n[k];
     }
-    if (lane == 31) ctl.rtile[p.E] = (uint16_t)incl;
+    if (lane == 31) ctl.rtile[p.E] = incl;
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -603,7 +603,7 @@ cudaError_t set_up() {
 moe_status_t launch_ffn_rows_fp4(const moe_layer_desc_t& d, const uint8_t* xq, const uint8_t* xs,
                                  const int32_t* off, const Fp4Weights& w, bf16* a, bf16* h,
                                  uint8_t* hq, uint8_t* hs, bf16* o, int* status, int* dep,
-                                 cudaStream_t st) {
+                                 cudaStream_t st, bool counters_zeroed) {
   const long long N = (long long)d.T * d.k;
   CUtensorMap m[6];
   if (!make_map(&m[0], w.w1q, 2, d.H / 2, 2ll * d.E * d.F, 1, 128, 1) ||
@@ -616,7 +616,7 @@ moe_status_t launch_ffn_rows_fp4(const moe_layer_desc_t& d, const uint8_t* xq, c
   const RowsParams p = {d.E, d.H, d.F, N, off, xs, w, a, h, hq, hs, o, status, dep,
                         tile_counter(status)};
   cudaError_t e = set_up();
-  if (e == cudaSuccess) e = launch_zero_counters(dep, d.E, p.tile, st);
+  if (e == cudaSuccess && !counters_zeroed) e = launch_zero_counters(dep, d.E, p.tile, st);
   // one CTA per SM, fewer when there cannot be as many tiles
   const long long rows = N / NT + std::min<long long>(N, d.E);
   const long long tiles = rows * (ceil_div(d.F, 128) + ceil_div(d.H, 256));
