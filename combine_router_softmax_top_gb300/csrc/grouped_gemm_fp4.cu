@@ -7,25 +7,35 @@
 // The tensor cores apply both scales (tcgen05.mma kind::mxf4, 64 K values an
 // instruction, two scales a row). One persistent launch for both products, a CTA pair
 // (cta_group::2, M = 256, N = 256) per two SMs, as in grouped_gemm_fp8.cu:
-//   warp 0      TMA producer of the operand ring: this CTA's 128 rows of A and its half
-//               of B, 256 K values (128 bytes), 32 KB a stage, 6 stages
+//   warp 0      TMA producer: this CTA's 128 rows of A, once for a strip of tiles beside each
+//               other, and its half of B, 256 K values (128 bytes) a stage. Twelve slots of 16
+//               KB: as many for A as the longer product has stages (up to 8), the others B's
 //   warp 1      TMEM allocator + (even CTA) MMA issuer; (odd CTA) claims tiles
 //   warp 2      counts FC1 tiles for their experts
 //   warp 3      producer of the scales' ring: contiguous copies of the rows' and the weights'
 //               scale bytes, 3 KB a stage, 4 stages
-//   warps 12..15 scales: shared memory -> TMEM (tcgen05.st), ahead of the MMAs. A stage's
-//               scales are 24 columns: eight times the 8-bit kernels' for as many clocks of
-//               the tensor pipe.
+//   warps 12..15 scales: shared memory -> TMEM (tcgen05.st), ahead of the MMAs: for each stage
+//               16 columns of B's, and in a strip's first tile 8 of A's, which stay
 //   warps 4..11 epilogue: TMEM -> registers -> SwiGLU, block scales, e2m1 -> global; two
 //               warps per TMEM lane quarter, each owning 64 of every 128 columns. A block of
 //               h (32 columns) lies in one thread.
-// FC2 tiles wait for their expert's FC1 tiles through per-expert counters. Tiles are
+// FC2 tiles wait for their expert's FC1 tiles through per-expert counters. Strips are
 // claimed in order from a counter, FC1's first, so a wait is always for a tile that a
 // running pair holds.
 //
-// TMEM: two 256-column accumulators that share 128 (columns 0..255 and 128..383) and
-// five buffers of 24 scale columns. The epilogue reads the shared columns first and
-// releases them (ovl), so the next tile's MMAs start while it works on the rest.
+// TMEM: two 256-column accumulators that share 128 (columns 0..255 and 128..383), the
+// scales of A's slots and four buffers of B's. The epilogue reads the shared columns first
+// and releases them (ovl), so the next tile's MMAs start while it works on the rest.
+//
+// What bounds it. 64 experts of H 2048, F 1408 at 8192 tokens, top 8, skewed, nothing kept: 1134
+// GFLOP in 244 us, 4.6 PFLOP/s, at 1330 W and 2070 MHz (the limit is 1400 W; before the
+// strips 272 us at 2032 to 2062 MHz with the power cap active). A stage's four MMAs alone take
+// some 600 clocks (512 at the tensor pipe's nominal rate), and what shares shared memory or
+// TMEM with them adds its time: B's loads 95 clocks, scales 70, the epilogue's
+// TMEM reads and boxes 190 (each found by leaving it out). A's loads were 85 more, hence the
+// strips; tiles of N = 192, which would need no shared columns, take as long as N = 256. 128
+// experts of F 768 at 4096 tokens, balanced, a and h kept: 621 MB of DRAM traffic in 114 us, 5.4
+// TB/s, 0.81 of a copy's rate: 8 us of set-up and last tiles, then 5.9.
 //
 // Ragged groups: expert e owns rows off[e]..off[e+1]-1; a tile's rows past the
 // expert's end are computed on whatever was loaded and not stored (rows do not mix).

@@ -10,6 +10,14 @@
 // squares and the one that scales, so it is read once. Sums are fp32: a thread's
 // columns in order, then the threads in a fixed tree, so results do not change
 // from call to call.
+//
+// Rows of 2048: 4096 with their sum 67 MB in 13.3 us (a library copy of as many bytes takes 14.2:
+// at this size launch and ramps count), 32768 with 8-bit rows 604 MB in 93 us, 6.5 TB/s, 0.97 of
+// a copy's rate; one row 3.0 us, the call itself. Gradient of 4096 rows: 67 MB in 14.4 us, and 2.7
+// us for dw's sum over blocks, which reads their 456 partial rows in a fixed order. (Each
+// thread's columns of the next rows on their way into shared memory by cp.async, 5 rows in three
+// blocks of 128 threads, to 8 in two: 20 to 25 us against 17.3; too few warps for a row's chain of
+// latencies.)
 #include <algorithm>
 #include <math.h>
 
