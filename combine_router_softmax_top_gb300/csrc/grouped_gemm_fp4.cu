@@ -251,7 +251,7 @@ __device__ __forceinline__ void arrive_remote(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
                : "memory");
 }
-// The producer: the n-th tile of this pair (past the last: none is left; -1: gave up).
+// The producer: the n-th tile of this pair (at or past the total: none is left; -1: gave up).
 __device__ __forceinline__ int mailed_tile(SmemCtl& c, uint32_t n, int* status) {
   const int slot = n % (2 * kHalf);
   const uint32_t round = n / (2 * kHalf);
@@ -283,9 +283,17 @@ __device__ __forceinline__ int handed_tile(SmemCtl& c, uint32_t n, int* status, 
   if (!warp || (threadIdx.x & 31) == 0) ptx::mbar_arrive(&c.hand_empty[n & 1]);
   return i;
 }
-// Claims tiles for the pair until none is left (one thread of the odd CTA).
+__device__ __forceinline__ void mail_tile(SmemCtl& c, int slot, int i) {
+  c.mail[slot] = i;
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(ptx::mapa_shared(&c.mail[slot], 0)), "r"(i)
+               : "memory");
+  ptx::mbar_arrive_cluster(ptx::mapa_shared(&c.mail_full[slot], 0));
+  ptx::mbar_arrive_cluster(ptx::mapa_shared(&c.mail_full[slot], 1));
+}
+// Claims tiles for the pair until none is left (one thread of the odd CTA): those after the
+// first, which has been mailed while the tables were made.
 __device__ __forceinline__ void claim_tiles(SmemCtl& c, const KParams& p, int first, int total) {
-  for (uint32_t n = 0;; ++n) {
+  for (uint32_t n = 1; first < total; ++n) {
     const int slot = n % (2 * kHalf);
     const uint32_t round = n / (2 * kHalf);
     if ((n == 1 && !ptx::mbar_wait(&c.claim, 0, &c.abort, kWaitLimitNs)) ||
@@ -295,14 +303,9 @@ __device__ __forceinline__ void claim_tiles(SmemCtl& c, const KParams& p, int fi
       give_up(c, p.status, 64);
       return;
     }
-    const int i = min(n > 0 ? atomicAdd(p.tile, 1) : first, total);
-    c.mail[slot] = i;
-    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(ptx::mapa_shared(&c.mail[slot], 0)),
-                 "r"(i)
-                 : "memory");
-    ptx::mbar_arrive_cluster(ptx::mapa_shared(&c.mail_full[slot], 0));
-    ptx::mbar_arrive_cluster(ptx::mapa_shared(&c.mail_full[slot], 1));
-    if (i == total) return;
+    const int i = atomicAdd(p.tile, 1);
+    mail_tile(c, slot, i);
+    if (i >= total) return;
   }
 }
 
@@ -744,7 +747,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   int first = 0;  // the first tile, claimed while the tables are made
-  if (warp == 1 && lane == 0 && rank == 1) first = atomicAdd(p.tile, 1);
+  if (warp == 1 && lane == 0 && rank == 1) {
+    first = atomicAdd(p.tile, 1);
+    mail_tile(ctl, 0, first);
+  }
   // offsets outside 0..N would send stores out of the buffers
   for (int e = threadIdx.x; e <= E; e += blockDim.x)
     ctl.off[e] = (int)min(max((long long)p.off[e], 0ll), p.N);

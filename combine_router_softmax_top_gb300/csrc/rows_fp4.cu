@@ -151,7 +151,7 @@ __device__ __forceinline__ bool wait_expert(SmemCtl& c, const RowsParams& p, int
   return true;
 }
 
-// The n-th tile claimed for this CTA (past the last: none is left; -1: gave up), for the
+// The n-th tile claimed for this CTA (at or past the total: none is left; -1: gave up), for the
 // 10 warps that read it: producer, MMA issuer, scales, epilogue. A reader's arrival
 // (release) comes after its read, the slot is overwritten after all of them.
 constexpr int kReaders = 10;
@@ -167,17 +167,21 @@ __device__ __forceinline__ int claimed_tile(SmemCtl& c, uint32_t n, int* status,
   if (!warp || (threadIdx.x & 31) == 0) ptx::mbar_arrive(&c.claim_empty[n & 1]);
   return i;
 }
+__device__ __forceinline__ void publish(SmemCtl& c, uint32_t n, int i) {
+  *(volatile int*)&c.claimed[n & 1] = i;
+  ptx::mbar_arrive(&c.claim_full[n & 1]);
+}
+// The tiles after the first, which has been published while the tables were made.
 __device__ __forceinline__ void claim_tiles(SmemCtl& c, const RowsParams& p, int first, int total) {
-  for (uint32_t n = 0;; ++n) {
+  for (uint32_t n = 1; first < total; ++n) {
     if ((n == 1 && !ptx::mbar_wait(&c.claim, 0, &c.abort, kWaitLimitNs)) ||
         !ptx::mbar_wait(&c.claim_empty[n & 1], ((n >> 1) & 1) ^ 1, &c.abort, kWaitLimitNs)) {
       give_up(c, p.status, 42);
       return;
     }
-    const int i = min(n > 0 ? atomicAdd(p.tile, 1) : first, total);
-    *(volatile int*)&c.claimed[n & 1] = i;
-    ptx::mbar_arrive(&c.claim_full[n & 1]);
-    if (i == total) return;
+    const int i = atomicAdd(p.tile, 1);
+    publish(c, n, i);
+    if (i >= total) return;
   }
 }
 
@@ -495,7 +499,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   int first = 0;  // the first tile, claimed while the tables are made
-  if (warp == 2 && lane == 0) first = atomicAdd(p.tile, 1);
+  if (warp == 2 && lane == 0) {
+    first = atomicAdd(p.tile, 1);
+    publish(ctl, 0, first);
+  }
   // offsets outside 0..N would send stores out of the buffers
   for (int e = threadIdx.x; e <= p.E; e += blockDim.x)
     ctl.off[e] = (uint16_t)min(max((long long)p.off[e], 0ll), p.N);
