@@ -11,9 +11,9 @@
 // columns in order, then the threads in a fixed tree, so results do not change
 // from call to call.
 //
-// Rows of 2048: 4096 with their sum 67 MB in 13.3 us (a library copy of as many bytes takes 14.2:
-// at this size launch and ramps count), 32768 with 8-bit rows 604 MB in 93 us, 6.5 TB/s, 0.97 of
-// a copy's rate; one row 3.0 us, the call itself. Gradient of 4096 rows: 67 MB in 14.4 us, and 2.7
+// Rows of 2048: 4096 with their sum 67 MB in 11.8 us (a library copy of as many bytes takes 14.2:
+// at this size launch and ramps count), 32768 with 8-bit rows 604 MB in 88 us, 6.9 TB/s, a
+// copy's rate; one row 3.0 us, the call itself. Gradient of 4096 rows: 67 MB in 14.4 us, and 2.7
 // us for dw's sum over blocks, which reads their 456 partial rows in a fixed order. (Each
 // thread's columns of the next rows on their way into shared memory by cp.async, 5 rows in three
 // blocks of 128 threads, to 8 in two: 20 to 25 us against 17.3; too few warps for a row's chain of
@@ -69,6 +69,7 @@ struct NormParams {
   int T, H, tpr;
 };
 
+// BLOCKS: resident on an SM at least, 0 for no limit on registers
 template <int V, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) rms_norm_kernel(const NormParams p) {
   extern __shared__ uint32_t s_words[];  // scale words of the block's rows
@@ -90,14 +91,11 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rms_norm_kernel(const NormPar
     if (p.res)
       q[i] = ok ? reinterpret_cast<const uint4*>(p.res + at)[c] : make_uint4(0, 0, 0, 0);
   }
-  uint4 wv[V];  // ahead of the sum where latency counts (registers are short with V = 8)
-  auto weight = [&](int i) {
-    const int c = sub + i * p.tpr;
-    return c < cpr ? __ldg(reinterpret_cast<const uint4*>(p.w) + c) : make_uint4(0, 0, 0, 0);
-  };
-  if (V == 2) {
+  uint4 wv[V];  // (on its way beside the row)
 #pragma unroll
-    for (int i = 0; i < V; ++i) wv[i] = weight(i);
+  for (int i = 0; i < V; ++i) {
+    const int c = sub + i * p.tpr;
+    wv[i] = c < cpr ? __ldg(reinterpret_cast<const uint4*>(p.w) + c) : make_uint4(0, 0, 0, 0);
   }
   float ss = 0.f;
 #pragma unroll
@@ -124,7 +122,6 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rms_norm_kernel(const NormPar
   for (int i = 0; i < V; ++i) {
     const int c = sub + i * p.tpr;
     const bool ok = t < p.T && c < cpr;
-    if (V != 2) wv[i] = weight(i);
     const uint32_t* wp = reinterpret_cast<const uint32_t*>(&wv[i]);
     uint32_t* a = reinterpret_cast<uint32_t*>(&v[i]);
 #pragma unroll
@@ -300,24 +297,24 @@ moe_status_t launch_rms_norm(const moe_layer_desc_t& d, const bf16* x, const bf1
                              float eps, bf16* r, bf16* y, uint8_t* yq, uint8_t* ys, float* rstd,
                              cudaStream_t st) {
   if (d.T == 0) return MOE_OK;
-  const bool few = d.T <= device_sm_count() * 4;
-  const int vecs = few ? 2 : 8;
+  // Two groups of 8 columns a thread, four in rows of more than 2048, unless every row has an SM.
+  // us with 8-bit rows, two against four against eight groups:
+  //   rows                     608             4096            32768
+  //   H 320                2.8  3.1  4.2   3.2  3.6  5.3    20   19   30
+  //   H 2048               2.9  3.7  5.3  13.4 15.0 15.0    88   90   93
+  //   H 4096               4.0  4.3  6.1  26.5 24.7 28.6   190  173  178
+  //   H 16384               22   17   21   120   91   96
+  // and blocks of 128 threads, or one row: of 32, H 320 4.4 and 20.5, of 256 3.5 and 21.5.
+  const int vecs = d.H > 2048 && d.T > device_sm_count() ? 4 : 2;
   NormParams p = {x, res, w, eps, r, y, yq, reinterpret_cast<uint32_t*>(ys), rstd, d.T, d.H,
                   row_threads(d.H, vecs)};
-  // many rows: small blocks of a few rows each, dealt by the hardware (prompts of 32768 x
-  // 2048: 94 us; 256 threads a block 97, a resident wave of blocks that loop 97)
-  const int threads = std::max(p.tpr, few ? 32 : 64);
-  const int rows = threads / p.tpr, grid = ceil_div(d.T, rows);
+  const int threads = std::max(p.tpr, 128), rows = threads / p.tpr, grid = ceil_div(d.T, rows);
   const size_t smem = yq ? (size_t)rows * ceil_div(d.H, 512) * 4 : 0;
   cudaError_t e;
   {
     LaunchScope _ls(K_NORM, st);
-#define GO(...) launch_k(rms_norm_kernel<__VA_ARGS__>, grid, threads, smem, st, p)
-    // rows that 28 warps an SM hold at once: 72 registers a thread instead of 80 (4096 x 2048:
-    // 13.2 against 14.6 us; 32768 rows 94.9 against 92.9)
-    const bool wave = (long long)d.T * p.tpr <= (long long)device_sm_count() * 28 * 32;
-    e = few ? GO(2, 1024, 1) : p.tpr > 64 ? GO(8, 256, 1) : wave ? GO(8, 64, 14) : GO(8, 64, 1);
-#undef GO
+    e = vecs == 2 ? launch_k(rms_norm_kernel<2, 1024, 0>, grid, threads, smem, st, p)
+                  : launch_k(rms_norm_kernel<4, 512, 2>, grid, threads, smem, st, p);
   }
   return launched(e, "rms_norm_kernel");
 }
