@@ -13,10 +13,10 @@
 //
 // Rows of 2048: 4096 with their sum 67 MB in 11.8 us (a library copy of as many bytes takes 14.2:
 // at this size launch and ramps count), 32768 with 8-bit rows 604 MB in 88 us, 6.9 TB/s, a
-// copy's rate; one row 3.0 us, the call itself. Gradient of 4096 rows: 67 MB in 14.4 us, and 2.7
+// copy's rate; one row 3.0 us, the call itself. Gradient of 4096 rows: 67 MB in 13.9 us, and 2.7
 // us for dw's sum over blocks, which reads their 456 partial rows in a fixed order. (Each
 // thread's columns of the next rows on their way into shared memory by cp.async, 5 rows in three
-// blocks of 128 threads, to 8 in two: 20 to 25 us against 17.3; too few warps for a row's chain of
+// blocks of 128 threads, to 8 in two: 20 to 25 us against 17.2; too few warps for a row's chain of
 // latencies.)
 #include <algorithm>
 #include <math.h>
@@ -38,8 +38,11 @@ int row_threads(int H, int vecs) {
 }
 
 // Sum over the threads of a row; s_part: a word for each warp of the block. Rows of
-// more than a warp meet at a barrier of the whole block (all its rows do); two
-// calls in a row need different s_part.
+// more than a warp meet at a barrier, of the whole block (all its rows do) or, with OWN, of the
+// row alone: a block's rows then drift apart, and one's loads run beside another's arithmetic
+// (norm_grad_layer 17.2 -> 16.6 us), but a block takes all sixteen of its barriers, which leaves an
+// SM four blocks. Two calls in a row need different s_part.
+template <bool OWN>
 __device__ __forceinline__ float row_sum(float v, int tpr, float* s_part) {
   const int width = tpr < 32 ? tpr : 32;
 #pragma unroll
@@ -47,7 +50,8 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float* s_part) {
     if (o < width) v += __shfl_xor_sync(0xffffffffu, v, o);
   if (tpr <= 32) return v;
   if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = v;
-  __syncthreads();
+  if (OWN) asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / tpr), "r"(tpr) : "memory");
+  else __syncthreads();
   const int first = threadIdx.x / tpr * (tpr / 32);
   v = s_part[first];
   for (int w = 1; w < tpr / 32; ++w) v += s_part[first + w];
@@ -115,7 +119,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rms_norm_kernel(const NormPar
       ss = fmaf(bf16_hi(a[j]), bf16_hi(a[j]), ss);
     }
   }
-  ss = row_sum(ss, p.tpr, s_part);
+  ss = row_sum<false>(ss, p.tpr, s_part);
   const float rs = 1.f / sqrtf(ss / (float)p.H + p.eps);
   if (p.rstd && sub == 0 && t < p.T) p.rstd[t] = rs;
 #pragma unroll
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rms_norm_bwd_kernel(const Nor
         dot = fmaf(p1, bf16_hi(wp[j]), dot);
       }
     }
-    const float mean = row_sum(dot, p.tpr, s_part[buf]) * inv_h;
+    const float mean = row_sum<true>(dot, p.tpr, s_part[buf]) * inv_h;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = sub + i * p.tpr;
