@@ -83,7 +83,9 @@ constexpr int kMaxE = 256;
 constexpr int kEpiAt = kSlots * kSlotBytes, kScAt = kEpiAt + kEpiBytes;
 constexpr size_t kDynSmem = kScAt + kSc * kScBytes + 1024;
 constexpr int kHalf = 8;  // slots of half a mailbox (below)
-// strips (below) that a pair should get of each product, if they can be as many
+// strips (below) that a pair should get of each product, if they can be as many. Prefill and
+// train, us a pass, for 1, 3, 4, 6, 8, 16 and strips of one tile: 272, 272, 268, 268, 276, 283,
+// 347 and 137, 132, 131.5, 131, 129, 132, 140 (fewer reuse the rows more, more deal better).
 constexpr int kStripsAPair = 6;
 
 struct Maps {

@@ -22,7 +22,7 @@
 // it reads, 0.9 of a copy's rate; 6.1 TB/s while its CTAs are active, the launches before and the
 // last tiles are the rest. An MMA takes the tensor pipe some 130 clocks however small its N (the
 // 8-bit ones 55), so a stage's eight are 1040 clocks, and its 37 KB arrive in 1700: with 32
-// rows an expert the call still takes 59 us. One token: 12.7 us for 20 MB, a chain of latencies
+// rows an expert the call still takes 59 us. One token: 12.5 us for 20 MB, a chain of latencies
 // (ns): set-up and tables 1200, claim 800, first stage 800, K loop 3700 (20 MB at 5.6 TB/s, the
 // second product's weights on their way beside the first's), epilogue 400, count 700, seen
 // by the second product 300, its rows and scales 900, its 3 stages 1450, o and end 1000. Tiles

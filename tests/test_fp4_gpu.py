@@ -204,6 +204,7 @@ SHAPES = [  # T, H, E, k, F, skew
     (400, 512, 8, 4, 192, 1), (600, 64, 3, 2, 576, 1), (500, 576, 6, 3, 256, 2), (1000, 320, 16, 4, 448, 1),
     (255, 1344, 4, 2, 128, 1), (3000, 128, 4, 2, 128, 1), (64, 2048, 1, 1, 768, 0),
     (300, 2304, 2, 1, 64, 0), (300, 64, 2, 1, 2304, 0), (290, 2624, 1, 1, 2112, 0), (70, 64, 1, 1, 2048, 0),
+    (3, 16384, 2, 1, 64, 0), (70, 16384, 1, 1, 64, 0), (70, 64, 1, 1, 16384, 0), (5, 64, 256, 32, 64, 1),
     (65, 64, 1, 1, 64, 0), (70, 2048, 1, 1, 768, 0), (140, 320, 2, 1, 448, 0), (128, 64, 2, 2, 192, 2),
 ]
 
@@ -539,3 +540,17 @@ def test_seeded_shapes(seed):
     d, f, off, off_np, a, h, o, ws = experts(T, H, E, k, F, int(rng.integers(0, 3)), bool(seed & 1), seed=seed)
     run(d, f, off, a, h, o, ws)
     check(d, f, off_np, a, h, o, ws)
+
+
+def test_no_tokens():
+    """A layer without tokens: nothing is written, nothing is wrong."""
+    d = moe.LayerDesc.of(0, 128, 4, 2, 64)
+    b, f = moe.LayerBuffers(d), moe.Fp4Buffers(d)
+    f.quantize_weights(b.w1, b.w2)
+    b.y.fill_(3), b.o.fill_(3)
+    for save in (False, True):
+        moe.moe_layer_forward_fp4(d, b, f, save=save)
+    moe.moe_permute_fp4(d, b.x, b.slot, f.xq, f.xs)
+    run(d, f, b.off, None, None, b.o, b.ws)
+    assert moe.moe_device_status(d, b.ws) == moe.MOE_OK
+    assert (b.y == 3).all() and (b.o == 3).all()
