@@ -83,10 +83,12 @@ constexpr int kMaxE = 256;
 constexpr int kEpiAt = kSlots * kSlotBytes, kScAt = kEpiAt + kEpiBytes;
 constexpr size_t kDynSmem = kScAt + kSc * kScBytes + 1024;
 constexpr int kHalf = 8;  // slots of half a mailbox (below)
-// strips (below) that a pair should get of each product, if they can be as many. Prefill and
-// train, us a pass, for 1, 3, 4, 6, 8, 16 and strips of one tile: 272, 272, 268, 268, 276, 283,
-// 347 and 137, 132, 131.5, 131, 129, 132, 140 (fewer reuse the rows more, more deal better).
-constexpr int kStripsAPair = 6;
+// Strips (below) that a pair should get of each product, if they can be as many: few of the
+// first, which the second follows, and more of the second, whose last ones are the end. us of
+// the products, tiles of a strip in the first and the second:
+//   prefill (11 and 8 tiles across)  11, 4 243   6, 4 244   11, 2 249   4, 4 249   2, 2 272   1, 1 328
+//   train (6 and 8)                   6, 2 112   2, 2 111    3, 2 113   6, 4 118   3, 3 114   1, 1 124
+constexpr int kStrips[2] = {2, 6};
 
 struct Maps {
   CUtensorMap a1, s1, b1, a2, s2, b2;  // operands: A, A in small boxes, B of both GEMMs
@@ -939,8 +941,7 @@ moe_status_t launch_ffn_fwd_fp4(const moe_layer_desc_t& d, const uint8_t* xq, co
   const int stages = std::max(fp4_groups(d.H), fp4_groups(d.F));
   p.na = stages <= kMaxA ? std::max(stages, kSlots - kMaxB) : kSlots / 2;
   p.nb = kSlots - p.na;
-  // row tiles, if half of the experts end inside one
-  const long long rt = std::max<long long>(1, N / (2 * BM) + std::min<long long>(N, d.E) / 2);
+  const long long rt = std::max<long long>(1, N / (2 * BM));  // row tiles, at the least
   int pairs = 0;
   cudaError_t e = resident_pairs(&pairs);
   if (e == cudaSuccess && !counters_zeroed) e = launch_zero_counters(dep, d.E, p.tile, st);
@@ -948,9 +949,9 @@ moe_status_t launch_ffn_fwd_fp4(const moe_layer_desc_t& d, const uint8_t* xq, co
     set_error("grouped_gemm_fp4_kernel set-up: %s", cudaGetErrorString(e));
     return MOE_ERR_CUDA;
   }
-  const int parts = (int)std::min<long long>(1 << 20, (kStripsAPair * pairs + rt - 1) / rt);
   const int nt[2] = {ceil_div(d.F, 128), ceil_div(d.H, BN)}, nk[2] = {fp4_groups(d.H), fp4_groups(d.F)};
-  for (int g = 0; g < 2; ++g) p.strip[g] = nk[g] > p.na ? 1 : ceil_div(nt[g], parts);
+  for (int g = 0; g < 2; ++g)
+    p.strip[g] = nk[g] > p.na ? 1 : ceil_div(nt[g], std::min(nt[g], ceil_div(kStrips[g] * pairs, rt)));
   // one pair for every two SMs, and no more than there can be tiles
   const long long rows = N / (2 * BM) + std::min<long long>(N, d.E);
   pairs = (int)std::min<long long>(pairs, rows * (ceil_div(d.F, 128) + ceil_div(d.H, BN)));
