@@ -88,7 +88,10 @@ constexpr int kHalf = 8;  // slots of half a mailbox (below)
 // the products, tiles of a strip in the first and the second:
 //   prefill (11 and 8 tiles across)  11, 4 243   6, 4 244   11, 2 249   4, 4 249   2, 2 272   1, 1 328
 //   train (6 and 8)                   6, 2 112   2, 2 111    3, 2 113   6, 4 118   3, 3 114   1, 1 124
-constexpr int kStrips[2] = {2, 6};
+// and these numbers, 2 and 4 against 2 and 6, 1 and 6, 4 and 6: 2048 tokens of the 64 experts, skewed,
+// 99 / 107 / 106 / 109; 8000 of 16 experts of H, F 1024, top 4, 65 / 72 / 69 / 74; 20480 of one
+// expert of H 2048, F 1408 97 / 97 / 112 / 93; train, a pass, 126.2 / 125.4 / 124.2 / 124.7.
+constexpr int kStrips[2] = {2, 4};
 
 struct Maps {
   CUtensorMap a1, s1, b1, a2, s2, b2;  // operands: A, A in small boxes, B of both GEMMs
