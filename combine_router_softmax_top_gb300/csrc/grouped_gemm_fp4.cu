@@ -34,8 +34,8 @@
 // TMEM with them adds its time: B's loads 95 clocks, scales 70, the epilogue's
 // TMEM reads and boxes 190 (each found by leaving it out). A's loads were 85 more, hence the
 // strips; tiles of N = 192, which would need no shared columns, take as long as N = 256. 128
-// experts of F 768 at 4096 tokens, balanced, a and h kept: 621 MB of DRAM traffic in 114 us, 5.4
-// TB/s, 0.81 of a copy's rate: 8 us of set-up and last tiles, then 5.9.
+// experts of F 768 at 4096 tokens, balanced, a and h kept: 620 MB of DRAM traffic in 113 us, 5.5
+// TB/s, 0.82 of a copy's rate: 8 us of set-up and last tiles, then 5.9.
 //
 // Ragged groups: expert e owns rows off[e]..off[e+1]-1; a tile's rows past the
 // expert's end are computed on whatever was loaded and not stored (rows do not mix).
