@@ -1,4 +1,4 @@
-// Argument checks of the C entry points in norm_api.cu and fp4_api.cu.
+// Argument checks of the C entry points in norm.cu and fp4_api.cu.
 #pragma once
 
 #include "moe_internal.cuh"
