@@ -497,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tmem_alloc(&ctl.tmem_base, kTmemCols);
     ptx::tmem_relinquish();
   }
+  __syncthreads();  // warp 2 arrives on claim_full below: initialised for every warp (beside the launch before)
   pdl_wait();
   int first = 0;  // the first tile, claimed while the tables are made
   if (warp == 2 && lane == 0) {
