@@ -393,7 +393,11 @@ _specs = {}  # call -> what _py_call knows of it
 
 def _call_spec(what, spec):
     lib()
-    from . import _py_call
+    from . import _py_call, build
+    made_for = getattr(_py_call, "built_for", "another build")
+    if made_for != build.built_for():  # (it reads torch's objects by their layout)
+        raise ImportError(f"{_py_call.__file__} is for {made_for}, not for "
+                          f"{build.built_for()}: run combine_router_softmax_top_gb300.build.build()")
     _specs[what] = s = (_py_call.call, _py_call.spec(what, tuple((dt, opt) for _, dt, opt in spec)))
     return s
 

@@ -145,4 +145,8 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_py_call", nullptr, -1, kMethods}
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__py_call(void) { return PyModule_Create(&kModule); }
+PyMODINIT_FUNC PyInit__py_call(void) {
+  PyObject* m = PyModule_Create(&kModule);
+  if (m && PyModule_AddStringConstant(m, "built_for", MOE_BUILT_FOR) < 0) Py_CLEAR(m);
+  return m;
+}
