@@ -19,6 +19,7 @@
 // blocks of 128 threads, to 8 in two: 20 to 25 us against 17.2; too few warps for a row's chain of
 // latencies.)
 #include <algorithm>
+#include <float.h>
 #include <math.h>
 
 #include "api_checks.cuh"
@@ -63,6 +64,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
+__device__ __forceinline__ uint4 add8(const uint4& x, const uint4& y) {
+  auto add = [](uint32_t a, uint32_t b) { return pack2(bf16_lo(a) + bf16_lo(b), bf16_hi(a) + bf16_hi(b)); };
+  return make_uint4(add(x.x, y.x), add(x.y, y.y), add(x.z, y.z), add(x.w, y.w));
+}
+
 struct NormParams {
   const bf16 *x, *res, *w;
   float eps;
@@ -71,11 +77,111 @@ struct NormParams {
   uint32_t* ys;
   float* rstd;
   int T, H, tpr;
+  float low, high;  // a row whose sum of squares is outside of these is looked at again (redo_row)
 };
 
-// BLOCKS: resident on an SM at least, 0 for no limit on registers
-template <int V, int THREADS, int BLOCKS>
-__global__ void __launch_bounds__(THREADS, BLOCKS) rms_norm_kernel(const NormParams p) {
+// ---- rows whose squares leave fp32's range: from 2^64 on, or below 2^-50 beside an eps that small
+// All threads of such a row (and of its warp) go through the following, once the kernel has done
+// the rest. A barrier of the row's threads: the block, one of its two halves, a warp.
+__device__ __forceinline__ void row_sync(int tpr) {
+  if (tpr <= 32) __syncwarp();
+  else if (tpr >= 128) __syncthreads();
+  else if (threadIdx.x < 64) asm volatile("bar.sync 1, 64;" ::: "memory");
+  else asm volatile("bar.sync 2, 64;" ::: "memory");
+}
+template <class T, class Op>
+__device__ __forceinline__ T row_reduce(T v, int tpr, float* s_part, Op op) {
+  const int width = tpr < 32 ? tpr : 32;
+  for (int o = 16; o; o >>= 1)
+    if (o < width) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if (tpr <= 32) return v;
+  T* part = reinterpret_cast<T*>(s_part);
+  row_sync(tpr);  // the last result has been read
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  row_sync(tpr);
+  const int first = threadIdx.x / tpr * (tpr / 32);
+  v = part[first];
+  for (int w = 1; w < tpr / 32; ++w) v = op(v, part[first + w]);
+  return v;
+}
+// The row is summed again under a power of two, 2^-k with 2^k its largest magnitude or eps' root, and
+// its outputs are written again, as the kernel writes them. It reads its input again, in a
+// function of its own: what it needs of a thread's registers would otherwise be taken from
+// ordinary rows (64 a thread for 48, norm_prompts 88 -> 94 us; with the kernel's own loop
+// shared between the two 89.4). In the same warp, rows that are in range and those with an
+// infinity keep their rstd, and their outputs' bits.
+__device__ __noinline__ void redo_row(const NormParams& p, int t, int sub, float ms, float* s_part,
+                                      uint32_t* words) {
+  // (the sum where it was kept: it may have taken x's or res' place)
+  const bf16 *x = p.r ? p.r : p.x, *res = p.r ? nullptr : p.res;
+  const size_t at = (size_t)t * p.H;
+  const int cpr = p.H / 8;
+  auto row = [&](int c) {
+    if (t >= p.T || c >= cpr) return make_uint4(0, 0, 0, 0);
+    const uint4 v = reinterpret_cast<const uint4*>(x + at)[c];
+    return res ? add8(v, reinterpret_cast<const uint4*>(res + at)[c]) : v;
+  };
+  auto larger = [](uint32_t a, uint32_t b) { return max(a, b); };
+  row_sync(p.tpr);  // s_part and words have been read
+  uint32_t m = 0;
+#pragma unroll 1
+  for (int c = sub; c < cpr; c += p.tpr) {
+    const uint4 v = row(c);
+    m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(m, v.x), v.y), v.z), v.w);
+  }
+  m = row_reduce(absmax_bits(m), p.tpr, s_part, larger);
+  const uint32_t e = max(m, __float_as_uint(sqrtf(p.eps))) >> 23;
+  const float down = __uint_as_float((254u - min(max(e, 1u), 253u)) << 23);
+  float ss = 0.f;
+#pragma unroll 1
+  for (int c = sub; c < cpr; c += p.tpr) {
+    const uint4 v = row(c);
+    const uint32_t a[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float lo = bf16_lo(a[j]) * down, hi = bf16_hi(a[j]) * down;
+      ss = fmaf(hi, hi, fmaf(lo, lo, ss));
+    }
+  }
+  ss = row_reduce(ss, p.tpr, s_part, [](float a, float b) { return a + b; });
+  float rs = 1.f / sqrtf(ms);
+  if ((ms < 0x1p-100f || ms > FLT_MAX) && m < 0x7F800000u)
+    rs = 1.f / sqrtf(ss / (float)p.H + p.eps * down * down) * down;
+  if (p.rstd && sub == 0 && t < p.T) p.rstd[t] = rs;
+#pragma unroll 1
+  for (int c = sub; c - sub < cpr; c += p.tpr) {
+    const bool ok = t < p.T && c < cpr;
+    uint4 v = row(c);
+    const uint4 w = ok ? __ldg(reinterpret_cast<const uint4*>(p.w) + c) : make_uint4(0, 0, 0, 0);
+    uint32_t* a = reinterpret_cast<uint32_t*>(&v);
+    const uint32_t* wp = reinterpret_cast<const uint32_t*>(&w);
+    uint32_t mx = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      a[j] = pack2(bf16_lo(a[j]) * rs * bf16_lo(wp[j]), bf16_hi(a[j]) * rs * bf16_hi(wp[j]));
+      mx = absmax_bf16x2(mx, a[j]);
+    }
+    if (ok && p.y) reinterpret_cast<uint4*>(p.y + at)[c] = v;
+    if (!p.yq) continue;
+    mx = c < cpr ? absmax_bits(mx) : 0;
+    for (int o = 1; o < 16; o <<= 1)
+      if (o < p.tpr) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const uint32_t b = fp8_scale_byte(mx), inv = fp8_inv_scale2(b);
+    if (ok)
+      reinterpret_cast<uint2*>(p.yq + at)[c] =
+          make_uint2(fp8x4_of_bf16(a[0], a[1], inv), fp8x4_of_bf16(a[2], a[3], inv));
+    if ((c & 15) == 0 && c < cpr) reinterpret_cast<uint8_t*>(words)[c >> 4] = (uint8_t)b;
+  }
+  if (p.yq) {
+    row_sync(p.tpr);
+    for (int i = sub; i < (p.H + 511) / 512; i += p.tpr)
+      if (t < p.T) p.ys[(size_t)i * p.T + t] = words[i];
+  }
+}
+
+// THREADS: of a block at most. REGS a thread: 1024 of 48, or two blocks of 512 of 64, on an SM
+template <int V, int THREADS, int REGS>
+__global__ void __maxnreg__(REGS) rms_norm_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ uint32_t s_words[];  // scale words of the block's rows
   __shared__ float s_part[THREADS / 32];
   const int rows = blockDim.x / p.tpr, lr = threadIdx.x / p.tpr, sub = threadIdx.x % p.tpr;
@@ -120,7 +226,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rms_norm_kernel(const NormPar
     }
   }
   ss = row_sum<false>(ss, p.tpr, s_part);
-  const float rs = 1.f / sqrtf(ss / (float)p.H + p.eps);
+  const float ms = ss / (float)p.H + p.eps, rs = 1.f / sqrtf(ms);
   if (p.rstd && sub == 0 && t < p.T) p.rstd[t] = rs;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -152,6 +258,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rms_norm_kernel(const NormPar
     for (int i = sub; i < nw; i += p.tpr)
       if (t < p.T) p.ys[(size_t)i * p.T + t] = s_words[lr * nw + i];
   }
+  bool again = ss < p.low || ss > p.high;  // (not for a NaN)
+  if (p.tpr <= 32) again = __any_sync(0xffffffffu, again);
+  if (again) redo_row(p, t, sub, ms, s_part, s_words + lr * nw);
 }
 
 struct NormBwdParams {
@@ -310,15 +419,17 @@ moe_status_t launch_rms_norm(const moe_layer_desc_t& d, const bf16* x, const bf1
   //   H 16384               22   17   21   120   91   96
   // and blocks of 128 threads, or one row: of 32, H 320 4.4 and 20.5, of 256 3.5 and 21.5.
   const int vecs = d.H > 2048 && d.T > device_sm_count() ? 4 : 2;
+  // Of the sums, whatever H (2^14 at most), those where mean + eps may be outside of 2^-100 to fp32's
+  // largest: at the former the squares that fall below fp32's normal range lose 2^-49 of it.
   NormParams p = {x, res, w, eps, r, y, yq, reinterpret_cast<uint32_t*>(ys), rstd, d.T, d.H,
-                  row_threads(d.H, vecs)};
+                  row_threads(d.H, vecs), eps < 0x1p-100f ? 0x1p-86f : 0.f, eps < 0x1p126f ? FLT_MAX : -1.f};
   const int threads = std::max(p.tpr, 128), rows = threads / p.tpr, grid = ceil_div(d.T, rows);
   const size_t smem = yq ? (size_t)rows * ceil_div(d.H, 512) * 4 : 0;
   cudaError_t e;
   {
     LaunchScope _ls(K_NORM, st);
-    e = vecs == 2 ? launch_k(rms_norm_kernel<2, 1024, 0>, grid, threads, smem, st, p)
-                  : launch_k(rms_norm_kernel<4, 512, 2>, grid, threads, smem, st, p);
+    e = vecs == 2 ? launch_k(rms_norm_kernel<2, 1024, 48>, grid, threads, smem, st, p)
+                  : launch_k(rms_norm_kernel<4, 512, 64>, grid, threads, smem, st, p);
   }
   return launched(e, "rms_norm_kernel");
 }

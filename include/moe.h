@@ -625,8 +625,10 @@ moe_status_t moe_layer_forward_fp4(const moe_layer_desc_t* d, const moe_mb_bufs_
  * [ceil(nb / 4), T, 4] with nb = ceil(H / 128), both or neither, exactly what
  * moe_permute_fp8 makes of y: the rows of an expert that every token visits
  * (moe_expert_ffn_fwd_fp8 with E = 1, k = 1, off = {0, T}); y or yq must be given; rstd [T]
- * fp32 or NULL. y, yq, ys and rstd overlap nothing. eps >= 0 and finite. A NaN makes
- * its whole row NaN; a row with an infinity is NaN there and 0 elsewhere. */
+ * fp32 or NULL. y, yq, ys and rstd overlap nothing. eps >= 0 and finite. Rows of any finite
+ * magnitude are summed without overflow or underflow. A NaN makes its whole row NaN; a row with an
+ * infinity is NaN there and 0 elsewhere. With eps = 0 a row of zeros is NaN (0 / 0), and rstd is
+ * infinite, and y with it, where every |r| is so far below 2^-126 that rstd passes fp32. */
 moe_status_t moe_rms_norm(const moe_layer_desc_t* d, const moe_bf16* x, const moe_bf16* res,
                           const moe_bf16* w, float eps, moe_bf16* r, moe_bf16* y, moe_e4m3* yq,
                           moe_e8m0* ys, float* rstd, void* stream);
