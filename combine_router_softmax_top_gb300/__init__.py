@@ -407,6 +407,8 @@ def _fp8_call(what, desc, spec, tensors, sizes, stream, tail=0, value=0.0):
     device, with at least so many elements, or None where spec allows it. tail, value: its
     workspace's size and its number that is no tensor, for calls that have them. Small calls
     are bound by their way here, so the checks are csrc/py_call.cpp's."""
+    if not isinstance(desc, LayerDesc):  # (addressof takes any ctypes object)
+        raise ctypes.ArgumentError(f"{what}: desc is {type(desc).__name__}, not LayerDesc")
     first = tensors[0]
     dev = -1 if first is None else first.get_device()
     if dev < 0 or dev != _get_device():
