@@ -531,7 +531,8 @@ moe_status_t moe_layer_forward_fp8(const moe_layer_desc_t* d, const moe_mb_bufs_
  * backward, activation gradient, dispatch and router backward, and, when
  * run_wgrad != 0, the bf16 weight gradients on the side stream as in
  * moe_layer_backward (flags apply as there). With run_wgrad = 0 b->d_o and b->da
- * may be NULL. Gradients pass through the roundings to 8 bits unchanged. */
+ * may be NULL. The roundings to 8 bits count as the identity; the weight gradients
+ * multiply by x_perm and h in bf16, as kept, not by their 8-bit values. */
 moe_status_t moe_layer_backward_fp8(const moe_layer_desc_t* d, const moe_mb_bufs_t* b,
                                     const moe_fp8_bufs_t* q, int32_t run_wgrad, void* stream);
 
@@ -561,7 +562,13 @@ moe_status_t moe_layer_backward_fp8(const moe_layer_desc_t* d, const moe_mb_bufs
  * There is no 4-bit gradient: a block's scale belongs to K of the forward, and the
  * gradient's K runs across it. A layer is trained through its 4-bit forward by
  * moe_layer_forward_fp4 with save != 0 and moe_layer_backward with b->w1, b->w2 = the values
- * of the 4-bit weights (w1v, w2v below): gradients pass through the roundings unchanged. */
+ * of the 4-bit weights (w1v, w2v below). da, dx_perm and dx are then the gradients of that
+ * forward with each rounding's derivative taken as 1, at its pre-activations as kept: they multiply
+ * by the weights that the forward multiplied by. dw1 and dw2 are not: they multiply by x_perm and h
+ * in bf16, as kept, where the forward multiplied by their 4-bit values, which differ by up to a
+ * fifth of a value that is no smaller than its block's scale, and by all of one that rounds to
+ * 0. This is a choice: the kept rows are what the codes estimate, and the products are the
+ * bf16 layer's. */
 
 /* Bytes of the scale buffer of `rows` rows of `blocks` blocks (0 if negative). */
 size_t moe_fp4_scale_bytes(int64_t rows, int32_t blocks);
