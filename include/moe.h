@@ -632,10 +632,14 @@ moe_status_t moe_layer_forward_fp4(const moe_layer_desc_t* d, const moe_mb_bufs_
  * [ceil(nb / 4), T, 4] with nb = ceil(H / 128), both or neither, exactly what
  * moe_permute_fp8 makes of y: the rows of an expert that every token visits
  * (moe_expert_ffn_fwd_fp8 with E = 1, k = 1, off = {0, T}); y or yq must be given; rstd [T]
- * fp32 or NULL. y, yq, ys and rstd overlap nothing. eps >= 0 and finite. Rows of any finite
- * magnitude are summed without overflow or underflow. A NaN makes its whole row NaN; a row with an
- * infinity is NaN there and 0 elsewhere. With eps = 0 a row of zeros is NaN (0 / 0), and rstd is
- * infinite, and y with it, where every |r| is so far below 2^-126 that rstd passes fp32. */
+ * fp32 or NULL. y, yq, ys and rstd overlap nothing. eps >= 0 and finite. The same call gives the
+ * same bits; a token's do not depend on the others', nor, for H <= 2048, on T. For H > 2048 a row's
+ * sum runs in one order up to as many tokens as the GPU has multiprocessors and in another
+ * above, so that a token's rstd may differ in its last bits between a decode step and a
+ * prompt, and its y by a rounding. Rows of any finite magnitude are summed without overflow or
+ * underflow. A NaN makes its whole row NaN; a row with an infinity is NaN there and 0 elsewhere.
+ * With eps = 0 a row of zeros is NaN (0 / 0), and rstd is infinite, and y with it, where every
+ * |r| is so far below 2^-126 that rstd passes fp32. */
 moe_status_t moe_rms_norm(const moe_layer_desc_t* d, const moe_bf16* x, const moe_bf16* res,
                           const moe_bf16* w, float eps, moe_bf16* r, moe_bf16* y, moe_e4m3* yq,
                           moe_e8m0* ys, float* rstd, void* stream);
