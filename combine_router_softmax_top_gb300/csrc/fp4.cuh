@@ -85,7 +85,14 @@ moe_status_t launch_ffn_fwd_fp4(const moe_layer_desc_t& d, const uint8_t* xq, co
 //   8 experts, H 4096, F 1408       22 / 28   23 / 28   24 / 30   27 / 33   33 / 29
 //   32 experts, H 512, F 512        11 / 19   11 / 19   12 / 19   17 / 19   18 / 20
 //   16 experts, H 320, F 448, skewed 10 / 14  11 / 14   11 / 15   13 / 15   15 / 15
-// The rule sees the average alone, as the offsets are on the device.
+// The rule sees the average alone, as the offsets are on the device. With all rows in a few experts
+// (`hot`, evenly) the few-rows kernel walks each 32 rows at a time; against the GEMMs on the same
+// rows (given as a layer of few enough experts), us:
+//   rows an expert on average            4         16        32        64
+//   128 experts, H 2048, F 768, 4 hot   18 / 17   27 / 19   42 / 25   75 / 34
+//                               16 hot            27 / 27   44 / 26   80 / 35
+//   64 experts, H 2048, F 1408, 4 hot             25 / 20   38 / 25   66 / 32
+//   16 experts, H 1024, F 1024, 4 hot                       13 / 16   19 / 16
 constexpr long long kFp4FewRows = 64;
 moe_status_t launch_ffn_rows_fp4(const moe_layer_desc_t& d, const uint8_t* xq, const uint8_t* xs,
                                  const int32_t* off, const Fp4Weights& w, bf16* a, bf16* h,

@@ -30,12 +30,12 @@
 // What bounds it. 64 experts of H 2048, F 1408 at 8192 tokens, top 8, skewed, nothing kept: 1134
 // GFLOP in 244 us, 4.6 PFLOP/s, at 1330 W and 2070 MHz (the limit is 1400 W; before the
 // strips 272 us at 2032 to 2062 MHz with the power cap active). A stage's four MMAs alone take
-// some 600 clocks (512 at the tensor pipe's nominal rate), and what shares shared memory or
-// TMEM with them adds its time: B's loads 95 clocks, scales 70, the epilogue's
-// TMEM reads and boxes 190 (each found by leaving it out). A's loads were 85 more, hence the
-// strips; tiles of N = 192, which would need no shared columns, take as long as N = 256. 128
-// experts of F 768 at 4096 tokens, balanced, a and h kept: 620 MB of DRAM traffic in 113 us, 5.5
-// TB/s, 0.82 of a copy's rate: 8 us of set-up and last tiles, then 5.9.
+// some 600 clocks (512 at the nominal rate of this form, 64 K values an instruction), and what
+// shares shared memory or TMEM with them adds its time: B's loads 95 clocks, scales 70, the
+// epilogue's TMEM reads and boxes 190 (each found by leaving it out). A's loads were 85 more,
+// hence the strips; tiles of N = 192, which would need no shared columns, take as long as N =
+// 256. 128 experts of F 768 at 4096 tokens, balanced, a and h kept: 620 MB of DRAM traffic in 113
+// us, 5.5 TB/s, 0.82 of a copy's rate: 8 us of set-up and last tiles, then 5.9.
 //
 // Ragged groups: expert e owns rows off[e]..off[e+1]-1; a tile's rows past the
 // expert's end are computed on whatever was loaded and not stored (rows do not mix).
