@@ -4,6 +4,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include "api_checks.cuh"
 #include "moe_internal.cuh"
 #include "moe_layer_ops.h"
 
@@ -13,8 +14,6 @@ namespace {
 thread_local char g_err[512] = "";
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 }  // namespace
 
 void set_error(const char* fmt, ...) {
@@ -126,23 +125,6 @@ moe_status_t validate(const moe_layer_desc_t* d) {
   }
   return MOE_OK;
 }
-
-#define MOE_CHECK(x)                 \
-  do {                               \
-    moe_status_t _s = (x);           \
-    if (_s != MOE_OK) return _s;     \
-  } while (0)
-
-#define MOE_PTR(p)                                                             \
-  do {                                                                         \
-    if (!(p)) { set_error("%s is NULL", #p); return MOE_ERR_INVALID_ARG; }     \
-    if (!aligned16(p)) { set_error("%s is not 16-byte aligned", #p); return MOE_ERR_INVALID_ARG; } \
-  } while (0)
-
-#define MOE_PTR_OPT(p)                                                         \
-  do {                                                                         \
-    if ((p) && !aligned16(p)) { set_error("%s is not 16-byte aligned", #p); return MOE_ERR_INVALID_ARG; } \
-  } while (0)
 
 static moe_status_t check_ws(const moe_layer_desc_t& d, void* ws, size_t ws_bytes) {
   MOE_PTR(ws);

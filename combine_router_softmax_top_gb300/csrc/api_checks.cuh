@@ -1,4 +1,4 @@
-// Argument checks of the C entry points in norm.cu and fp4_api.cu.
+// Argument checks of the C entry points (api.cu, fp8_api.cu, fp4_api.cu, norm.cu).
 #pragma once
 
 #include "moe_internal.cuh"

@@ -1,41 +1,16 @@
 // C ABI of the 8-bit floating-point experts (include/moe.h): argument checks
 // and the launch sequence of each call. No entry point allocates device memory.
+#include "api_checks.cuh"
 #include "fp8.cuh"
 #include "moe_layer_ops.h"
 
 using namespace moe;
 
-namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-#define MOE_CHECK(x)             \
-  do {                           \
-    moe_status_t _s = (x);       \
-    if (_s != MOE_OK) return _s; \
-  } while (0)
-
-#define MOE_PTR(p)                                                                             \
-  do {                                                                                         \
-    if (!(p)) { set_error("%s is NULL", #p); return MOE_ERR_INVALID_ARG; }                     \
-    if (!aligned16(p)) { set_error("%s is not 16-byte aligned", #p); return MOE_ERR_INVALID_ARG; } \
-  } while (0)
-
-// rows that the expert products move in whole 32-byte sectors
-#define MOE_PTR32(p)                                                                           \
-  do {                                                                                         \
-    MOE_PTR(p);                                                                                \
-    if (reinterpret_cast<uintptr_t>(p) & 31u) { set_error("%s is not 32-byte aligned", #p); return MOE_ERR_INVALID_ARG; } \
-  } while (0)
-
-#define MOE_PTR_OPT(p)                                                                         \
-  do {                                                                                         \
-    if ((p) && !aligned16(p)) { set_error("%s is not 16-byte aligned", #p); return MOE_ERR_INVALID_ARG; } \
-  } while (0)
-
 #define S(st) static_cast<cudaStream_t>(st)
 #define BF(p) reinterpret_cast<const bf16*>(p)
 #define BFW(p) reinterpret_cast<bf16*>(p)
+
+namespace {
 
 moe_status_t check_ws(const moe_layer_desc_t& d, void* ws, size_t ws_bytes) {
   MOE_PTR(ws);
